@@ -1,4 +1,4 @@
-"""Thin ctypes binding of libgq (``include/gq.h``), same names as the C ABI.
+"""Thin ctypes binding of libgq (``include/gq.h``, ``include/gq_kv.h``), same names as the C ABI.
 
 The functions here only marshal arguments: they check the dtype, shape,
 contiguity and device of every torch tensor they pass (inputs and
@@ -30,6 +30,9 @@ EXPORTS = (
     "gq_q4k_quantize", "gq_q4k_gemv", "gq_ingest_group_major",
     "gq_w4a16_gemv_f16", "gq_w4a16_gemv_f16_ws", "gq_w4a16_gemm_f16", "gq_w4a16_gemm_f16_ws",
 )
+# the 4-bit key/value cache and its attention (include/gq_kv.h)
+KV_EXPORTS = ("gq_kv4_cache_bytes", "gq_kv4_write", "gq_kv4_read",
+              "gq_kv4_attention_workspace_size", "gq_kv4_attention")
 # comparators and probes (include/gq_bench.h)
 BENCH_EXPORTS = ("gq_bf16_gemv", "gq_stream_read", "gq_probe_mfma_valu", "gq_probe_lds_read")
 
@@ -37,6 +40,25 @@ BENCH_EXPORTS = ("gq_bf16_gemv", "gq_stream_read", "gq_probe_mfma_valu", "gq_pro
 class GqQParams(ctypes.Structure):
     _fields_ = [("bits", ctypes.c_int32), ("group_size", ctypes.c_int32),
                 ("symmetric", ctypes.c_int32)]
+
+
+class GqKv4Layout(ctypes.Structure):
+    _fields_ = [("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("group_size", ctypes.c_int32),
+                ("symmetric", ctypes.c_int32)]
+
+
+class GqKv4AttentionArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("q_tokens", ctypes.c_int64),
+                ("q_heads", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("cache", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("layout", GqKv4Layout),
+                ("page_table", ctypes.c_void_p), ("batch", ctypes.c_int64),
+                ("table_pages", ctypes.c_int64), ("kv_lens", ctypes.c_void_p),
+                ("q_starts", ctypes.c_void_p), ("max_q_len", ctypes.c_int64),
+                ("max_kv_len", ctypes.c_int64), ("causal", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p)]
 
 
 class GqError(RuntimeError):
@@ -85,6 +107,11 @@ def lib() -> ctypes.CDLL:
         "gq_w4a16_gemv_f16_ws": mm_ws,
         "gq_w4a16_gemm_f16": mm,
         "gq_w4a16_gemm_f16_ws": mm_ws,
+        "gq_kv4_cache_bytes": [i64, GqKv4Layout, ctypes.POINTER(sz)],
+        "gq_kv4_write": [p, i64, i64, p, i64, i64, c, i64, p, p, i64, GqKv4Layout, p],
+        "gq_kv4_read": [p, i64, GqKv4Layout, p, i64, p, p, c, p],
+        "gq_kv4_attention_workspace_size": [ctypes.POINTER(GqKv4AttentionArgs), ctypes.POINTER(sz)],
+        "gq_kv4_attention": [ctypes.POINTER(GqKv4AttentionArgs), p, sz, p],
         "gq_stream_read": [p, i64, p, p],
         "gq_probe_mfma_valu": [i32, i32, i32, p, p, p],
         "gq_probe_lds_read": [i32, i32, i32, p, p, p],
@@ -495,3 +522,207 @@ def gq_ingest_group_major(codes: torch.Tensor, scales: torch.Tensor, qweight=Non
     _ok(lib().gq_ingest_group_major(_ptr(codes), _ptr(scales), ng, g, N, _ptr(qweight),
                                     _ptr(scales_out), _stream(stream)), "gq_ingest_group_major")
     return qweight, scales_out
+
+
+# ---------------------------------------------------------------------------
+# The 4-bit key/value cache (include/gq_kv.h)
+# ---------------------------------------------------------------------------
+
+_KV_DIMS = (64, 96, 128, 256)
+
+
+def _kv4_block_bytes(head_dim: int, group_size: int, symmetric: bool) -> int:
+    """Bytes of 16 tokens of one head: keys and values, codes and parameters."""
+    return 2 * (8 * head_dim + 16 * (head_dim // group_size) * (2 if symmetric else 4))
+
+
+def _kv4_shape(head_dim: int, group_size: int) -> None:
+    if head_dim not in _KV_DIMS:
+        raise ValueError(f"head_dim {head_dim} not in {_KV_DIMS}")
+    if group_size < 32 or group_size % 32 or head_dim % group_size:
+        raise ValueError(f"group_size {group_size} must be a multiple of 32 that divides "
+                         f"head_dim={head_dim}")
+
+
+def gq_kv4_empty(n_pages: int, kv_heads: int, head_dim: int, page_size: int = 64,
+                 group_size: int = 128, symmetric: bool = False, device="cuda") -> torch.Tensor:
+    """A cache of n_pages pages of page_size tokens: uint8 [n_pages, kv_heads,
+    page_size / 16, bytes of 16 tokens], uninitialised.  The shape carries what
+    the other calls need; the bytes are the library's own (gq_kv4_write and
+    gq_kv4_read are the way in and out)."""
+    _kv4_shape(head_dim, group_size)
+    if page_size < 16 or page_size > 1024 or page_size & (page_size - 1):
+        raise ValueError(f"page_size {page_size} must be a power of two in 16..1024")
+    if n_pages < 1 or kv_heads < 1:
+        raise ValueError("n_pages and kv_heads must be positive")
+    return torch.empty((n_pages, kv_heads, page_size // 16,
+                        _kv4_block_bytes(head_dim, group_size, symmetric)),
+                       dtype=torch.uint8, device=device)
+
+
+def _kv4_cache(cache, head_dim: int, group_size: int, symmetric: bool):
+    """Check a cache against head_dim and the quantisation; its layout."""
+    _need(cache, "cache", (torch.uint8,))
+    _kv4_shape(head_dim, group_size)
+    blk = _kv4_block_bytes(head_dim, group_size, symmetric)
+    if cache.dim() != 4 or cache.shape[3] != blk:
+        raise ValueError(f"cache has shape {tuple(cache.shape)}, expected (n_pages, kv_heads, "
+                         f"page_size / 16, {blk}) for head_dim {head_dim}, group_size {group_size}, "
+                         f"symmetric {bool(symmetric)}")
+    return GqKv4Layout(cache.shape[1], head_dim, cache.shape[2] * 16, group_size, int(bool(symmetric)))
+
+
+def _rows16(t, name: str, dtypes, heads=None, dim=None):
+    """A [tokens, heads, dim] tensor whose rows of `dim` are contiguous and
+    16-byte aligned (a slice of a projection's output); its two strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or \
+            (dim is not None and t.shape[2] != dim):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (tokens, "
+                         f"{'heads' if heads is None else heads}, {'dim' if dim is None else dim})")
+    # the stride of a dimension of one element is never walked
+    ts = t.stride(0) if t.shape[0] > 1 else 0
+    hs = t.stride(1) if t.shape[1] > 1 else 0
+    if (t.shape[2] > 1 and t.stride(2) != 1) or ts % 8 or hs % 8:
+        raise ValueError(f"{name}: strides {t.stride()}; the last must be 1, the others multiples of 8")
+    return ts, hs
+
+
+def _slots(slots, tokens: int) -> None:
+    _need(slots, "slots", (torch.int64,), (tokens,))
+
+
+def gq_kv4_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor,
+                 group_size: int = 128, symmetric: bool = False, stream=None) -> None:
+    """Quantise k, v [tokens, kv_heads, head_dim] (bf16 or fp16; views with
+    contiguous rows are taken as they are) into the cache at the given slots
+    (int64; page * page_size + place, out of range: skipped)."""
+    kts, khs = _rows16(k, "k", (torch.bfloat16, torch.float16))
+    T, H, D = k.shape
+    vts, vhs = _rows16(v, "v", (k.dtype,), H, D)
+    if v.shape[0] != T:
+        raise ValueError(f"v has {v.shape[0]} tokens, k has {T}")
+    lay = _kv4_cache(cache, D, group_size, symmetric)
+    if lay.kv_heads != H:
+        raise ValueError(f"cache has {lay.kv_heads} heads, k has {H}")
+    _slots(slots, T)
+    _on_device(None, k=k)
+    _on_device(k.device, v=v, cache=cache, slots=slots)
+    _ok(lib().gq_kv4_write(_ptr(k), kts, khs, _ptr(v), vts, vhs, _DT[k.dtype], T, _ptr(slots),
+                           _ptr(cache), cache.shape[0], lay, _stream(stream)), "gq_kv4_write")
+
+
+def gq_kv4_read(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, group_size: int = 128,
+                symmetric: bool = False, out_dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """(k, v) [tokens, kv_heads, head_dim] in out_dtype: the values that the cache
+    stands for at the given slots (fp32 exact; a slot out of range: zeros)."""
+    lay = _kv4_cache(cache, head_dim, group_size, symmetric)
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be a 1-D tensor")
+    _slots(slots, slots.shape[0])
+    shape = (slots.shape[0], lay.kv_heads, head_dim)
+    if out_dtype not in _DT:
+        raise TypeError(f"out_dtype {out_dtype} not in {tuple(_DT)}")
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _need(t, name, (out_dtype,), shape)
+    _on_device(None, cache=cache)
+    _on_device(cache.device, slots=slots, k=k, v=v)
+    if k is None:
+        k = torch.empty(shape, dtype=out_dtype, device=cache.device)
+    if v is None:
+        v = torch.empty(shape, dtype=out_dtype, device=cache.device)
+    _ok(lib().gq_kv4_read(_ptr(cache), cache.shape[0], lay, _ptr(slots), slots.shape[0], _ptr(k),
+                          _ptr(v), _DT[out_dtype], _stream(stream)), "gq_kv4_read")
+    return k, v
+
+
+def gq_kv4_attention_workspace_size(batch: int, q_heads: int, kv_heads: int, head_dim: int,
+                                    max_q_len: int, max_kv_len: int) -> int:
+    """Bytes of scratch gq_kv4_attention can use (0: none).  Depends on the
+    current device's compute-unit count."""
+    a = GqKv4AttentionArgs()
+    a.layout = GqKv4Layout(kv_heads, head_dim, 16, head_dim, 0)
+    a.q_heads, a.batch, a.q_tokens, a.n_pages = q_heads, batch, max(batch, 1), 1
+    a.max_q_len, a.max_kv_len, a.scale, a.dtype = max_q_len, max_kv_len, 1.0, GQ_BF16
+    b = ctypes.c_size_t()
+    _ok(lib().gq_kv4_attention_workspace_size(ctypes.byref(a), ctypes.byref(b)),
+        "gq_kv4_attention_workspace_size")
+    return int(b.value)
+
+
+def gq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
+                     kv_lens: torch.Tensor, group_size: int = 128, symmetric: bool = False,
+                     q_starts: Optional[torch.Tensor] = None, max_q_len: Optional[int] = None,
+                     max_kv_len: Optional[int] = None, causal: bool = True, window: int = 0,
+                     scale: Optional[float] = None, return_lse: bool = False, out=None, lse=None,
+                     stream=None, workspace=None):
+    """Attention of q [tokens, q_heads, head_dim] (bf16 or fp16) over the cache.
+
+    Sequence b owns the query rows q_starts[b] .. q_starts[b + 1] - 1 (row b
+    where q_starts is None), its keys are the first kv_lens[b] tokens of its row
+    of page_table [batch, pages] (all int32, on the GPU).  Its last query stands
+    at the last key; with `causal` a query sees the keys up to its own position,
+    with `window` > 0 only the last `window` of them.  A query without keys gives
+    zeros and lse = -inf.  max_q_len and max_kv_len bound the lengths for the
+    choice of kernels (default: 1 or the number of tokens, and the whole table);
+    scale defaults to 1 / sqrt(head_dim).  Returns out, or (out, lse) with the
+    natural-log sums [tokens, q_heads] in fp32."""
+    qts, qhs = _rows16(q, "q", (torch.bfloat16, torch.float16))
+    T, HQ, D = q.shape
+    lay = _kv4_cache(cache, D, group_size, symmetric)
+    if HQ % lay.kv_heads:
+        raise ValueError(f"{HQ} query heads are not a multiple of {lay.kv_heads} key/value heads")
+    _need(page_table, "page_table", (torch.int32,))
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [batch, pages], got {tuple(page_table.shape)}")
+    nb = page_table.shape[0]
+    _need(kv_lens, "kv_lens", (torch.int32,), (nb,))
+    if q_starts is not None:
+        _need(q_starts, "q_starts", (torch.int32,), (nb + 1,))
+    elif T != nb:
+        raise ValueError(f"q has {T} tokens for {nb} sequences; more than one each needs q_starts")
+    if out is not None:
+        _need(out, "out", (q.dtype,), (T, HQ, D))
+    if lse is not None:
+        _need(lse, "lse", (torch.float32,), (T, HQ))
+    if workspace is not None:
+        _need(workspace, "workspace", (torch.uint8,))
+    if max_q_len is None:
+        max_q_len = 1 if q_starts is None else T
+    if max_kv_len is None:
+        max_kv_len = page_table.shape[1] * lay.page_size
+    _on_device(None, q=q)
+    _on_device(q.device, cache=cache, page_table=page_table, kv_lens=kv_lens, q_starts=q_starts,
+               out=out, lse=lse, workspace=workspace)
+    if out is None:
+        out = torch.empty((T, HQ, D), dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty((T, HQ), dtype=torch.float32, device=q.device)
+    a = GqKv4AttentionArgs(
+        q.data_ptr(), qts, qhs, T, HQ, _DT[q.dtype], cache.data_ptr(), cache.shape[0], lay,
+        page_table.data_ptr(), nb, page_table.shape[1], kv_lens.data_ptr(),
+        None if q_starts is None else q_starts.data_ptr(), int(max_q_len), int(max_kv_len),
+        int(bool(causal)), int(window), D ** -0.5 if scale is None else float(scale), out.data_ptr(),
+        None if lse is None else lse.data_ptr())
+    ref = ctypes.byref(a)
+    size = ctypes.c_size_t()
+    _ok(lib().gq_kv4_attention_workspace_size(ref, ctypes.byref(size)), "gq_kv4_attention_workspace_size")
+    need = size.value
+    if workspace is not None and workspace.numel() < need:
+        raise ValueError(f"workspace has {workspace.numel()} bytes, the call needs {need}")
+    if need > 0 and workspace is None:
+        if stream is not None and not hasattr(stream, "cuda_stream"):
+            raise ValueError("with a raw stream handle the caller passes the workspace "
+                             f"({need} bytes) that the call needs")
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _ok(lib().gq_kv4_attention(ref, _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                               _stream(stream)), "gq_kv4_attention")
+    return (out, lse) if return_lse else out

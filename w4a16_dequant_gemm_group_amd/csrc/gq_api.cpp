@@ -19,22 +19,6 @@ std::atomic<int> g_num_cus[kMaxDevices];
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
-gq_status check_device(hipStream_t stream) {
-  (void)stream;
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return GQ_ERR_HIP;
-  if (dev < 0 || dev >= kMaxDevices) return GQ_ERR_UNSUPPORTED;
-  int st = g_arch_state[dev].load(std::memory_order_relaxed);
-  if (st == 0) {
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return GQ_ERR_HIP;
-    st = (std::strncmp(prop.gcnArchName, "gfx950", 6) == 0) ? 1 : 2;
-    g_num_cus[dev].store(prop.multiProcessorCount, std::memory_order_relaxed);
-    g_arch_state[dev].store(st, std::memory_order_relaxed);
-  }
-  return st == 1 ? GQ_OK : GQ_ERR_UNSUPPORTED;
-}
-
 gq_status from_hip(hipError_t e) { return e == hipSuccess ? GQ_OK : GQ_ERR_HIP; }
 
 bool valid_dtype(gq_dtype d) { return d == GQ_F32 || d == GQ_F16 || d == GQ_BF16; }
@@ -71,6 +55,22 @@ gq_status check_w4_matmul(const uint16_t* x, int64_t M, int64_t K, const uint8_t
 
 namespace gq {
 
+gq_status check_device(hipStream_t stream) {
+  (void)stream;
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return GQ_ERR_HIP;
+  if (dev < 0 || dev >= kMaxDevices) return GQ_ERR_UNSUPPORTED;
+  int st = g_arch_state[dev].load(std::memory_order_relaxed);
+  if (st == 0) {
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return GQ_ERR_HIP;
+    st = (std::strncmp(prop.gcnArchName, "gfx950", 6) == 0) ? 1 : 2;
+    g_num_cus[dev].store(prop.multiProcessorCount, std::memory_order_relaxed);
+    g_arch_state[dev].store(st, std::memory_order_relaxed);
+  }
+  return st == 1 ? GQ_OK : GQ_ERR_UNSUPPORTED;
+}
+
 uint64_t next_launch_id() {
   static std::atomic<uint64_t> seq{[] {
     std::random_device rd;
@@ -81,6 +81,12 @@ uint64_t next_launch_id() {
   return seq.fetch_add(2, std::memory_order_relaxed) | 1ull;
 }
 
+// The CU count the split decision uses: the device's when one is present.
+void probe_device() {
+  int n = 0;
+  if (hipGetDeviceCount(&n) == hipSuccess && n > 0) (void)check_device(nullptr);
+}
+
 int num_cus() {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return 256;
@@ -89,6 +95,9 @@ int num_cus() {
 }
 
 }  // namespace gq
+
+using gq::check_device;
+using gq::probe_device;
 
 extern "C" {
 
@@ -202,12 +211,6 @@ gq_status check_gemm(int64_t M, int64_t K, int64_t N) {
   if (K > kMaxGemmK || M > kMaxDim / 2) return GQ_ERR_UNSUPPORTED;
   if (((M + 127) / 128) * ((N + 255) / 256) > INT32_MAX / 2) return GQ_ERR_UNSUPPORTED;
   return GQ_OK;
-}
-
-// The CU count the split decision uses: the device's when one is present.
-void probe_device() {
-  int n = 0;
-  if (hipGetDeviceCount(&n) == hipSuccess && n > 0) (void)check_device(nullptr);
 }
 
 gq_status gemm_call(const uint16_t* x, int64_t M, int64_t K, const uint8_t* qweight,

@@ -89,7 +89,11 @@ __device__ __forceinline__ double load_elem_f64(const void* p, int64_t i, gq_dty
   return (double)((const float*)p)[i];
 }
 
-// Compute units of the current device (set by the C ABI's device check).
+// GQ_OK on a gfx950 device (looked up once per device).
+gq_status check_device(hipStream_t stream);
+// The same for the size queries, where no device may be present.
+void probe_device();
+// Compute units of the current device (set by the device check; 256 before).
 int num_cus();
 
 // A 64-bit id unique to each launch that needs one (odd, never 0), random

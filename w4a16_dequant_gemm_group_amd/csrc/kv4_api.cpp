@@ -1,0 +1,220 @@
+// C ABI of the 4-bit key/value cache (gq_kv.h): argument validation, the launch
+// plan of the attention, and dispatch.  Validation runs on the host before any
+// HIP call, as in gq_api.cpp.
+#include <algorithm>
+#include <cmath>
+
+#include "kv4.h"
+
+namespace gq {
+namespace {
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;
+
+gq_status check_layout(const gq_kv4_layout& y) {
+  if (y.kv_heads < 1 || y.kv_heads > 65535 || y.head_dim < 1) return GQ_ERR_INVALID_ARG;
+  if (y.page_size < 16 || y.page_size > 1024 || (y.page_size & (y.page_size - 1)) != 0)
+    return GQ_ERR_INVALID_ARG;
+  if (y.symmetric != 0 && y.symmetric != 1) return GQ_ERR_INVALID_ARG;
+  if (y.group_size < 32 || y.group_size % 32 != 0 || y.head_dim % y.group_size != 0)
+    return GQ_ERR_INVALID_ARG;
+  if (y.head_dim != 64 && y.head_dim != 96 && y.head_dim != 128 && y.head_dim != 256)
+    return GQ_ERR_UNSUPPORTED;
+  return GQ_OK;
+}
+
+gq_status check_cache(int64_t n_pages, const gq_kv4_layout& y) {
+  if (gq_status s = check_layout(y)) return s;
+  if (n_pages < 1 || n_pages > INT32_MAX) return GQ_ERR_INVALID_ARG;
+  return GQ_OK;
+}
+
+Kv4Geo geometry(const uint8_t* cache, int64_t n_pages, const gq_kv4_layout& y) {
+  Kv4Geo c;
+  c.cache = const_cast<uint8_t*>(cache);
+  c.n_pages = n_pages;
+  c.hkv = y.kv_heads;
+  c.d = y.head_dim;
+  c.g = y.group_size;
+  c.ng = y.head_dim / y.group_size;
+  c.sym = y.symmetric;
+  c.page_shift = __builtin_ctz((unsigned)y.page_size);
+  c.meta = 16u * c.ng * (c.sym ? 2u : 4u);
+  c.sb = 2u * (8u * c.d + c.meta);
+  return c;
+}
+
+gq_status from_hip(hipError_t e) { return e == hipSuccess ? GQ_OK : GQ_ERR_HIP; }
+
+// Strides in elements: rows of 16-byte pieces, far from overflowing 64 bits.
+gq_status check_strides(int64_t ts, int64_t hs) {
+  constexpr int64_t lim = (int64_t)1 << 40;
+  if (ts < -lim || ts > lim || hs < -lim || hs > lim) return GQ_ERR_INVALID_ARG;
+  if (ts % 8 != 0 || hs % 8 != 0) return GQ_ERR_MISALIGNED;
+  return GQ_OK;
+}
+
+// What the sizes and options of an attention call have to satisfy.
+gq_status check_attention(const gq_kv4_attention_args& a) {
+  if (gq_status s = check_cache(a.n_pages, a.layout)) return s;
+  if (a.dtype != GQ_BF16 && a.dtype != GQ_F16)
+    return a.dtype == GQ_F32 ? GQ_ERR_UNSUPPORTED : GQ_ERR_INVALID_ARG;
+  if (a.q_heads < 1 || a.q_heads % a.layout.kv_heads != 0 || a.q_heads / a.layout.kv_heads > 64)
+    return GQ_ERR_INVALID_ARG;
+  if (a.q_tokens < 0 || a.q_tokens * a.q_heads > kMaxTokens || a.q_tokens > kMaxTokens)
+    return GQ_ERR_INVALID_ARG;
+  if (a.batch < 0 || a.batch > (1 << 24) || a.table_pages < 0) return GQ_ERR_INVALID_ARG;
+  if (a.table_pages > kMaxTokens / a.layout.page_size) return GQ_ERR_INVALID_ARG;
+  if (a.max_q_len < 0 || a.max_kv_len < 0 || a.max_q_len > kMaxTokens || a.max_kv_len > kMaxTokens)
+    return GQ_ERR_INVALID_ARG;
+  if ((a.causal != 0 && a.causal != 1) || a.window < 0 || (a.window > 0 && !a.causal))
+    return GQ_ERR_INVALID_ARG;
+  if (!(a.scale > 0.0f) || !std::isfinite(a.scale)) return GQ_ERR_INVALID_ARG;
+  return GQ_OK;
+}
+
+}  // namespace
+
+Kv4Plan kv4_plan(const gq_kv4_attention_args& a) {
+  constexpr int kTileKeys = 128;   // keys of one tile of the split
+  const int r = a.q_heads / a.layout.kv_heads;
+  const int64_t rows = std::max<int64_t>(1, a.max_q_len) * r;
+  Kv4Plan p;
+  // Query tiles of 16 rows per workgroup: as many as the longest query needs,
+  // up to the 4 (2 at head_dim 256) whose results fit the registers.
+  const int top = a.layout.head_dim > 128 ? 2 : 4;
+  p.nq = rows <= 16 ? 1 : (rows <= 32 || top == 2 ? 2 : 4);
+  p.grid_q = (int)((rows + 16 * p.nq - 1) / (16 * p.nq));
+  const int64_t segs = a.batch * a.layout.kv_heads * p.grid_q;
+  const int64_t tiles = segs * std::max<int64_t>(1, (a.max_kv_len + kTileKeys - 1) / kTileKeys);
+  p.split = a.max_kv_len > 1024 || segs > INT32_MAX;
+  p.workers = 0;
+  p.ws_bytes = 0;
+  if (p.split) {
+    const int64_t want = (int64_t)num_cus() * (p.nq == 1 ? 4 : 2);
+    p.workers = (int)std::max<int64_t>(8, std::min(tiles, want) & ~(int64_t)7);
+    p.ws_bytes = (size_t)p.workers * 32 +
+                 (size_t)p.workers * 2 * 16 * p.nq * (a.layout.head_dim + 2) * sizeof(float);
+  }
+  return p;
+}
+
+hipError_t launch_kv4_attention(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
+  switch (a.c.d) {
+    case 64: return launch_kv4_rows_64(a, p, s);
+    case 96: return launch_kv4_rows_96(a, p, s);
+    case 128: return launch_kv4_rows_128(a, p, s);
+    default: return launch_kv4_rows_256(a, p, s);
+  }
+}
+
+}  // namespace gq
+
+using namespace gq;
+
+extern "C" {
+
+gq_status gq_kv4_cache_bytes(int64_t n_pages, gq_kv4_layout layout, size_t* bytes) {
+  if (!bytes) return GQ_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (gq_status s = check_cache(n_pages, layout)) return s;
+  const Kv4Geo c = geometry(nullptr, n_pages, layout);
+  *bytes = (size_t)n_pages * layout.kv_heads * (layout.page_size / 16) * c.sb;
+  return GQ_OK;
+}
+
+gq_status gq_kv4_write(const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                       const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                       gq_dtype dtype, int64_t tokens, const int64_t* slots, uint8_t* cache,
+                       int64_t n_pages, gq_kv4_layout layout, void* stream) {
+  if (gq_status s = check_cache(n_pages, layout)) return s;
+  if (dtype != GQ_BF16 && dtype != GQ_F16)
+    return dtype == GQ_F32 ? GQ_ERR_UNSUPPORTED : GQ_ERR_INVALID_ARG;
+  if (tokens < 0 || tokens > kMaxTokens) return GQ_ERR_INVALID_ARG;
+  if (tokens == 0) return GQ_OK;
+  if (!k || !v || !slots || !cache) return GQ_ERR_INVALID_ARG;
+  if (gq_status s = check_strides(k_token_stride, k_head_stride)) return s;
+  if (gq_status s = check_strides(v_token_stride, v_head_stride)) return s;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || ((uintptr_t)slots & 7u))
+    return GQ_ERR_MISALIGNED;
+  hipStream_t s = (hipStream_t)stream;
+  if (gq_status st = check_device(s)) return st;
+  return from_hip(launch_kv4_write(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride,
+                                   dtype, tokens, slots, geometry(cache, n_pages, layout), s));
+}
+
+gq_status gq_kv4_read(const uint8_t* cache, int64_t n_pages, gq_kv4_layout layout,
+                      const int64_t* slots, int64_t tokens, void* k, void* v, gq_dtype out_dtype,
+                      void* stream) {
+  if (gq_status s = check_cache(n_pages, layout)) return s;
+  if (out_dtype != GQ_F32 && out_dtype != GQ_F16 && out_dtype != GQ_BF16) return GQ_ERR_INVALID_ARG;
+  if (tokens < 0 || tokens > kMaxTokens) return GQ_ERR_INVALID_ARG;
+  if (tokens == 0) return GQ_OK;
+  if (!k || !v || !slots || !cache) return GQ_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || ((uintptr_t)slots & 7u))
+    return GQ_ERR_MISALIGNED;
+  hipStream_t s = (hipStream_t)stream;
+  if (gq_status st = check_device(s)) return st;
+  return from_hip(launch_kv4_read(geometry(cache, n_pages, layout), slots, tokens, k, v, out_dtype, s));
+}
+
+gq_status gq_kv4_attention_workspace_size(const gq_kv4_attention_args* args, size_t* bytes) {
+  if (!args || !bytes) return GQ_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (gq_status s = check_attention(*args)) return s;
+  if (args->batch == 0 || args->q_tokens == 0) return GQ_OK;
+  probe_device();
+  *bytes = kv4_plan(*args).ws_bytes;
+  return GQ_OK;
+}
+
+gq_status gq_kv4_attention(const gq_kv4_attention_args* args, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (!args) return GQ_ERR_INVALID_ARG;
+  const gq_kv4_attention_args& a = *args;
+  if (gq_status s = check_attention(a)) return s;
+  if (a.batch == 0 || a.q_tokens == 0) return GQ_OK;
+  if (!a.q || !a.cache || !a.kv_lens || !a.out) return GQ_ERR_INVALID_ARG;
+  if (!a.page_table && a.table_pages > 0) return GQ_ERR_INVALID_ARG;
+  if (!a.q_starts && a.q_tokens < a.batch) return GQ_ERR_INVALID_ARG;
+  if (gq_status s = check_strides(a.q_token_stride, a.q_head_stride)) return s;
+  if (!aligned16(a.q) || !aligned16(a.cache) || !aligned16(a.out)) return GQ_ERR_MISALIGNED;
+  if (((uintptr_t)a.page_table & 3u) || ((uintptr_t)a.kv_lens & 3u) || ((uintptr_t)a.q_starts & 3u) ||
+      ((uintptr_t)a.lse & 3u))
+    return GQ_ERR_MISALIGNED;
+  probe_device();   // the split depends on the device's compute-unit count
+  const Kv4Plan p = kv4_plan(a);
+  if (p.ws_bytes > 0 && (!workspace || workspace_bytes < p.ws_bytes)) return GQ_ERR_INVALID_ARG;
+  if (p.ws_bytes > 0 && !aligned16(workspace)) return GQ_ERR_MISALIGNED;
+  hipStream_t s = (hipStream_t)stream;
+  if (gq_status st = check_device(s)) return st;
+  Kv4Attn k;
+  k.c = geometry(a.cache, a.n_pages, a.layout);
+  k.q = (const uint16_t*)a.q;
+  k.q_ts = a.q_token_stride;
+  k.q_hs = a.q_head_stride;
+  k.q_tokens = a.q_tokens;
+  k.hq = a.q_heads;
+  k.r = a.q_heads / a.layout.kv_heads;
+  k.bf16 = a.dtype == GQ_BF16;
+  k.table = a.page_table;
+  k.batch = a.batch;
+  k.table_pages = a.table_pages;
+  k.kv_lens = a.kv_lens;
+  k.q_starts = a.q_starts;
+  k.causal = a.causal;
+  // a window longer than any sequence hides nothing
+  k.window = a.window > kMaxTokens ? 0 : a.window;
+  k.scale_log2 = a.scale * 1.4426950408889634f;
+  k.out = (uint16_t*)a.out;
+  k.lse = a.lse;
+  k.workers = p.workers;
+  k.grid_q = p.grid_q;
+  k.meta = (int32_t*)workspace;
+  k.part = p.split ? (float*)((uint8_t*)workspace + (size_t)p.workers * 32) : nullptr;
+  return from_hip(launch_kv4_attention(k, p, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,821 @@
+// Attention over the 4-bit cache for few query rows per key/value head (single
+// tokens, a few tokens to verify), and the pieces that every attention kernel
+// of the cache shares: row tiles, the split of the key axis, the join.
+//
+// A query row is one (token, query head) pair; the r query heads that share a
+// key/value head are rows of the same tile, so keys and values are read once
+// for all of them.  Row tile qt of a sequence holds its rows qt * TQ ..; row i
+// is token i / r, head kvh * r + i % r.
+#pragma once
+
+#include "kv4.h"
+#include "stream_util.h"
+
+namespace gq {
+namespace kv4 {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kWaves = 4;            // waves per workgroup
+constexpr int kUnit = 32;            // tokens a wave takes at once (two sub-blocks)
+constexpr int kTile = kWaves * kUnit;  // tokens of a key tile, the grain of the split
+constexpr int kMetaInts = 8;
+constexpr float kNegInf = -__builtin_inff();
+// The running reference of the softmax is raised only when a score exceeds it
+// by this many powers of two: P stays below 2^9, well inside fp16.
+constexpr float kSlack = 8.0f;
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+struct Seq {
+  int q0, n, kv;   // first query row of q, queries, keys
+};
+
+__device__ __forceinline__ Seq get_seq(const Kv4Attn& a, int64_t b) {
+  Seq s;
+  if (a.q_starts) {
+    const int64_t lim = a.q_tokens;
+    int64_t x = a.q_starts[b], y = a.q_starts[b + 1];
+    x = x < 0 ? 0 : (x > lim ? lim : x);
+    y = y < x ? x : (y > lim ? lim : y);
+    s.q0 = (int)x;
+    s.n = (int)(y - x);
+  } else {
+    s.q0 = (int)b;
+    s.n = 1;
+  }
+  const int64_t cap = a.table_pages << a.c.page_shift;
+  int64_t kv = a.kv_lens[b];
+  kv = kv < 0 ? 0 : (kv > cap ? cap : kv);
+  s.kv = (int)kv;
+  return s;
+}
+
+// The keys that a row tile can see: positions lo .. hi - 1, tiles of T keys
+// t0 .. t0 + cnt - 1 (one empty tile where nothing is seen, so that every row
+// tile is visited and written).
+struct Span {
+  int p0, p1;   // positions of the first and last query
+  int lo, hi, t0, cnt;
+};
+
+template <int TQ, int T>
+__device__ __forceinline__ Span get_span(const Kv4Attn& a, const Seq& s, int qt) {
+  const int rows = s.n * a.r;
+  const int last = (qt + 1) * TQ < rows ? (qt + 1) * TQ - 1 : rows - 1;
+  Span p;
+  p.p0 = s.kv - s.n + qt * TQ / a.r;
+  p.p1 = s.kv - s.n + last / a.r;
+  p.hi = a.causal ? (p.p1 + 1 < s.kv ? p.p1 + 1 : s.kv) : s.kv;
+  p.hi = p.hi < 0 ? 0 : p.hi;
+  p.lo = a.window > 0 && p.p0 - a.window + 1 > 0 ? p.p0 - a.window + 1 : 0;
+  p.t0 = p.lo / T;
+  const int t1 = (p.hi + T - 1) / T;
+  p.cnt = t1 > p.t0 ? t1 - p.t0 : 1;
+  return p;
+}
+
+// Where the split stands: sequence, head, row tile, and the key tiles j0 .. j1
+// of its cnt that are this workgroup's.
+struct Cursor {
+  int64_t b;
+  int h, qt;
+  int64_t off;   // tiles of the row tile that lie before
+};
+
+__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t u = __shfl_up(v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+
+__device__ __forceinline__ int64_t uniform64(int64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)((uint64_t)v >> 32), lane);
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// Key tiles of one head over all row tiles of a sequence; lanes share the row
+// tiles.  With `find` >= 0: the row tile that holds tile number `find`.
+template <int TQ, int T>
+__device__ int64_t seq_tiles(const Kv4Attn& a, const Seq& s, int lane, int64_t find, Cursor* cur) {
+  const int nqt = (s.n * a.r + TQ - 1) / TQ;
+  int64_t base = 0;
+  for (int q = 0; q < nqt; q += 64) {
+    const int64_t v = q + lane < nqt ? get_span<TQ, T>(a, s, q + lane).cnt : 0;
+    const int64_t sc = wave_scan(v, lane);
+    if (find >= 0) {
+      const uint64_t hit = __ballot(base + sc > find);
+      if (hit) {
+        const int l = __builtin_ctzll(hit);
+        cur->qt = q + l;
+        cur->off = find - base - uniform64(sc - v, l);
+        return 0;
+      }
+    }
+    base += uniform64(sc, 63);
+  }
+  return base;
+}
+
+// All key tiles of the call, in the order sequence, head, row tile, key tile;
+// with `find` >= 0 the place of tile number `find`.  Few row tiles: lanes share
+// the sequences.  Many: lanes share the row tiles of one sequence at a time.
+template <int TQ, int T>
+__device__ int64_t all_tiles(const Kv4Attn& a, int lane, bool few, int64_t find, Cursor* cur) {
+  int64_t base = 0;
+  if (few) {
+    for (int64_t b0 = 0; b0 < a.batch; b0 += 64) {
+      int64_t v = 0;
+      if (b0 + lane < a.batch) {
+        const Seq s = get_seq(a, b0 + lane);
+        const int nqt = (s.n * a.r + TQ - 1) / TQ;
+        for (int q = 0; q < nqt; ++q) v += get_span<TQ, T>(a, s, q).cnt;
+        v *= a.c.hkv;
+      }
+      const int64_t sc = wave_scan(v, lane);
+      if (find >= 0) {
+        const uint64_t hit = __ballot(base + sc > find);
+        if (hit) {
+          const int l = __builtin_ctzll(hit);
+          cur->b = b0 + l;
+          const int64_t per = uniform64(v, l) / a.c.hkv;
+          const int64_t rem = find - base - uniform64(sc - v, l);
+          cur->h = (int)(rem / per);
+          seq_tiles<TQ, T>(a, get_seq(a, cur->b), lane, rem - cur->h * per, cur);
+          return 0;
+        }
+      }
+      base += uniform64(sc, 63);
+    }
+    return base;
+  }
+  for (int64_t b = 0; b < a.batch; ++b) {
+    const Seq s = get_seq(a, b);
+    const int64_t per = seq_tiles<TQ, T>(a, s, lane, -1, nullptr);
+    if (find >= 0 && base + per * a.c.hkv > find) {
+      cur->b = b;
+      cur->h = (int)((find - base) / per);
+      seq_tiles<TQ, T>(a, s, lane, find - base - cur->h * per, cur);
+      return 0;
+    }
+    base += per * a.c.hkv;
+  }
+  return base;
+}
+
+// N dwords from a 4-byte (N = 1, 3) or 8 / 16-byte aligned address.
+template <int N>
+__device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const u32x4 v = ((const u32x4*)p)[i];
+      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (N == 2) {
+    const uint2 v = *(const uint2*)p;
+    w[0] = v.x; w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = ((const uint32_t*)p)[i];
+  }
+}
+
+// Everything a wave reads of one sub-block: codes, the scales of this lane's
+// result tokens 4 kg .. 4 kg + 3 (pairs of halfs), the key zero points of its
+// operand token m, the value zero points of its operand tokens 4 kg ...
+template <int D, int NG, bool SYM>
+struct Block {
+  static constexpr int NS = D / 32;
+  uint32_t k[NS], v[NS];
+  uint32_t ks[NG][2], vs[NG][2];
+  uint32_t kz[(NG + 1) / 2];
+  uint32_t vz[SYM ? 1 : NG][2];
+
+  __device__ __forceinline__ void load(const uint8_t* blk, uint32_t meta, int m, int kg) {
+    load_dwords<NS>(blk + m * (D / 2) + kg * (4 * NS), k);
+    const uint8_t* p = blk + 8 * D;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) load_dwords<2>(p + g * 32 + kg * 8, ks[g]);
+    const uint8_t* w = p + meta;
+    load_dwords<NS>(w + kg * (64 * NS) + m * (4 * NS), v);
+    const uint8_t* pv = w + 8 * D;
+    if constexpr (SYM) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) load_dwords<2>(pv + g * 32 + kg * 8, vs[g]);
+    } else {
+      const uint8_t* z = p + 32 * NG + m * (2 * NG);
+      if constexpr (NG % 2 == 0) {
+        load_dwords<NG / 2>(z, kz);
+      } else {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t h = ((const uint16_t*)z)[g];
+          kz[g / 2] = g & 1 ? kz[g / 2] | h << 16 : h;
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        uint32_t t[4];
+        load_dwords<4>(pv + g * 64 + kg * 16, t);
+        vs[g][0] = t[0]; vs[g][1] = t[1];
+        vz[g][0] = t[2]; vz[g][1] = t[3];
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ float lo_f16(uint32_t w) { return f16_to_f32((uint16_t)(w & 0xFFFFu)); }
+__device__ __forceinline__ float hi_f16(uint32_t w) { return f16_to_f32((uint16_t)(w >> 16)); }
+
+// Half i of a dword array, as float.
+template <int N>
+__device__ __forceinline__ float half_of(const uint32_t (&w)[N], int i) {
+  return i & 1 ? hi_f16(w[i >> 1]) : lo_f16(w[i >> 1]);
+}
+
+// Byte i of a dword array next to byte j: {i, 0, j, 0}.
+template <int N>
+__device__ __forceinline__ uint32_t byte_pair(const uint32_t (&w)[N], int i, int j) {
+  const uint32_t sel = (uint32_t)(i & 3) | 0x0C000C00u | (uint32_t)(4 + (j & 3)) << 16;
+  return __builtin_amdgcn_perm(w[j >> 2], w[i >> 2], sel);
+}
+
+// A pair of codes, masked in place, to fp16 c - z.  lo: nibbles at bits 0..3
+// of each half, where 0x6400 | c is 1024 + c; hi: at bits 4..7, where it is
+// 1024 + 16 c.  n: -(1024 + z), or -(64 + z).  Every step is exact.
+__device__ __forceinline__ uint32_t minus_zero_lo(uint32_t w, f16x2 n) {
+  const f16x2 v = __builtin_bit_cast(f16x2, (w & 0x000F000Fu) | 0x64006400u);
+  return __builtin_bit_cast(uint32_t, v + n);
+}
+__device__ __forceinline__ uint32_t minus_zero_hi(uint32_t w, f16x2 n) {
+  const f16x2 v = __builtin_bit_cast(f16x2, (w & 0x00F000F0u) | 0x64006400u);
+  const f16x2 s = {(_Float16)0.0625f, (_Float16)0.0625f};
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(v, s, n));
+}
+
+__device__ __forceinline__ f16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const u32x4 v = {a, b, c, d};
+  return __builtin_bit_cast(f16x8, v);
+}
+
+// The rows kernel.  Each wave takes 32 keys at a time on its own, straight from
+// memory to registers, with two products of the matrix cores:
+//   S^T [keys, rows] = codes_K [keys, D] Q^T     (16x16x32, one step per 32 channels)
+//   O^T [D, rows]   += codes_V^T [D, keys] P^T   (one step per 32 keys)
+// The result layout of the first (lane = row, registers = 4 keys) is the operand
+// layout of the second, so P never leaves its lane.
+//
+// Codes enter as the exact fp16 integers c - z.  (As subnormals c 2^-24, two of
+// them for one AND, they would be exact too, but the products are aligned by
+// the operands' exponent fields: measured errors of 2^-14 of a code.)
+// Q becomes fp16 with a power of two per row that puts its largest element
+// near 2^14: exact for fp16 and bf16 elements down to 2^-29 of the largest.
+// So the scores are exact up to fp32 sums: s = sum_g S_g ((codes - z) . q).
+// P' = p S_V goes to the matrix cores as fp16, one operand per group; it is
+// rounded once (2^-11).  The reference that the exponentials subtract is the
+// running maximum of score + log2 S_V, so that P' itself, not p, is what lies
+// in fp16's range, whatever the scales are.
+template <int D, int NG, int NQ, bool SYM>
+struct Rows {
+  static constexpr int NS = D / 32, SPG = NS / NG, TQ = 16 * NQ;
+  static constexpr int DH = D > 128 ? 128 : D;       // columns of a join pass
+  static constexpr int kSmemRow = DH + 4;
+  static constexpr int kSmemFloats = kWaves * 16 * kSmemRow + 2 * kWaves * 16;
+
+  f16x8 q[NQ][NS];
+  float A[NQ];                      // score factor
+  f32x4 o[NQ][2 * NS];
+  float mref[NQ], l[NQ];
+
+  __device__ __forceinline__ void load_q(const Kv4Attn& a, const Seq& s, int h, int qt, int m, int kg) {
+    const int rows = s.n * a.r;
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq) {
+      const int row = qt * TQ + nq * 16 + m;
+      float x[NS][8];
+      float mx = 0.0f;
+      const bool ok = row < rows;
+      const uint16_t* p = a.q;
+      if (ok) p += (int64_t)(s.q0 + row / a.r) * a.q_ts + (int64_t)(h * a.r + row % a.r) * a.q_hs;
+#pragma unroll
+      for (int st = 0; st < NS; ++st) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (ok) v = *(const uint4*)(p + 32 * st + 8 * kg);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[st][2 * i] = a.bf16 ? bf16_to_f32(w[i] & 0xFFFFu) : lo_f16(w[i]);
+          x[st][2 * i + 1] = a.bf16 ? __uint_as_float(w[i] & 0xFFFF0000u) : hi_f16(w[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(x[st][i]));
+      }
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      int e = (int)(__float_as_uint(mx) >> 23) - 127;   // exponent of the largest
+      e = e < -60 ? -60 : (e > 100 ? 100 : e);
+      const float f = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+      A[nq] = a.scale_log2 * __uint_as_float((uint32_t)(127 - 14 + e) << 23);   // / f
+#pragma unroll
+      for (int st = 0; st < NS; ++st)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[nq][st][i] = (_Float16)(x[st][i] * f);
+    }
+  }
+
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq) {
+      mref[nq] = kNegInf;
+      l[nq] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2 * NS; ++i) o[nq][i] = f32x4{0, 0, 0, 0};
+    }
+  }
+
+  // 32 keys from position u on; `masked` where some row does not see all of
+  // them.  ok0 / ok1: the sub-blocks that exist.
+  __device__ __forceinline__ void unit(const Kv4Attn& a, const Seq& s, const Span& sp, int qt, int u,
+                                       bool masked, bool ok0, bool ok1, Block<D, NG, SYM> (&blk)[2], int m,
+                                       int kg) {
+    if (masked) {
+      // keys that no row of the tile sees: whatever their memory holds counts
+      // as value scale and zero point 0 (their scores are dropped below)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        uint32_t live[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int pos = u + 16 * t + 4 * kg + 2 * i;
+          const bool ok = t ? ok1 : ok0;
+          live[i] = (ok && pos >= sp.lo && pos < sp.hi ? 0xFFFFu : 0u) |
+                    (ok && pos + 1 >= sp.lo && pos + 1 < sp.hi ? 0xFFFF0000u : 0u);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            blk[t].vs[g][i] &= live[i];
+            if constexpr (!SYM) blk[t].vz[g][i] &= live[i];
+          }
+      }
+    }
+    float x[NQ][2][4];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      f32x4 acc[NQ][2];
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) acc[nq][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        f16x2 z2 = {(_Float16)8.0f, (_Float16)8.0f};
+        if constexpr (!SYM) {
+          const f16x2 zp = __builtin_bit_cast(f16x2, blk[t].kz[g / 2]);
+          z2 = f16x2{zp[g & 1], zp[g & 1]};
+        }
+        const f16x2 n1 = (_Float16)-1024.0f - z2, n2 = (_Float16)-64.0f - z2;
+#pragma unroll
+        for (int st = g * SPG; st < (g + 1) * SPG; ++st) {
+          const uint32_t d = blk[t].k[st], e = d >> 8;
+          const f16x8 w = frag(minus_zero_lo(d, n1), minus_zero_hi(d, n2), minus_zero_lo(e, n1),
+                               minus_zero_hi(e, n2));
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq)
+            acc[nq][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, q[nq][st], acc[nq][t], 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float S = half_of(blk[t].ks[g], i);
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq)
+            x[nq][t][i] = g == 0 ? S * acc[nq][t][i] : __builtin_fmaf(S, acc[nq][t][i], x[nq][t][i]);
+        }
+    }
+    // log2 of the largest value scale of each key, within a tenth
+    float lv[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t b = 0;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t c = i & 1 ? blk[t].vs[g][i >> 1] >> 16 : blk[t].vs[g][i >> 1] & 0xFFFFu;
+          b = c > b ? c : b;
+        }
+        lv[t][i] = __builtin_fmaf((float)b, 1.0f / 1024.0f, -15.0f);
+      }
+    float p[NQ][2][4];
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq) {
+      float y[2][4], top = kNegInf;
+      uint32_t hide = 0;
+      if (masked) {
+        const int tok = (qt * TQ + nq * 16 + m) / a.r;
+        const int pos = s.kv - s.n + tok;
+        const int last = a.causal ? pos : 0x7FFFFFFF;
+        const int first = a.window > 0 ? pos - a.window + 1 : -0x7FFFFFFF;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = u + 16 * t + 4 * kg + i;
+            const bool seen = (t ? ok1 : ok0) && j < s.kv && j <= last && j >= first;
+            hide |= seen ? 0u : 1u << (4 * t + i);
+          }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y[t][i] = __builtin_fmaf(x[nq][t][i], A[nq], lv[t][i]);
+          if (masked && (hide >> (4 * t + i) & 1u)) y[t][i] = kNegInf;
+          top = fmaxf(top, y[t][i]);
+        }
+      if (__any(top > mref[nq] + kSlack)) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(top, mref[nq]);
+        const float c = mn == mref[nq] ? 1.0f : exp2_hw(mref[nq] - mn);
+        mref[nq] = mn;
+        l[nq] *= c;
+#pragma unroll
+        for (int i = 0; i < 2 * NS; ++i) o[nq][i] *= c;
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float e = exp2_hw(__builtin_fmaf(x[nq][t][i], A[nq], -mref[nq]));
+          if (masked && (hide >> (4 * t + i) & 1u)) e = 0.0f;
+          p[nq][t][i] = e;
+          l[nq] += e;
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      f16x8 pw[NQ];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float S = half_of(blk[t].vs[g], i);
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq) pw[nq][4 * t + i] = (_Float16)(p[nq][t][i] * S);
+        }
+      f16x2 n1[4], n2[4];   // by token pair
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f16x2 z = SYM ? f16x2{(_Float16)8.0f, (_Float16)8.0f}
+                            : __builtin_bit_cast(f16x2, blk[i >> 1].vz[SYM ? 0 : g][i & 1]);
+        n1[i] = (_Float16)-1024.0f - z;
+        n2[i] = (_Float16)-64.0f - z;
+      }
+#pragma unroll
+      for (int b = g * SPG; b < (g + 1) * SPG; ++b) {
+        uint32_t w[4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          w[2 * t] = byte_pair<NS>(blk[t].v, b, NS + b);
+          w[2 * t + 1] = byte_pair<NS>(blk[t].v, 2 * NS + b, 3 * NS + b);
+        }
+        const f16x8 ev = frag(minus_zero_lo(w[0], n1[0]), minus_zero_lo(w[1], n1[1]),
+                              minus_zero_lo(w[2], n1[2]), minus_zero_lo(w[3], n1[3]));
+        const f16x8 od = frag(minus_zero_hi(w[0], n2[0]), minus_zero_hi(w[1], n2[1]),
+                              minus_zero_hi(w[2], n2[2]), minus_zero_hi(w[3], n2[3]));
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+          o[nq][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ev, pw[nq], o[nq][2 * b], 0, 0, 0);
+          o[nq][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(od, pw[nq], o[nq][2 * b + 1], 0, 0, 0);
+        }
+      }
+    }
+  }
+
+  // Key tiles j0 .. j1 - 1 of the span.
+  __device__ __forceinline__ void keys(const Kv4Attn& a, const Seq& s, const Span& sp, int64_t b, int h,
+                                       int qt, int j0, int j1, int wave, int m, int kg) {
+    const int32_t* row = a.table + b * a.table_pages;
+    const int ps = a.c.page_shift;
+    for (int j = j0; j < j1; ++j) {
+      const int u = (sp.t0 + j) * kTile + wave * kUnit;
+      if (u >= sp.hi || u + kUnit <= sp.lo) continue;
+      Block<D, NG, SYM> blk[2];
+      bool ok[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int pos = u + 16 * t;
+        int64_t page = 0;
+        ok[t] = false;
+        if (pos < sp.hi && pos + 16 > sp.lo) {
+          page = row[pos >> ps];
+          ok[t] = page >= 0 && page < a.c.n_pages;
+          page = ok[t] ? page : 0;
+        }
+        blk[t].load(a.c.cache + kv4_block_offset(a.c, page, h, ok[t] ? pos & ((1 << ps) - 1) : 0),
+                    a.c.meta, m, kg);
+      }
+      // every row sees every key: all before the first query's position and
+      // inside the last one's window
+      bool full = ok[0] && ok[1] && u + kUnit <= s.kv;
+      if (a.causal) full = full && u + kUnit - 1 <= sp.p0;
+      if (a.window > 0) full = full && u > sp.p1 - a.window;
+      if (full)
+        unit(a, s, sp, qt, u, false, true, true, blk, m, kg);
+      else
+        unit(a, s, sp, qt, u, true, ok[0], ok[1], blk, m, kg);
+    }
+  }
+
+  // Joins the four waves' results and writes the rows: to `out` (part null) or,
+  // unnormalized with their statistics, to a partial slot.
+  __device__ __forceinline__ void finish(const Kv4Attn& a, const Seq& s, int h, int qt, float* part,
+                                         float* smem, int wave, int m, int kg) {
+    const int rows = s.n * a.r;
+    float* so = smem;
+    float* sm = smem + kWaves * 16 * kSmemRow;
+    float* sl = sm + kWaves * 16;
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq) {
+      float lt = l[nq];
+      lt += __shfl_xor(lt, 16);
+      lt += __shfl_xor(lt, 32);
+      // the reference is the same in the four lanes of a row unless the row
+      // has seen nothing; the waves' references differ
+      for (int half = 0; half < D / DH; ++half) {
+        __syncthreads();
+        if (kg == 0) {
+          sm[wave * 16 + m] = mref[nq];
+          sl[wave * 16 + m] = lt;
+        }
+#pragma unroll
+        for (int bb = 0; bb < DH / 32; ++bb) {
+#pragma unroll
+          for (int hb = 0; hb < D / DH; ++hb) {
+            if (hb != half) continue;
+            const int b = hb * (DH / 32) + bb;
+            const f32x4 e = o[nq][2 * b], d = o[nq][2 * b + 1];
+            float4* dst = (float4*)(so + (wave * 16 + m) * kSmemRow + 32 * bb + 8 * kg);
+            dst[0] = make_float4(e[0], d[0], e[1], d[1]);
+            dst[1] = make_float4(e[2], d[2], e[3], d[3]);
+          }
+        }
+        __syncthreads();
+        constexpr int C = DH / 16;               // columns per thread
+        const int rr = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * C;
+        const int row = qt * TQ + nq * 16 + rr;
+        if (row < rows) {
+          float M = kNegInf;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) M = fmaxf(M, sm[w * 16 + rr]);
+          float L = 0.0f, acc[C];
+#pragma unroll
+          for (int i = 0; i < C; ++i) acc[i] = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) {
+            const float mw = sm[w * 16 + rr];
+            const float f = mw == kNegInf ? 0.0f : exp2_hw(mw - M);
+            L = __builtin_fmaf(f, sl[w * 16 + rr], L);
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+              acc[i] = __builtin_fmaf(f, so[(w * 16 + rr) * kSmemRow + c0 + i], acc[i]);
+          }
+          if (part) {
+            float* po = part + (nq * 16 + rr) * D + half * DH + c0;
+#pragma unroll
+            for (int i = 0; i < C; ++i) po[i] = acc[i];
+            if ((threadIdx.x & 15) == 0 && half == 0) {
+              part[TQ * D + nq * 16 + rr] = M;
+              part[TQ * D + TQ + nq * 16 + rr] = L;
+            }
+          } else {
+            const int64_t orow = (int64_t)(s.q0 + row / a.r) * a.hq + h * a.r + row % a.r;
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+            uint16_t* po = a.out + orow * D + half * DH + c0;
+#pragma unroll
+            for (int i = 0; i < C; i += 2) {
+              const float v0 = acc[i] * inv, v1 = acc[i + 1] * inv;
+              *(uint32_t*)(po + i) = pack_out(a.bf16, v0, v1);
+            }
+            if (a.lse && (threadIdx.x & 15) == 0 && half == 0) a.lse[orow] = lse_of(M, L);
+          }
+        }
+      }
+    }
+  }
+
+  static __device__ __forceinline__ float lse_of(float M, float L) {
+    return L == 0.0f ? kNegInf : (M + __log2f(L)) * 0.69314718055994531f;
+  }
+  static __device__ __forceinline__ uint32_t pack_out(int bf16, float a, float b) {
+    if (bf16) return bf16_bits(a) | (uint32_t)bf16_bits(b) << 16;
+    return stream_util::f32_to_f16_rne(a) | (uint32_t)stream_util::f32_to_f16_rne(b) << 16;
+  }
+  // nearest-even bf16; NaN stays NaN
+  static __device__ __forceinline__ uint16_t bf16_bits(float f) {
+    return f == f ? f32_to_bf16_rne(f) : (uint16_t)0x7FC0u;
+  }
+};
+
+// XCD-aware order: workgroups go round robin over the 8 dies, so worker
+// numbers are dealt such that each die works on one run of the tiles and its
+// L2 cache sees neighbouring keys.
+__device__ __forceinline__ int worker_of(int bid, int workers) {
+  return workers % 8 == 0 ? (bid & 7) * (workers >> 3) + (bid >> 3) : bid;
+}
+
+template <int D, int NG, int NQ, bool SYM, bool SPLIT>
+__global__ __launch_bounds__(kWaves * 64, NQ <= 2 && D * NQ <= 256 ? 2 : 1) void kv4_rows_kernel(Kv4Attn a, int few) {
+  using R = Rows<D, NG, NQ, SYM>;
+  __shared__ __attribute__((aligned(16))) float smem[R::kSmemFloats];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = lane & 15, kg = lane >> 4;
+  R st;
+  if constexpr (!SPLIT) {
+    // one workgroup per (sequence, head, row tile)
+    const int gq = a.grid_q;
+    const int64_t id = blockIdx.x;
+    const int64_t b = id / ((int64_t)gq * a.c.hkv);
+    const int h = (int)(id / gq % a.c.hkv);
+    const Seq s = get_seq(a, b);
+    const int nqt = (s.n * a.r + R::TQ - 1) / R::TQ;
+    for (int qt = (int)(id % gq); qt < nqt; qt += gq) {
+      const Span sp = get_span<R::TQ, kTile>(a, s, qt);
+      st.load_q(a, s, h, qt, m, kg);
+      st.reset();
+      st.keys(a, s, sp, b, h, qt, 0, sp.cnt, wave, m, kg);
+      st.finish(a, s, h, qt, nullptr, smem, wave, m, kg);
+    }
+  } else {
+    const int w = worker_of(blockIdx.x, a.workers);
+    const int64_t total = all_tiles<R::TQ, kTile>(a, lane, few != 0, -1, nullptr);
+    int64_t at = total * w / a.workers;
+    const int64_t end = total * (w + 1) / a.workers;
+    int32_t head_valid = 0, head_ends = 0, tail_valid = 0;
+    Cursor cur{0, 0, 0, 0};
+    if (at < end) {
+      all_tiles<R::TQ, kTile>(a, lane, few != 0, at, &cur);
+      Seq s = get_seq(a, cur.b);
+      for (;;) {
+        const Span sp = get_span<R::TQ, kTile>(a, s, cur.qt);
+        const int j0 = (int)cur.off;
+        const int j1 = sp.cnt - j0 < end - at ? sp.cnt : j0 + (int)(end - at);
+        const bool starts = j0 == 0, ends = j1 == sp.cnt;
+        st.load_q(a, s, cur.h, cur.qt, m, kg);
+        st.reset();
+        st.keys(a, s, sp, cur.b, cur.h, cur.qt, j0, j1, wave, m, kg);
+        float* part = nullptr;
+        if (!(starts && ends)) {
+          part = a.part + ((int64_t)2 * w + (starts ? 1 : 0)) * (R::TQ * (D + 2));
+          if (starts) { tail_valid = 1; } else { head_valid = 1; head_ends = ends; }
+        }
+        st.finish(a, s, cur.h, cur.qt, part, smem, wave, m, kg);
+        at += j1 - j0;
+        if (at >= end) break;
+        // the next row tile, head, sequence that has rows
+        cur.off = 0;
+        const int nqt = (s.n * a.r + R::TQ - 1) / R::TQ;
+        if (++cur.qt == nqt) {
+          cur.qt = 0;
+          if (++cur.h == a.c.hkv) {
+            cur.h = 0;
+            do { ++cur.b; s = get_seq(a, cur.b); } while (s.n == 0);
+          }
+        }
+      }
+    }
+    if (threadIdx.x == 0) {
+      int32_t* mt = a.meta + (int64_t)w * kMetaInts;
+      mt[0] = head_valid;
+      mt[1] = head_ends;
+      mt[2] = tail_valid;
+      mt[3] = (int32_t)cur.b;
+      mt[4] = cur.h;
+      mt[5] = cur.qt;
+    }
+  }
+}
+
+// Joins the partial results of the row tiles that were split.  Worker w left
+// its last row tile open (tail): the workers after it hold the rest, up to the
+// one that ended it.  One workgroup per (worker, row): D / 4 threads hold a
+// row, the others take every PG-th partial.
+template <int D, int TQ>
+__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
+  constexpr int QD = D / 4, PG = 256 / QD;
+  __shared__ int stop;
+  __shared__ float4 so[PG][QD];
+  __shared__ float sm[PG], sl[PG];
+  const int w = blockIdx.x;
+  const int32_t* mt = a.meta + (int64_t)w * kMetaInts;
+  if (!mt[2]) return;
+  const Seq s = get_seq(a, mt[3]);
+  const int h = mt[4], row = mt[5] * TQ + blockIdx.y;
+  if (row >= s.n * a.r) return;
+  const int tid = threadIdx.x;
+  if (tid == 0) stop = 0x7FFFFFFF;
+  __syncthreads();
+  for (int c = w + 1; c < a.workers; c += 256) {
+    if (c + tid < a.workers && a.meta[(int64_t)(c + tid) * kMetaInts + 1]) atomicMin(&stop, c + tid);
+    __syncthreads();
+    const int found = stop;
+    __syncthreads();
+    if (found != 0x7FFFFFFF) break;
+  }
+  const int last = stop < a.workers ? stop : a.workers - 1;
+  const int64_t slot = TQ * (D + 2);
+  const int pg = tid / QD, qd = tid % QD;
+  float M = kNegInf, L = 0.0f;
+  float4 acc = make_float4(0, 0, 0, 0);
+  if (pg < PG) {
+#pragma unroll 4
+    for (int c = w + pg; c <= last; c += PG) {
+      const float* p = a.part + (2 * (int64_t)c + (c == w ? 1 : 0)) * slot;
+      // a worker in between that had no tile wrote nothing
+      const bool valid = c == w || a.meta[(int64_t)c * kMetaInts];
+      if (!valid) continue;
+      const float mc = p[TQ * D + blockIdx.y], lc = p[TQ * D + TQ + blockIdx.y];
+      const float4 v = *(const float4*)(p + blockIdx.y * D + qd * 4);
+      const float mn = fmaxf(M, mc);
+      const float f0 = M == kNegInf ? 0.0f : exp2_hw(M - mn);
+      const float f1 = mc == kNegInf ? 0.0f : exp2_hw(mc - mn);
+      M = mn;
+      L = L * f0 + lc * f1;
+      acc.x = acc.x * f0 + v.x * f1;
+      acc.y = acc.y * f0 + v.y * f1;
+      acc.z = acc.z * f0 + v.z * f1;
+      acc.w = acc.w * f0 + v.w * f1;
+    }
+    so[pg][qd] = acc;
+    if (qd == 0) { sm[pg] = M; sl[pg] = L; }
+  }
+  __syncthreads();
+  if (tid >= QD) return;
+  M = kNegInf;
+#pragma unroll
+  for (int i = 0; i < PG; ++i) M = fmaxf(M, sm[i]);
+  L = 0.0f;
+  acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < PG; ++i) {
+    const float f = sm[i] == kNegInf ? 0.0f : exp2_hw(sm[i] - M);
+    const float4 v = so[i][tid];
+    L += f * sl[i];
+    acc.x += f * v.x;
+    acc.y += f * v.y;
+    acc.z += f * v.z;
+    acc.w += f * v.w;
+  }
+  using R = Rows<D, 1, 1, true>;
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  const int64_t orow = (int64_t)(s.q0 + row / a.r) * a.hq + h * a.r + row % a.r;
+  *(uint2*)(a.out + orow * D + tid * 4) =
+      make_uint2(R::pack_out(a.bf16, acc.x * inv, acc.y * inv), R::pack_out(a.bf16, acc.z * inv, acc.w * inv));
+  if (a.lse && tid == 0) a.lse[orow] = R::lse_of(M, L);
+}
+
+template <int D, int NG, int NQ, bool SYM>
+hipError_t launch_rows(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
+  if (!p.split) {
+    const int64_t n = (int64_t)p.grid_q * a.c.hkv * a.batch;
+    hipLaunchKernelGGL((kv4_rows_kernel<D, NG, NQ, SYM, false>), dim3((unsigned)n), dim3(kWaves * 64), 0,
+                       s, a, 0);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((kv4_rows_kernel<D, NG, NQ, SYM, true>), dim3(a.workers), dim3(kWaves * 64), 0, s, a,
+                     (int)(p.grid_q <= 4));
+  if (hipError_t e = hipGetLastError()) return e;
+  hipLaunchKernelGGL((kv4_join_kernel<D, 16 * NQ>), dim3(a.workers, 16 * NQ), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int D, int NG, bool SYM>
+hipError_t launch_rows_nq(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
+  if (p.nq == 1) return launch_rows<D, NG, 1, SYM>(a, p, s);
+  if (p.nq == 2) return launch_rows<D, NG, 2, SYM>(a, p, s);
+  if constexpr (D <= 128) return launch_rows<D, NG, 4, SYM>(a, p, s);
+  return hipErrorInvalidValue;
+}
+
+template <int D, int NG>
+hipError_t launch_rows_sym(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
+  return a.c.sym ? launch_rows_nq<D, NG, true>(a, p, s) : launch_rows_nq<D, NG, false>(a, p, s);
+}
+
+}  // namespace kv4
+
+}  // namespace gq
