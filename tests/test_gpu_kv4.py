@@ -216,13 +216,35 @@ def test_few_tokens_and_head_ratios(h, r, dtype, d, g):
     p.check(*p.run(), what="few tokens")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,g,sym", LAYOUTS)
+def test_prompts(d, g, sym, dtype):
+    p = Problem(d * 5 + g, d, g, sym, 16, dtype, 2, 2, [150, 1, 0, 65, 200], [150, 40, 9, 1100, 333])
+    announce_case(p, "prompts")
+    a = p.run()
+    p.check(*a, fp16_operands=True, what="prompts")
+    b = p.run()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("h,r,q,kv", [(1, 64, [9, 70], [700, 70]), (3, 7, [40, 1, 80], [40, 1, 2000]),
+                                      (8, 1, [513], [600])])
+def test_prompt_head_ratios(h, r, q, kv):
+    p = Problem(h + r, 128, 64, False, 64, "bf16", h, r, q, kv)
+    announce_case(p, "prompt head ratios")
+    p.check(*p.run(), fp16_operands=True, what="prompt head ratios")
+
+
 @pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 1), (True, 20), (True, 130), (True, 2 ** 31 - 1)])
 @pytest.mark.parametrize("long", [False, True])
 def test_masks(causal, window, long):
     kv = [1500, 40, 9, 5, 2100] if long else [200, 40, 9, 5, 300]
     p = Problem(77 + window % 1000, 128, 32, False, 16, "f16", 2, 2, [70, 40, 12, 9, 1], kv)   # 12 > 9: rows before all keys
     announce_case(p, f"masks causal={causal} window={window}")
-    p.check(*p.run(causal=causal, window=window), causal=causal, window=window, what="masks")
+    p.check(*p.run(causal=causal, window=window), causal=causal, window=window, fp16_operands=True,
+            what="masks")
+    few = Problem(78 + window % 1000, 128, 32, False, 16, "f16", 2, 2, [7, 8, 3, 9, 1], kv)           # the other kernel
+    few.check(*few.run(causal=causal, window=window), causal=causal, window=window, what="masks, few rows")
 
 
 @pytest.mark.parametrize("max_kv", [None, 1, 5000])
@@ -246,6 +268,12 @@ def test_bad_pages_and_lengths():
     dead[2][:] = True
     announce_case(p, "bad pages")
     p.check(*p.run(table=table), dead=dead, what="bad pages")
+    for what, q_lens in (("few rows", [1, 3, 1]), ("many rows", [60, 70, 9])):
+        p = Problem(19, 128, 64, False, 16, "bf16", 2, 4, q_lens, [100, 1200, 40])
+        table = p.table.clone()
+        table[0, 2], table[1, 70], table[1, 3] = -1, p.n_pages, -2 ** 31
+        table[2, :] = 2 ** 31 - 1
+        p.check(*p.run(table=table), dead=dead, fp16_operands=True, what="bad pages, " + what)
     # lengths below zero and beyond the table
     q = Problem(10, 128, 128, True, 16, "f16", 1, 2, [1, 1], [0, 64])
     short = q.table[:, :4].contiguous()
@@ -264,8 +292,9 @@ def test_query_starts_out_of_range_and_rows_left_alone():
 
 def test_extreme_values():
     # scales over fp16's whole range, large scores, a key that takes all the weight
-    for sk, sv, qs in ((1e-4, 1e-6, 2.0), (40.0, 3e4, 1.0), (1.0, 1e-7, 30.0), (1e-7, 60.0, 1e4)):
-        p = Problem(31, 128, 32, False, 16, "bf16", 1, 4, [1, 2], [37, 1100], q_scale=qs)
+    for sk, sv, qs, q_lens in [(*c, n) for n in ([1, 2], [30, 50])
+                               for c in ((1e-4, 1e-6, 2.0), (40.0, 3e4, 1.0), (1.0, 1e-7, 30.0), (1e-7, 60.0, 1e4))]:
+        p = Problem(31, 128, 32, False, 16, "bf16", 1, 4, q_lens, [37, 1100], q_scale=qs)
         gen = torch.Generator().manual_seed(8)
         k, v = rows(gen, 1137, 1, 128, torch.bfloat16) * sk, rows(gen, 1137, 1, 128, torch.bfloat16) * sv
         slots = torch.cat([p.table[b].long()[torch.arange(n) // 16] * 16 + torch.arange(n) % 16
@@ -275,19 +304,20 @@ def test_extreme_values():
         p.v, b, _ = quantise64(v, 32, False)
         p.sk, p.sv = a.amax(-1), b.amax(-1)
         announce(f"kv4 extreme keys x{sk} values x{sv} queries x{qs}")
-        p.check(*p.run(), what="extreme values")
+        p.check(*p.run(), fp16_operands=q_lens[0] > 1, what="extreme values")
 
 
 def test_nonfinite_query_stays_in_its_row():
-    p = Problem(14, 128, 128, False, 16, "bf16", 2, 4, [1, 1], [70, 1300])
-    q = p.q.cuda().clone()
-    q[0, 1, 5], q[1, 6, 0] = math.nan, math.inf
-    out, lse = p.run(q=q)
-    assert torch.isnan(out[0, 1]).all() and torch.isnan(out[1, 6]).all()
-    ref, rl = p.run()
-    keep = torch.ones(2, 8, dtype=torch.bool)
-    keep[0, 1] = keep[1, 6] = False
-    assert torch.equal(out[keep], ref[keep]) and torch.equal(lse[keep], rl[keep])
+    for q_lens in ([1, 1], [40, 50]):
+        p = Problem(14, 128, 128, False, 16, "bf16", 2, 4, q_lens, [70, 1300])
+        q = p.q.cuda().clone()
+        q[0, 1, 5], q[1, 6, 0] = math.nan, math.inf
+        out, lse = p.run(q=q)
+        assert torch.isnan(out[0, 1]).all() and torch.isnan(out[1, 6]).all()
+        ref, rl = p.run()
+        keep = torch.ones(sum(q_lens), 8, dtype=torch.bool)
+        keep[0, 1] = keep[1, 6] = False
+        assert torch.equal(out[keep], ref[keep]) and torch.equal(lse[keep], rl[keep])
 
 
 def test_strided_queries_streams_and_workspace():

@@ -21,7 +21,8 @@ LIB = os.path.join(PKG, "libgq.so")
 
 SOURCES = ["gq_api.cpp", "quant.hip", "gemv.hip", "gemv_mfma.hip", "gemm.hip", "q4k.hip",
            "kv4_api.cpp", "kv4_store.hip", "kv4_rows_d64.hip", "kv4_rows_d96.hip", "kv4_rows_d128.hip",
-           "kv4_rows_d256.hip", "bench_kernels.hip"]
+           "kv4_rows_d256.hip", "kv4_tile_d64.hip", "kv4_tile_d96.hip", "kv4_tile_d128.hip",
+           "kv4_tile_d256.hip", "bench_kernels.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

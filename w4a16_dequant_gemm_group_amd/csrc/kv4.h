@@ -76,8 +76,9 @@ struct Kv4Attn {
 };
 
 struct Kv4Plan {
+  bool tile;           // the kernel for many rows; else the rows kernel
   bool split;
-  int nq;              // 16-row query tiles per workgroup
+  int nq;              // rows kernel: 16-row query tiles per workgroup
   int workers;         // workgroups when split
   int grid_q;          // row tiles per (sequence, head) when not split
   size_t ws_bytes;
@@ -91,5 +92,9 @@ hipError_t launch_kv4_rows_64(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s)
 hipError_t launch_kv4_rows_96(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s);
 hipError_t launch_kv4_rows_128(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s);
 hipError_t launch_kv4_rows_256(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s);
+hipError_t launch_kv4_tile_64(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s);
+hipError_t launch_kv4_tile_96(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s);
+hipError_t launch_kv4_tile_128(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s);
+hipError_t launch_kv4_tile_256(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s);
 
 }  // namespace gq

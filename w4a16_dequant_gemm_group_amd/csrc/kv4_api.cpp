@@ -78,30 +78,36 @@ gq_status check_attention(const gq_kv4_attention_args& a) {
 }  // namespace
 
 Kv4Plan kv4_plan(const gq_kv4_attention_args& a) {
-  constexpr int kTileKeys = 128;   // keys of one tile of the split
-  const int r = a.q_heads / a.layout.kv_heads;
+  const int d = a.layout.head_dim, r = a.q_heads / a.layout.kv_heads;
   const int64_t rows = std::max<int64_t>(1, a.max_q_len) * r;
   Kv4Plan p;
-  // Query tiles of 16 rows per workgroup: as many as the longest query needs,
-  // up to the 4 (2 at head_dim 256) whose results fit the registers.
-  const int top = a.layout.head_dim > 128 ? 2 : 4;
-  p.nq = rows <= 16 ? 1 : (rows <= 32 || top == 2 ? 2 : 4);
-  p.grid_q = (int)((rows + 16 * p.nq - 1) / (16 * p.nq));
-  const int64_t segs = a.batch * a.layout.kv_heads * p.grid_q;
-  const int64_t tiles = segs * std::max<int64_t>(1, (a.max_kv_len + kTileKeys - 1) / kTileKeys);
-  p.split = a.max_kv_len > 1024 || segs > INT32_MAX;
   p.workers = 0;
   p.ws_bytes = 0;
+  p.nq = rows <= 16 ? 1 : 2;
+  p.tile = rows > 32;
+  const int tq = p.tile ? (d > 128 ? 128 : 256) : 16 * p.nq;    // rows of a row tile
+  const int keys = p.tile ? 64 : 128;                           // keys of a tile of the split
+  p.grid_q = (int)((rows + tq - 1) / tq);
+  const int64_t segs = a.batch * a.layout.kv_heads * p.grid_q;
+  const int64_t tiles = segs * std::max<int64_t>(1, (a.max_kv_len + keys - 1) / keys);
+  p.split = p.tile || a.max_kv_len > 1024 || segs > INT32_MAX;
   if (p.split) {
-    const int64_t want = (int64_t)num_cus() * (p.nq == 1 ? 4 : 2);
+    const int64_t want = (int64_t)num_cus() * (p.tile ? 1 : (p.nq == 1 ? 4 : 2));
     p.workers = (int)std::max<int64_t>(8, std::min(tiles, want) & ~(int64_t)7);
-    p.ws_bytes = (size_t)p.workers * 32 +
-                 (size_t)p.workers * 2 * 16 * p.nq * (a.layout.head_dim + 2) * sizeof(float);
+    p.ws_bytes = (size_t)p.workers * 32 + (size_t)p.workers * 2 * tq * (d + 2) * sizeof(float);
   }
   return p;
 }
 
 hipError_t launch_kv4_attention(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
+  if (p.tile) {
+    switch (a.c.d) {
+      case 64: return launch_kv4_tile_64(a, p, s);
+      case 96: return launch_kv4_tile_96(a, p, s);
+      case 128: return launch_kv4_tile_128(a, p, s);
+      default: return launch_kv4_tile_256(a, p, s);
+    }
+  }
   switch (a.c.d) {
     case 64: return launch_kv4_rows_64(a, p, s);
     case 96: return launch_kv4_rows_96(a, p, s);

@@ -637,121 +637,123 @@ __device__ __forceinline__ int worker_of(int bid, int workers) {
   return workers % 8 == 0 ? (bid & 7) * (workers >> 3) + (bid >> 3) : bid;
 }
 
-template <int D, int NG, int NQ, bool SYM, bool SPLIT>
-__global__ __launch_bounds__(kWaves * 64, NQ <= 2 && D * NQ <= 256 ? 2 : 1) void kv4_rows_kernel(Kv4Attn a, int few) {
+template <int D, int NG, int NQ, bool SYM>
+__global__ __launch_bounds__(kWaves * 64, NQ <= 2 && D * NQ <= 256 ? 2 : 1) void kv4_rows_kernel(Kv4Attn a,
+                                                                                             int few) {
   using R = Rows<D, NG, NQ, SYM>;
   __shared__ __attribute__((aligned(16))) float smem[R::kSmemFloats];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, kg = lane >> 4;
   R st;
-  if constexpr (!SPLIT) {
-    // one workgroup per (sequence, head, row tile)
-    const int gq = a.grid_q;
-    const int64_t id = blockIdx.x;
-    const int64_t b = id / ((int64_t)gq * a.c.hkv);
-    const int h = (int)(id / gq % a.c.hkv);
-    const Seq s = get_seq(a, b);
-    const int nqt = (s.n * a.r + R::TQ - 1) / R::TQ;
-    for (int qt = (int)(id % gq); qt < nqt; qt += gq) {
-      const Span sp = get_span<R::TQ, kTile>(a, s, qt);
-      st.load_q(a, s, h, qt, m, kg);
-      st.reset();
-      st.keys(a, s, sp, b, h, qt, 0, sp.cnt, wave, m, kg);
-      st.finish(a, s, h, qt, nullptr, smem, wave, m, kg);
-    }
-  } else {
-    const int w = worker_of(blockIdx.x, a.workers);
+  const bool split = a.workers > 0;
+  int w = 0;
+  int64_t at = 0, end = 0;
+  Cursor cur{0, 0, 0, 0};
+  if (split) {
+    w = worker_of(blockIdx.x, a.workers);
     const int64_t total = all_tiles<R::TQ, kTile>(a, lane, few != 0, -1, nullptr);
-    int64_t at = total * w / a.workers;
-    const int64_t end = total * (w + 1) / a.workers;
-    int32_t head_valid = 0, head_ends = 0, tail_valid = 0;
-    Cursor cur{0, 0, 0, 0};
-    if (at < end) {
-      all_tiles<R::TQ, kTile>(a, lane, few != 0, at, &cur);
-      Seq s = get_seq(a, cur.b);
-      for (;;) {
-        const Span sp = get_span<R::TQ, kTile>(a, s, cur.qt);
-        const int j0 = (int)cur.off;
-        const int j1 = sp.cnt - j0 < end - at ? sp.cnt : j0 + (int)(end - at);
-        const bool starts = j0 == 0, ends = j1 == sp.cnt;
-        st.load_q(a, s, cur.h, cur.qt, m, kg);
-        st.reset();
-        st.keys(a, s, sp, cur.b, cur.h, cur.qt, j0, j1, wave, m, kg);
-        float* part = nullptr;
-        if (!(starts && ends)) {
-          part = a.part + ((int64_t)2 * w + (starts ? 1 : 0)) * (R::TQ * (D + 2));
-          if (starts) { tail_valid = 1; } else { head_valid = 1; head_ends = ends; }
-        }
-        st.finish(a, s, cur.h, cur.qt, part, smem, wave, m, kg);
-        at += j1 - j0;
-        if (at >= end) break;
-        // the next row tile, head, sequence that has rows
-        cur.off = 0;
-        const int nqt = (s.n * a.r + R::TQ - 1) / R::TQ;
-        if (++cur.qt == nqt) {
-          cur.qt = 0;
-          if (++cur.h == a.c.hkv) {
-            cur.h = 0;
-            do { ++cur.b; s = get_seq(a, cur.b); } while (s.n == 0);
-          }
-        }
+    at = total * w / a.workers;
+    end = total * (w + 1) / a.workers;
+    if (at < end) all_tiles<R::TQ, kTile>(a, lane, few != 0, at, &cur);
+  } else {
+    // one workgroup per (sequence, head, row tile)
+    const int64_t id = blockIdx.x;
+    cur.qt = (int)(id % a.grid_q);
+    cur.h = (int)(id / a.grid_q % a.c.hkv);
+    cur.b = id / ((int64_t)a.grid_q * a.c.hkv);
+  }
+  int32_t head_valid = 0, head_ends = 0, tail_valid = 0;
+  Seq s = get_seq(a, cur.b);
+  int nqt = (s.n * a.r + R::TQ - 1) / R::TQ;
+  while (split ? at < end : cur.qt < nqt) {
+    const Span sp = get_span<R::TQ, kTile>(a, s, cur.qt);
+    const int j0 = (int)cur.off;
+    const int j1 = !split || sp.cnt - j0 < end - at ? sp.cnt : j0 + (int)(end - at);
+    const bool starts = j0 == 0, ends = j1 == sp.cnt;
+    st.load_q(a, s, cur.h, cur.qt, m, kg);
+    st.reset();
+    st.keys(a, s, sp, cur.b, cur.h, cur.qt, j0, j1, wave, m, kg);
+    float* part = nullptr;
+    if (!(starts && ends)) {
+      part = a.part + ((int64_t)2 * w + (starts ? 1 : 0)) * (R::TQ * (D + 2));
+      if (starts) { tail_valid = 1; } else { head_valid = 1; head_ends = ends; }
+    }
+    st.finish(a, s, cur.h, cur.qt, part, smem, wave, m, kg);
+    if (!split) {
+      cur.qt += a.grid_q;
+      continue;
+    }
+    at += j1 - j0;
+    if (at >= end) break;
+    // the next row tile, head, sequence that has rows
+    cur.off = 0;
+    if (++cur.qt == nqt) {
+      cur.qt = 0;
+      if (++cur.h == a.c.hkv) {
+        cur.h = 0;
+        do { ++cur.b; s = get_seq(a, cur.b); } while (s.n == 0);
+        nqt = (s.n * a.r + R::TQ - 1) / R::TQ;
       }
     }
-    if (threadIdx.x == 0) {
-      int32_t* mt = a.meta + (int64_t)w * kMetaInts;
-      mt[0] = head_valid;
-      mt[1] = head_ends;
-      mt[2] = tail_valid;
-      mt[3] = (int32_t)cur.b;
-      mt[4] = cur.h;
-      mt[5] = cur.qt;
-    }
+  }
+  if (split && threadIdx.x == 0) {
+    int32_t* mt = a.meta + (int64_t)w * kMetaInts;
+    mt[0] = head_valid;
+    mt[1] = head_ends;
+    mt[2] = tail_valid;
+    mt[3] = (int32_t)cur.b;
+    mt[4] = cur.h;
+    mt[5] = cur.qt;
   }
 }
 
 // Joins the partial results of the row tiles that were split.  Worker w left
 // its last row tile open (tail): the workers after it hold the rest, up to the
-// one that ended it.  One workgroup per (worker, row): D / 4 threads hold a
-// row, the others take every PG-th partial.
-template <int D, int TQ>
+// one that ended it.  One workgroup per worker and RW rows: D / 4 threads hold
+// a row, PG such sets take every PG-th partial of it (many partials of few
+// rows for single tokens, few of many rows for prompts).
+template <int D, int TQ, int PG>
 __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
-  constexpr int QD = D / 4, PG = 256 / QD;
+  constexpr int QD = D / 4, RW = 256 / (QD * PG);
   __shared__ int stop;
-  __shared__ float4 so[PG][QD];
-  __shared__ float sm[PG], sl[PG];
+  __shared__ float4 so[RW][PG][QD];
+  __shared__ float sm[RW][PG], sl[RW][PG];
   const int w = blockIdx.x;
   const int32_t* mt = a.meta + (int64_t)w * kMetaInts;
   if (!mt[2]) return;
   const Seq s = get_seq(a, mt[3]);
-  const int h = mt[4], row = mt[5] * TQ + blockIdx.y;
-  if (row >= s.n * a.r) return;
+  const int h = mt[4], qt = mt[5];
+  const int rows = s.n * a.r - qt * TQ;
+  if ((int)blockIdx.y * RW >= rows) return;
   const int tid = threadIdx.x;
-  if (tid == 0) stop = 0x7FFFFFFF;
+  if (tid == 0) stop = a.workers - 1;
   __syncthreads();
   for (int c = w + 1; c < a.workers; c += 256) {
     if (c + tid < a.workers && a.meta[(int64_t)(c + tid) * kMetaInts + 1]) atomicMin(&stop, c + tid);
     __syncthreads();
     const int found = stop;
     __syncthreads();
-    if (found != 0x7FFFFFFF) break;
+    if (found < c + 256) break;
   }
-  const int last = stop < a.workers ? stop : a.workers - 1;
+  const int last = stop;
   const int64_t slot = TQ * (D + 2);
-  const int pg = tid / QD, qd = tid % QD;
+  const int rw = tid / (QD * PG), pg = tid / QD % PG, qd = tid % QD;
+  const int ri = blockIdx.y * RW + rw;      // row within the tile
   float M = kNegInf, L = 0.0f;
   float4 acc = make_float4(0, 0, 0, 0);
-  if (pg < PG) {
+  if (rw < RW && ri < rows && ri < TQ) {
 #pragma unroll 4
     for (int c = w + pg; c <= last; c += PG) {
       const float* p = a.part + (2 * (int64_t)c + (c == w ? 1 : 0)) * slot;
       // a worker in between that had no tile wrote nothing
       const bool valid = c == w || a.meta[(int64_t)c * kMetaInts];
       if (!valid) continue;
-      const float mc = p[TQ * D + blockIdx.y], lc = p[TQ * D + TQ + blockIdx.y];
-      const float4 v = *(const float4*)(p + blockIdx.y * D + qd * 4);
+      const float mc = p[TQ * D + ri], lc = p[TQ * D + TQ + ri];
+      const float4 v = *(const float4*)(p + ri * D + qd * 4);
       const float mn = fmaxf(M, mc);
       const float f0 = M == kNegInf ? 0.0f : exp2_hw(M - mn);
+      // NaN statistics (a non-finite query) come with reference -inf: kept
       const float f1 = mc == kNegInf ? 0.0f : exp2_hw(mc - mn);
       M = mn;
       L = L * f0 + lc * f1;
@@ -760,60 +762,62 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
       acc.z = acc.z * f0 + v.z * f1;
       acc.w = acc.w * f0 + v.w * f1;
     }
-    so[pg][qd] = acc;
-    if (qd == 0) { sm[pg] = M; sl[pg] = L; }
+    if constexpr (PG > 1) {
+      so[rw][pg][qd] = acc;
+      if (qd == 0) { sm[rw][pg] = M; sl[rw][pg] = L; }
+    }
   }
-  __syncthreads();
-  if (tid >= QD) return;
-  M = kNegInf;
+  if constexpr (PG > 1) {
+    __syncthreads();
+    if (pg != 0) return;
+  }
+  if (rw >= RW || ri >= rows || ri >= TQ) return;
+  if constexpr (PG > 1) {
+    M = kNegInf;
 #pragma unroll
-  for (int i = 0; i < PG; ++i) M = fmaxf(M, sm[i]);
-  L = 0.0f;
-  acc = make_float4(0, 0, 0, 0);
+    for (int i = 0; i < PG; ++i) M = fmaxf(M, sm[rw][i]);
+    L = 0.0f;
+    acc = make_float4(0, 0, 0, 0);
 #pragma unroll
-  for (int i = 0; i < PG; ++i) {
-    const float f = sm[i] == kNegInf ? 0.0f : exp2_hw(sm[i] - M);
-    const float4 v = so[i][tid];
-    L += f * sl[i];
-    acc.x += f * v.x;
-    acc.y += f * v.y;
-    acc.z += f * v.z;
-    acc.w += f * v.w;
+    for (int i = 0; i < PG; ++i) {
+      const float f = sm[rw][i] == kNegInf ? 0.0f : exp2_hw(sm[rw][i] - M);
+      const float4 v = so[rw][i][qd];
+      L += f * sl[rw][i];
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
+    }
   }
   using R = Rows<D, 1, 1, true>;
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  const int row = qt * TQ + ri;
   const int64_t orow = (int64_t)(s.q0 + row / a.r) * a.hq + h * a.r + row % a.r;
-  *(uint2*)(a.out + orow * D + tid * 4) =
+  *(uint2*)(a.out + orow * D + qd * 4) =
       make_uint2(R::pack_out(a.bf16, acc.x * inv, acc.y * inv), R::pack_out(a.bf16, acc.z * inv, acc.w * inv));
-  if (a.lse && tid == 0) a.lse[orow] = R::lse_of(M, L);
+  if (a.lse && qd == 0) a.lse[orow] = R::lse_of(M, L);
+}
+
+template <int D, int TQ, int PG>
+hipError_t launch_join(const Kv4Attn& a, hipStream_t s) {
+  constexpr int RW = 256 / (D / 4 * PG);
+  hipLaunchKernelGGL((kv4_join_kernel<D, TQ, PG>), dim3(a.workers, (TQ + RW - 1) / RW), dim3(256), 0, s, a);
+  return hipGetLastError();
 }
 
 template <int D, int NG, int NQ, bool SYM>
 hipError_t launch_rows(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
-  if (!p.split) {
-    const int64_t n = (int64_t)p.grid_q * a.c.hkv * a.batch;
-    hipLaunchKernelGGL((kv4_rows_kernel<D, NG, NQ, SYM, false>), dim3((unsigned)n), dim3(kWaves * 64), 0,
-                       s, a, 0);
-    return hipGetLastError();
-  }
-  hipLaunchKernelGGL((kv4_rows_kernel<D, NG, NQ, SYM, true>), dim3(a.workers), dim3(kWaves * 64), 0, s, a,
+  const int64_t n = p.split ? a.workers : (int64_t)p.grid_q * a.c.hkv * a.batch;
+  hipLaunchKernelGGL((kv4_rows_kernel<D, NG, NQ, SYM>), dim3((unsigned)n), dim3(kWaves * 64), 0, s, a,
                      (int)(p.grid_q <= 4));
   if (hipError_t e = hipGetLastError()) return e;
-  hipLaunchKernelGGL((kv4_join_kernel<D, 16 * NQ>), dim3(a.workers, 16 * NQ), dim3(256), 0, s, a);
-  return hipGetLastError();
-}
-
-template <int D, int NG, bool SYM>
-hipError_t launch_rows_nq(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
-  if (p.nq == 1) return launch_rows<D, NG, 1, SYM>(a, p, s);
-  if (p.nq == 2) return launch_rows<D, NG, 2, SYM>(a, p, s);
-  if constexpr (D <= 128) return launch_rows<D, NG, 4, SYM>(a, p, s);
-  return hipErrorInvalidValue;
+  return p.split ? launch_join<D, 16 * NQ, 256 / (D / 4)>(a, s) : hipSuccess;
 }
 
 template <int D, int NG>
-hipError_t launch_rows_sym(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
-  return a.c.sym ? launch_rows_nq<D, NG, true>(a, p, s) : launch_rows_nq<D, NG, false>(a, p, s);
+hipError_t launch_rows_any(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
+  if (p.nq == 1) return a.c.sym ? launch_rows<D, NG, 1, true>(a, p, s) : launch_rows<D, NG, 1, false>(a, p, s);
+  return a.c.sym ? launch_rows<D, NG, 2, true>(a, p, s) : launch_rows<D, NG, 2, false>(a, p, s);
 }
 
 }  // namespace kv4

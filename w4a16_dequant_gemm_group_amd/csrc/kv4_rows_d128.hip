@@ -4,9 +4,9 @@
 namespace gq {
 
 hipError_t launch_kv4_rows_128(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
-  if (a.c.ng == 4) return kv4::launch_rows_sym<128, 4>(a, p, s);
-  if (a.c.ng == 2) return kv4::launch_rows_sym<128, 2>(a, p, s);
-  if (a.c.ng == 1) return kv4::launch_rows_sym<128, 1>(a, p, s);
+  if (a.c.ng == 4) return kv4::launch_rows_any<128, 4>(a, p, s);
+  if (a.c.ng == 2) return kv4::launch_rows_any<128, 2>(a, p, s);
+  if (a.c.ng == 1) return kv4::launch_rows_any<128, 1>(a, p, s);
   return hipErrorInvalidValue;
 }
 

@@ -4,10 +4,10 @@
 namespace gq {
 
 hipError_t launch_kv4_rows_256(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
-  if (a.c.ng == 8) return kv4::launch_rows_sym<256, 8>(a, p, s);
-  if (a.c.ng == 4) return kv4::launch_rows_sym<256, 4>(a, p, s);
-  if (a.c.ng == 2) return kv4::launch_rows_sym<256, 2>(a, p, s);
-  if (a.c.ng == 1) return kv4::launch_rows_sym<256, 1>(a, p, s);
+  if (a.c.ng == 8) return kv4::launch_rows_any<256, 8>(a, p, s);
+  if (a.c.ng == 4) return kv4::launch_rows_any<256, 4>(a, p, s);
+  if (a.c.ng == 2) return kv4::launch_rows_any<256, 2>(a, p, s);
+  if (a.c.ng == 1) return kv4::launch_rows_any<256, 1>(a, p, s);
   return hipErrorInvalidValue;
 }
 

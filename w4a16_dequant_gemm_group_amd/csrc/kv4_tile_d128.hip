@@ -1,0 +1,13 @@
+// Many-row attention over the 4-bit cache, head_dim 128.
+#include "kv4_tile.h"
+
+namespace gq {
+
+hipError_t launch_kv4_tile_128(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
+  if (a.c.ng == 4) return kv4::launch_tile<128, 4>(a, p, s);
+  if (a.c.ng == 2) return kv4::launch_tile<128, 2>(a, p, s);
+  if (a.c.ng == 1) return kv4::launch_tile<128, 1>(a, p, s);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace gq

@@ -1,0 +1,12 @@
+// Many-row attention over the 4-bit cache, head_dim 64.
+#include "kv4_tile.h"
+
+namespace gq {
+
+hipError_t launch_kv4_tile_64(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
+  if (a.c.ng == 2) return kv4::launch_tile<64, 2>(a, p, s);
+  if (a.c.ng == 1) return kv4::launch_tile<64, 1>(a, p, s);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace gq
