@@ -71,9 +71,15 @@ struct Kv4Attn {
   // the split over workgroups
   int32_t workers;                   // workgroups of a split launch
   int32_t grid_q;                    // row tiles in an unsplit launch's grid
-  int32_t* meta;                     // [workers][8] which segments were left open
+  int32_t* meta;                     // [workers][8] which row tiles were left open
   float* part;                       // [2 * workers][rows][D + 2] partial results
 };
+
+// Waves per SIMD of the rows kernel: as many as its registers allow without
+// spilling (d channels in ng groups, nq tiles of 16 rows).
+constexpr int kv4_rows_waves(int d, int ng, int nq) {
+  return d * nq > 256 ? 1 : d > 128 || nq > 1 || ng > 2 ? 2 : 3;
+}
 
 struct Kv4Plan {
   bool tile;           // the kernel for many rows; else the rows kernel
@@ -81,6 +87,7 @@ struct Kv4Plan {
   int nq;              // rows kernel: 16-row query tiles per workgroup
   int workers;         // workgroups when split
   int grid_q;          // row tiles per (sequence, head) when not split
+  int tile_rows;       // rows of a row tile, as far as max_q_len tells
   size_t ws_bytes;
 };
 

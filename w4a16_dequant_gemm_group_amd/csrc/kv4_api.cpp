@@ -88,11 +88,13 @@ Kv4Plan kv4_plan(const gq_kv4_attention_args& a) {
   const int tq = p.tile ? (d > 128 ? 128 : 256) : 16 * p.nq;    // rows of a row tile
   const int keys = p.tile ? 64 : 128;                           // keys of a tile of the split
   p.grid_q = (int)((rows + tq - 1) / tq);
+  p.tile_rows = (int)std::min<int64_t>(rows, tq);
   const int64_t segs = a.batch * a.layout.kv_heads * p.grid_q;
   const int64_t tiles = segs * std::max<int64_t>(1, (a.max_kv_len + keys - 1) / keys);
   p.split = p.tile || a.max_kv_len > 1024 || segs > INT32_MAX;
   if (p.split) {
-    const int64_t want = (int64_t)num_cus() * (p.tile ? 1 : (p.nq == 1 ? 4 : 2));
+    // as many workgroups (a wave on each SIMD) as run at once
+    const int64_t want = (int64_t)num_cus() * (p.tile ? 1 : kv4_rows_waves(d, d / a.layout.group_size, p.nq));
     p.workers = (int)std::max<int64_t>(8, std::min(tiles, want) & ~(int64_t)7);
     p.ws_bytes = (size_t)p.workers * 32 + (size_t)p.workers * 2 * tq * (d + 2) * sizeof(float);
   }

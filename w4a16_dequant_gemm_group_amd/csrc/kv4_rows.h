@@ -18,6 +18,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;            // waves per workgroup
 constexpr int kUnit = 32;            // tokens a wave takes at once (two sub-blocks)
@@ -188,45 +189,51 @@ __device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t (&w)[N]) 
   }
 }
 
-// Everything a wave reads of one sub-block: codes, the scales of this lane's
-// result tokens 4 kg .. 4 kg + 3 (pairs of halfs), the key zero points of its
-// operand token m, the value zero points of its operand tokens 4 kg ...
+// What a wave reads of one sub-block.  Keys: codes of its operand token m, the
+// scales of its result tokens 4 kg .. 4 kg + 3 (pairs of halfs), the zero points
+// of token m.  Values: codes, scales and zero points of its operand tokens 4 kg ...
 template <int D, int NG, bool SYM>
-struct Block {
+struct KeyBlock {
   static constexpr int NS = D / 32;
-  uint32_t k[NS], v[NS];
-  uint32_t ks[NG][2], vs[NG][2];
-  uint32_t kz[(NG + 1) / 2];
-  uint32_t vz[SYM ? 1 : NG][2];
+  uint32_t c[NS], s[NG][2], z[(NG + 1) / 2];
 
-  __device__ __forceinline__ void load(const uint8_t* blk, uint32_t meta, int m, int kg) {
-    load_dwords<NS>(blk + m * (D / 2) + kg * (4 * NS), k);
+  __device__ __forceinline__ void load(const uint8_t* blk, uint32_t m, uint32_t kg) {
+    load_dwords<NS>(blk + m * (D / 2) + kg * (4 * NS), c);
     const uint8_t* p = blk + 8 * D;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) load_dwords<2>(p + g * 32 + kg * 8, ks[g]);
-    const uint8_t* w = p + meta;
-    load_dwords<NS>(w + kg * (64 * NS) + m * (4 * NS), v);
-    const uint8_t* pv = w + 8 * D;
-    if constexpr (SYM) {
-#pragma unroll
-      for (int g = 0; g < NG; ++g) load_dwords<2>(pv + g * 32 + kg * 8, vs[g]);
-    } else {
-      const uint8_t* z = p + 32 * NG + m * (2 * NG);
+    for (int g = 0; g < NG; ++g) load_dwords<2>(p + g * 32 + kg * 8, s[g]);
+    if constexpr (!SYM) {
+      const uint8_t* zp = p + 32 * NG + m * (2 * NG);
       if constexpr (NG % 2 == 0) {
-        load_dwords<NG / 2>(z, kz);
+        load_dwords<NG / 2>(zp, z);
       } else {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const uint32_t h = ((const uint16_t*)z)[g];
-          kz[g / 2] = g & 1 ? kz[g / 2] | h << 16 : h;
+          const uint32_t h = ((const uint16_t*)zp)[g];
+          z[g / 2] = g & 1 ? z[g / 2] | h << 16 : h;
         }
       }
+    }
+  }
+};
+
+template <int D, int NG, bool SYM>
+struct ValueBlock {
+  static constexpr int NS = D / 32;
+  uint32_t c[NS], s[NG][2], z[SYM ? 1 : NG][2];
+
+  __device__ __forceinline__ void load(const uint8_t* w, uint32_t m, uint32_t kg) {
+    load_dwords<NS>(w + kg * (64 * NS) + m * (4 * NS), c);
+    const uint8_t* pv = w + 8 * D;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
+    for (int g = 0; g < NG; ++g) {
+      if constexpr (SYM) {
+        load_dwords<2>(pv + g * 32 + kg * 8, s[g]);
+      } else {
         uint32_t t[4];
         load_dwords<4>(pv + g * 64 + kg * 16, t);
-        vs[g][0] = t[0]; vs[g][1] = t[1];
-        vz[g][0] = t[2]; vz[g][1] = t[3];
+        s[g][0] = t[0]; s[g][1] = t[1];
+        z[g][0] = t[2]; z[g][1] = t[3];
       }
     }
   }
@@ -248,18 +255,25 @@ __device__ __forceinline__ uint32_t byte_pair(const uint32_t (&w)[N], int i, int
   return __builtin_amdgcn_perm(w[j >> 2], w[i >> 2], sel);
 }
 
-// A pair of codes, masked in place, to fp16 c - z.  lo: nibbles at bits 0..3
-// of each half, where 0x6400 | c is 1024 + c; hi: at bits 4..7, where it is
-// 1024 + 16 c.  n: -(1024 + z), or -(64 + z).  Every step is exact.
-__device__ __forceinline__ uint32_t minus_zero_lo(uint32_t w, f16x2 n) {
-  const f16x2 v = __builtin_bit_cast(f16x2, (w & 0x000F000Fu) | 0x64006400u);
-  return __builtin_bit_cast(uint32_t, v + n);
-}
-__device__ __forceinline__ uint32_t minus_zero_hi(uint32_t w, f16x2 n) {
-  const f16x2 v = __builtin_bit_cast(f16x2, (w & 0x00F000F0u) | 0x64006400u);
-  const f16x2 s = {(_Float16)0.0625f, (_Float16)0.0625f};
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(v, s, n));
-}
+// A pair of codes, masked in place, to fp16 c - z.  lo: nibbles at bits 0..3 of
+// each half, where 0x6400 | c is 1024 + c; hi: at bits 4..7, where 0x5400 | c is
+// 64 + c.  n: -(1024 + z), or -(64 + z).  Every step is exact.
+// The masks live in vector registers and the exponents in scalar ones: an
+// instruction takes one scalar and no literal besides, so mask and exponent
+// as constants would make two of each and-or.
+struct Nibbles {
+  uint32_t mlo, mhi, elo, ehi;
+  __device__ __forceinline__ Nibbles() : mlo(0x000F000Fu), mhi(0x00F000F0u), elo(0x64006400u), ehi(0x54005400u) {
+    asm("" : "+v"(mlo), "+v"(mhi));
+    asm("" : "+s"(elo), "+s"(ehi));
+  }
+  __device__ __forceinline__ uint32_t lo(uint32_t w, f16x2 n) const {
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, (w & mlo) | elo) + n);
+  }
+  __device__ __forceinline__ uint32_t hi(uint32_t w, f16x2 n) const {
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, (w & mhi) | ehi) + n);
+  }
+};
 
 __device__ __forceinline__ f16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   const u32x4 v = {a, b, c, d};
@@ -280,7 +294,7 @@ __device__ __forceinline__ f16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32
 // near 2^14: exact for fp16 and bf16 elements down to 2^-29 of the largest.
 // So the scores are exact up to fp32 sums: s = sum_g S_g ((codes - z) . q).
 // P' = p S_V goes to the matrix cores as fp16, one operand per group; it is
-// rounded once (2^-11).  The reference that the exponentials subtract is the
+// rounded once (2^-11; `rest` below keeps what that leaves where it would show).  The reference that the exponentials subtract is the
 // running maximum of score + log2 S_V, so that P' itself, not p, is what lies
 // in fp16's range, whatever the scales are.
 template <int D, int NG, int NQ, bool SYM>
@@ -294,12 +308,20 @@ struct Rows {
   float A[NQ];                      // score factor
   f32x4 o[NQ][2 * NS];
   float mref[NQ], l[NQ];
+  // fp16 outputs of at most 8 rows: lanes 8 .. 15 of a tile hold the same rows
+  // once more and carry what the rounding of p S_V to fp16 left, so that it
+  // costs an fp16 result no accuracy.  The columns would be idle otherwise.
+  bool rest;
+  Nibbles nib;
+
+  __device__ __forceinline__ int row_of_lane() const { return threadIdx.x & (rest ? 7 : 15); }
 
   __device__ __forceinline__ void load_q(const Kv4Attn& a, const Seq& s, int h, int qt, int m, int kg) {
     const int rows = s.n * a.r;
+    rest = NQ == 1 && !a.bf16 && rows <= 8;
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) {
-      const int row = qt * TQ + nq * 16 + m;
+      const int row = qt * TQ + nq * 16 + row_of_lane();
       float x[NS][8];
       float mx = 0.0f;
       const bool ok = row < rows;
@@ -341,110 +363,113 @@ struct Rows {
     }
   }
 
-  // 32 keys from position u on; `masked` where some row does not see all of
-  // them.  ok0 / ok1: the sub-blocks that exist.
-  __device__ __forceinline__ void unit(const Kv4Attn& a, const Seq& s, const Span& sp, int qt, int u,
-                                       bool masked, bool ok0, bool ok1, Block<D, NG, SYM> (&blk)[2], int m,
-                                       int kg) {
-    if (masked) {
-      // keys that no row of the tile sees: whatever their memory holds counts
-      // as value scale and zero point 0 (their scores are dropped below)
+  // x = K^ q of 32 keys, without the row's factor A.
+  __device__ __forceinline__ void scores(const KeyBlock<D, NG, SYM> (&kb)[2], float (&x)[NQ][2][4]) const {
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        uint32_t live[2];
+        f32x4 acc[NQ];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int pos = u + 16 * t + 4 * kg + 2 * i;
-          const bool ok = t ? ok1 : ok0;
-          live[i] = (ok && pos >= sp.lo && pos < sp.hi ? 0xFFFFu : 0u) |
-                    (ok && pos + 1 >= sp.lo && pos + 1 < sp.hi ? 0xFFFF0000u : 0u);
-        }
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            blk[t].vs[g][i] &= live[i];
-            if constexpr (!SYM) blk[t].vz[g][i] &= live[i];
-          }
-      }
-    }
-    float x[NQ][2][4];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      f32x4 acc[NQ][2];
-#pragma unroll
-      for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) acc[nq][t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
+        for (int nq = 0; nq < NQ; ++nq) acc[nq] = f32x4{0, 0, 0, 0};
         f16x2 z2 = {(_Float16)8.0f, (_Float16)8.0f};
         if constexpr (!SYM) {
-          const f16x2 zp = __builtin_bit_cast(f16x2, blk[t].kz[g / 2]);
-          z2 = f16x2{zp[g & 1], zp[g & 1]};
+          const _Float16 z = __builtin_bit_cast(_Float16, (uint16_t)(kb[t].z[g / 2] >> (16 * (g & 1))));
+          z2 = f16x2{z, z};
         }
         const f16x2 n1 = (_Float16)-1024.0f - z2, n2 = (_Float16)-64.0f - z2;
 #pragma unroll
         for (int st = g * SPG; st < (g + 1) * SPG; ++st) {
-          const uint32_t d = blk[t].k[st], e = d >> 8;
-          const f16x8 w = frag(minus_zero_lo(d, n1), minus_zero_hi(d, n2), minus_zero_lo(e, n1),
-                               minus_zero_hi(e, n2));
+          const uint32_t d = kb[t].c[st], e = d >> 8;
+          const f16x8 w = frag(nib.lo(d, n1), nib.hi(d, n2), nib.lo(e, n1), nib.hi(e, n2));
 #pragma unroll
           for (int nq = 0; nq < NQ; ++nq)
-            acc[nq][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, q[nq][st], acc[nq][t], 0, 0, 0);
+            acc[nq] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, q[nq][st], acc[nq], 0, 0, 0);
         }
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float S = half_of(blk[t].ks[g], i);
+          const float S = half_of(kb[t].s[g], i);
 #pragma unroll
           for (int nq = 0; nq < NQ; ++nq)
-            x[nq][t][i] = g == 0 ? S * acc[nq][t][i] : __builtin_fmaf(S, acc[nq][t][i], x[nq][t][i]);
+            x[nq][t][i] = __builtin_fmaf(S, acc[nq][i], g == 0 ? 0.0f : x[nq][t][i]);
+        }
+      }
+  }
+
+  // Keys that no row of the tile sees: whatever their memory holds counts as
+  // value scale and zero point 0 (their scores are dropped in `weights`).
+  static __device__ __forceinline__ void clear_unseen(const Span& sp, int u, bool ok0, bool ok1,
+                                                      ValueBlock<D, NG, SYM> (&vb)[2], int kg) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      uint32_t live[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int pos = u + 16 * t + 4 * kg + 2 * i;
+        const bool ok = t ? ok1 : ok0;
+        live[i] = (ok && pos >= sp.lo && pos < sp.hi ? 0xFFFFu : 0u) |
+                  (ok && pos + 1 >= sp.lo && pos + 1 < sp.hi ? 0xFFFF0000u : 0u);
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          vb[t].s[g][i] &= live[i];
+          if constexpr (!SYM) vb[t].z[g][i] &= live[i];
         }
     }
-    // log2 of the largest value scale of each key, within a tenth
+  }
+
+  // Scores to weights p = 2^(x A - mref); `masked` where some row does not see
+  // all 32 keys from position u on.  ok0 / ok1: the sub-blocks that exist.
+  __device__ __forceinline__ void weights(const Kv4Attn& a, const Seq& s, int qt, int u, bool masked, bool ok0,
+                                          bool ok1, const ValueBlock<D, NG, SYM> (&vb)[2], float (&x)[NQ][2][4],
+                                          int kg) {
+    // log2 of the largest value scale of each key, within a tenth: the bits of
+    // a non-negative half count powers of two in steps of 1 / 1024.  As the low
+    // half of 2^23 + bits they are a float at once.
     float lv[2][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t b = 0;
+      for (int i = 0; i < 2; ++i) {
+        u16x2 b = __builtin_bit_cast(u16x2, vb[t].s[0][i]);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const uint32_t c = i & 1 ? blk[t].vs[g][i >> 1] >> 16 : blk[t].vs[g][i >> 1] & 0xFFFFu;
-          b = c > b ? c : b;
-        }
-        lv[t][i] = __builtin_fmaf((float)b, 1.0f / 1024.0f, -15.0f);
+        for (int g = 1; g < NG; ++g) b = __builtin_elementwise_max(b, __builtin_bit_cast(u16x2, vb[t].s[g][i]));
+        const uint32_t w = __builtin_bit_cast(uint32_t, b);
+        const float f0 = __uint_as_float(__builtin_amdgcn_perm(0x4B000000u, w, 0x07060100u));
+        const float f1 = __uint_as_float(__builtin_amdgcn_perm(0x4B000000u, w, 0x07060302u));
+        lv[t][2 * i] = __builtin_fmaf(f0, 1.0f / 1024.0f, -8207.0f);
+        lv[t][2 * i + 1] = __builtin_fmaf(f1, 1.0f / 1024.0f, -8207.0f);
       }
-    float p[NQ][2][4];
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) {
-      float y[2][4], top = kNegInf;
+      float y[2][4];
       uint32_t hide = 0;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[t][i] = __builtin_fmaf(x[nq][t][i], A[nq], lv[t][i]);
       if (masked) {
-        const int tok = (qt * TQ + nq * 16 + m) / a.r;
+        const int tok = (qt * TQ + nq * 16 + row_of_lane()) / a.r;
         const int pos = s.kv - s.n + tok;
-        const int last = a.causal ? pos : 0x7FFFFFFF;
-        const int first = a.window > 0 ? pos - a.window + 1 : -0x7FFFFFFF;
+        const int last = a.causal && pos < s.kv - 1 ? pos : s.kv - 1;
+        const int first = a.window > 0 ? pos - a.window + 1 : 0;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = u + 16 * t + 4 * kg + i;
-            const bool seen = (t ? ok1 : ok0) && j < s.kv && j <= last && j >= first;
+            const bool seen = (t ? ok1 : ok0) && j <= last && j >= first;
             hide |= seen ? 0u : 1u << (4 * t + i);
+            y[t][i] = seen ? y[t][i] : kNegInf;
           }
       }
+      float top = kNegInf;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[t][i] = __builtin_fmaf(x[nq][t][i], A[nq], lv[t][i]);
-          if (masked && (hide >> (4 * t + i) & 1u)) y[t][i] = kNegInf;
-          top = fmaxf(top, y[t][i]);
-        }
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, y[t][i]);
       if (__any(top > mref[nq] + kSlack)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
@@ -458,13 +483,22 @@ struct Rows {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float e = exp2_hw(__builtin_fmaf(x[nq][t][i], A[nq], -mref[nq]));
-          if (masked && (hide >> (4 * t + i) & 1u)) e = 0.0f;
-          p[nq][t][i] = e;
-          l[nq] += e;
-        }
+        for (int i = 0; i < 4; ++i) x[nq][t][i] = exp2_hw(__builtin_fmaf(x[nq][t][i], A[nq], -mref[nq]));
+      if (masked) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[nq][t][i] = hide >> (4 * t + i) & 1u ? 0.0f : x[nq][t][i];
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[nq] += x[nq][t][i];
     }
+  }
+
+  // o += V^^T p
+  __device__ __forceinline__ void values(const ValueBlock<D, NG, SYM> (&vb)[2], const float (&p)[NQ][2][4]) {
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       f16x8 pw[NQ];
@@ -472,15 +506,29 @@ struct Rows {
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float S = half_of(blk[t].vs[g], i);
+          const float S = half_of(vb[t].s[g], i);
 #pragma unroll
-          for (int nq = 0; nq < NQ; ++nq) pw[nq][4 * t + i] = (_Float16)(p[nq][t][i] * S);
+          for (int nq = 0; nq < NQ; ++nq) pw[nq][4 * t + i] = (_Float16)__builtin_fmaf(p[nq][t][i], S, 0.0f);
         }
+      if (rest) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float S = half_of(vb[t].s[g], i);
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq) {
+              const _Float16 h = pw[nq][4 * t + i];
+              const _Float16 d = (_Float16)__builtin_fmaf(p[nq][t][i], S, -(float)h);
+              pw[nq][4 * t + i] = (threadIdx.x & 8) != 0 ? d : h;
+            }
+          }
+      }
       f16x2 n1[4], n2[4];   // by token pair
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f16x2 z = SYM ? f16x2{(_Float16)8.0f, (_Float16)8.0f}
-                            : __builtin_bit_cast(f16x2, blk[i >> 1].vz[SYM ? 0 : g][i & 1]);
+                            : __builtin_bit_cast(f16x2, vb[i >> 1].z[SYM ? 0 : g][i & 1]);
         n1[i] = (_Float16)-1024.0f - z;
         n2[i] = (_Float16)-64.0f - z;
       }
@@ -489,13 +537,11 @@ struct Rows {
         uint32_t w[4];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          w[2 * t] = byte_pair<NS>(blk[t].v, b, NS + b);
-          w[2 * t + 1] = byte_pair<NS>(blk[t].v, 2 * NS + b, 3 * NS + b);
+          w[2 * t] = byte_pair<NS>(vb[t].c, b, NS + b);
+          w[2 * t + 1] = byte_pair<NS>(vb[t].c, 2 * NS + b, 3 * NS + b);
         }
-        const f16x8 ev = frag(minus_zero_lo(w[0], n1[0]), minus_zero_lo(w[1], n1[1]),
-                              minus_zero_lo(w[2], n1[2]), minus_zero_lo(w[3], n1[3]));
-        const f16x8 od = frag(minus_zero_hi(w[0], n2[0]), minus_zero_hi(w[1], n2[1]),
-                              minus_zero_hi(w[2], n2[2]), minus_zero_hi(w[3], n2[3]));
+        const f16x8 ev = frag(nib.lo(w[0], n1[0]), nib.lo(w[1], n1[1]), nib.lo(w[2], n1[2]), nib.lo(w[3], n1[3]));
+        const f16x8 od = frag(nib.hi(w[0], n2[0]), nib.hi(w[1], n2[1]), nib.hi(w[2], n2[2]), nib.hi(w[3], n2[3]));
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) {
           o[nq][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ev, pw[nq], o[nq][2 * b], 0, 0, 0);
@@ -505,38 +551,64 @@ struct Rows {
     }
   }
 
-  // Key tiles j0 .. j1 - 1 of the span.
+  // Key tiles j0 .. j1 - 1 of the span.  The next unit's keys are fetched once
+  // the present ones are multiplied, its values once the present ones are: no
+  // register more than one unit needs, and each load has the other half of the
+  // work to arrive.  Page numbers are fetched a unit earlier still.
   __device__ __forceinline__ void keys(const Kv4Attn& a, const Seq& s, const Span& sp, int64_t b, int h,
                                        int qt, int j0, int j1, int wave, int m, int kg) {
     const int32_t* row = a.table + b * a.table_pages;
     const int ps = a.c.page_shift;
-    for (int j = j0; j < j1; ++j) {
-      const int u = (sp.t0 + j) * kTile + wave * kUnit;
-      if (u >= sp.hi || u + kUnit <= sp.lo) continue;
-      Block<D, NG, SYM> blk[2];
-      bool ok[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int pos = u + 16 * t;
-        int64_t page = 0;
-        ok[t] = false;
-        if (pos < sp.hi && pos + 16 > sp.lo) {
-          page = row[pos >> ps];
-          ok[t] = page >= 0 && page < a.c.n_pages;
-          page = ok[t] ? page : 0;
-        }
-        blk[t].load(a.c.cache + kv4_block_offset(a.c, page, h, ok[t] ? pos & ((1 << ps) - 1) : 0),
-                    a.c.meta, m, kg);
-      }
+    int u = (sp.t0 + j0) * kTile + wave * kUnit;
+    int end = (sp.t0 + j1) * kTile;
+    end = end < sp.hi ? end : sp.hi;
+    if (u + kUnit <= sp.lo) u += kTile;      // only the first tile can hold keys before the span
+    if (u >= end) return;
+    struct Place { const uint8_t* p; bool ok; };
+    auto page_of = [&](int pos) -> int32_t {
+      return pos < sp.hi && pos + 16 > sp.lo ? row[pos >> ps] : -1;
+    };
+    auto place = [&](int32_t page, int pos) {
+      Place w;
+      w.ok = page >= 0 && page < a.c.n_pages;
+      w.p = a.c.cache + kv4_block_offset(a.c, w.ok ? page : 0, h, w.ok ? pos & ((1 << ps) - 1) : 0);
+      return w;
+    };
+    const uint32_t to_v = 8 * D + a.c.meta;
+    KeyBlock<D, NG, SYM> kb[2];
+    ValueBlock<D, NG, SYM> vb[2];
+    Place w0 = place(page_of(u), u), w1 = place(page_of(u + 16), u + 16);
+    kb[0].load(w0.p, m, kg);
+    kb[1].load(w1.p, m, kg);
+    vb[0].load(w0.p + to_v, m, kg);
+    vb[1].load(w1.p + to_v, m, kg);
+    int32_t pg0 = page_of(u + kTile), pg1 = page_of(u + kTile + 16);
+    for (;;) {
+      const int un = u + kTile;
+      const bool more = un < end;
       // every row sees every key: all before the first query's position and
       // inside the last one's window
-      bool full = ok[0] && ok[1] && u + kUnit <= s.kv;
+      bool full = w0.ok && w1.ok && u + kUnit <= s.kv;
       if (a.causal) full = full && u + kUnit - 1 <= sp.p0;
       if (a.window > 0) full = full && u > sp.p1 - a.window;
-      if (full)
-        unit(a, s, sp, qt, u, false, true, true, blk, m, kg);
-      else
-        unit(a, s, sp, qt, u, true, ok[0], ok[1], blk, m, kg);
+      const bool ok0 = w0.ok, ok1 = w1.ok;
+      float x[NQ][2][4];
+      scores(kb, x);
+      if (more) {
+        w0 = place(pg0, un);
+        w1 = place(pg1, un + 16);
+        kb[0].load(w0.p, m, kg);
+        kb[1].load(w1.p, m, kg);
+        pg0 = page_of(un + kTile);
+        pg1 = page_of(un + kTile + 16);
+      }
+      if (!full) clear_unseen(sp, u, ok0, ok1, vb, kg);
+      weights(a, s, qt, u, !full, ok0, ok1, vb, x, kg);
+      values(vb, x);
+      if (!more) break;
+      vb[0].load(w0.p + to_v, m, kg);
+      vb[1].load(w1.p + to_v, m, kg);
+      u = un;
     }
   }
 
@@ -548,6 +620,12 @@ struct Rows {
     float* so = smem;
     float* sm = smem + kWaves * 16 * kSmemRow;
     float* sl = sm + kWaves * 16;
+    if (rest) {
+#pragma unroll
+      for (int i = 0; i < 2 * NS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[0][i][e] += __shfl_xor(o[0][i][e], 8);
+    }
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) {
       float lt = l[nq];
@@ -637,8 +715,25 @@ __device__ __forceinline__ int worker_of(int bid, int workers) {
   return workers % 8 == 0 ? (bid & 7) * (workers >> 3) + (bid >> 3) : bid;
 }
 
+// The worker whose share of the `total` tiles (total * w / workers ..) holds tile i.
+__device__ __forceinline__ int worker_with(int64_t i, int64_t total, int workers) {
+  return (int)(((i + 1) * workers + total - 1) / total) - 1;
+}
+
+// What the join has to know of worker w: the row tile that it left open, if
+// any, and the last of the workers after it that hold the rest of that tile.
+__device__ __forceinline__ void leave_meta(const Kv4Attn& a, int w, int last, const Cursor& cur, int64_t total) {
+  int32_t* mt = a.meta + (int64_t)w * kMetaInts;
+  mt[0] = last;
+  mt[1] = (int32_t)cur.b;
+  mt[2] = cur.h;
+  mt[3] = cur.qt;
+  // fewer tiles than workers: some had none
+  mt[4] = total < a.workers ? (int32_t)total : a.workers;
+}
+
 template <int D, int NG, int NQ, bool SYM>
-__global__ __launch_bounds__(kWaves * 64, NQ <= 2 && D * NQ <= 256 ? 2 : 1) void kv4_rows_kernel(Kv4Attn a,
+__global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NG, NQ)) void kv4_rows_kernel(Kv4Attn a,
                                                                                              int few) {
   using R = Rows<D, NG, NQ, SYM>;
   __shared__ __attribute__((aligned(16))) float smem[R::kSmemFloats];
@@ -648,11 +743,11 @@ __global__ __launch_bounds__(kWaves * 64, NQ <= 2 && D * NQ <= 256 ? 2 : 1) void
   R st;
   const bool split = a.workers > 0;
   int w = 0;
-  int64_t at = 0, end = 0;
+  int64_t at = 0, end = 0, total = 0;
   Cursor cur{0, 0, 0, 0};
   if (split) {
     w = worker_of(blockIdx.x, a.workers);
-    const int64_t total = all_tiles<R::TQ, kTile>(a, lane, few != 0, -1, nullptr);
+    total = all_tiles<R::TQ, kTile>(a, lane, few != 0, -1, nullptr);
     at = total * w / a.workers;
     end = total * (w + 1) / a.workers;
     if (at < end) all_tiles<R::TQ, kTile>(a, lane, few != 0, at, &cur);
@@ -663,7 +758,7 @@ __global__ __launch_bounds__(kWaves * 64, NQ <= 2 && D * NQ <= 256 ? 2 : 1) void
     cur.h = (int)(id / a.grid_q % a.c.hkv);
     cur.b = id / ((int64_t)a.grid_q * a.c.hkv);
   }
-  int32_t head_valid = 0, head_ends = 0, tail_valid = 0;
+  int last = -1;
   Seq s = get_seq(a, cur.b);
   int nqt = (s.n * a.r + R::TQ - 1) / R::TQ;
   while (split ? at < end : cur.qt < nqt) {
@@ -677,7 +772,7 @@ __global__ __launch_bounds__(kWaves * 64, NQ <= 2 && D * NQ <= 256 ? 2 : 1) void
     float* part = nullptr;
     if (!(starts && ends)) {
       part = a.part + ((int64_t)2 * w + (starts ? 1 : 0)) * (R::TQ * (D + 2));
-      if (starts) { tail_valid = 1; } else { head_valid = 1; head_ends = ends; }
+      if (starts) last = worker_with(at + sp.cnt - 1, total, a.workers);
     }
     st.finish(a, s, cur.h, cur.qt, part, smem, wave, m, kg);
     if (!split) {
@@ -697,111 +792,96 @@ __global__ __launch_bounds__(kWaves * 64, NQ <= 2 && D * NQ <= 256 ? 2 : 1) void
       }
     }
   }
-  if (split && threadIdx.x == 0) {
-    int32_t* mt = a.meta + (int64_t)w * kMetaInts;
-    mt[0] = head_valid;
-    mt[1] = head_ends;
-    mt[2] = tail_valid;
-    mt[3] = (int32_t)cur.b;
-    mt[4] = cur.h;
-    mt[5] = cur.qt;
-  }
+  if (split && threadIdx.x == 0) leave_meta(a, w, last, cur, total);
 }
 
 // Joins the partial results of the row tiles that were split.  Worker w left
-// its last row tile open (tail): the workers after it hold the rest, up to the
-// one that ended it.  One workgroup per worker and RW rows: D / 4 threads hold
-// a row, PG such sets take every PG-th partial of it (many partials of few
-// rows for single tokens, few of many rows for prompts).
+// its last row tile open: the workers after it, up to `last`, hold the rest.
+// One workgroup per worker and RW rows at a time: D / 4 threads hold a row, PG
+// such sets take every PG-th partial of it (many partials of few rows for
+// single tokens, few of many rows for prompts).
 template <int D, int TQ, int PG>
 __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
   constexpr int QD = D / 4, RW = 256 / (QD * PG);
-  __shared__ int stop;
+  constexpr int64_t kSlot = TQ * (D + 2);
   __shared__ float4 so[RW][PG][QD];
   __shared__ float sm[RW][PG], sl[RW][PG];
   const int w = blockIdx.x;
   const int32_t* mt = a.meta + (int64_t)w * kMetaInts;
-  if (!mt[2]) return;
-  const Seq s = get_seq(a, mt[3]);
-  const int h = mt[4], qt = mt[5];
-  const int rows = s.n * a.r - qt * TQ;
-  if ((int)blockIdx.y * RW >= rows) return;
+  const int last = mt[0];
+  if (last < 0) return;
+  const int h = mt[2], qt = mt[3], busy = mt[4];
+  const Seq s = get_seq(a, mt[1]);
+  const int left = s.n * a.r - qt * TQ, rows = left < TQ ? left : TQ;
   const int tid = threadIdx.x;
-  if (tid == 0) stop = a.workers - 1;
-  __syncthreads();
-  for (int c = w + 1; c < a.workers; c += 256) {
-    if (c + tid < a.workers && a.meta[(int64_t)(c + tid) * kMetaInts + 1]) atomicMin(&stop, c + tid);
-    __syncthreads();
-    const int found = stop;
-    __syncthreads();
-    if (found < c + 256) break;
-  }
-  const int last = stop;
-  const int64_t slot = TQ * (D + 2);
   const int rw = tid / (QD * PG), pg = tid / QD % PG, qd = tid % QD;
-  const int ri = blockIdx.y * RW + rw;      // row within the tile
-  float M = kNegInf, L = 0.0f;
-  float4 acc = make_float4(0, 0, 0, 0);
-  if (rw < RW && ri < rows && ri < TQ) {
+  for (int r0 = blockIdx.y * RW; r0 < rows; r0 += gridDim.y * RW) {
+    const int ri = r0 + rw;      // row within the tile
+    const bool mine = rw < RW && ri < rows;
+    float M = kNegInf, L = 0.0f;
+    float4 acc = make_float4(0, 0, 0, 0);
+    if (mine) {
 #pragma unroll 4
-    for (int c = w + pg; c <= last; c += PG) {
-      const float* p = a.part + (2 * (int64_t)c + (c == w ? 1 : 0)) * slot;
-      // a worker in between that had no tile wrote nothing
-      const bool valid = c == w || a.meta[(int64_t)c * kMetaInts];
-      if (!valid) continue;
-      const float mc = p[TQ * D + ri], lc = p[TQ * D + TQ + ri];
-      const float4 v = *(const float4*)(p + ri * D + qd * 4);
-      const float mn = fmaxf(M, mc);
-      const float f0 = M == kNegInf ? 0.0f : exp2_hw(M - mn);
-      // NaN statistics (a non-finite query) come with reference -inf: kept
-      const float f1 = mc == kNegInf ? 0.0f : exp2_hw(mc - mn);
-      M = mn;
-      L = L * f0 + lc * f1;
-      acc.x = acc.x * f0 + v.x * f1;
-      acc.y = acc.y * f0 + v.y * f1;
-      acc.z = acc.z * f0 + v.z * f1;
-      acc.w = acc.w * f0 + v.w * f1;
+      for (int c = w + pg; c <= last; c += PG) {
+        // a worker in between that had no tile wrote nothing
+        if (busy < a.workers && c != w && (int64_t)busy * c / a.workers == (int64_t)busy * (c + 1) / a.workers)
+          continue;
+        const float* p = a.part + (2 * (int64_t)c + (c == w ? 1 : 0)) * kSlot;
+        const float mc = p[TQ * D + ri], lc = p[TQ * D + TQ + ri];
+        const float4 v = *(const float4*)(p + ri * D + qd * 4);
+        const float mn = fmaxf(M, mc);
+        const float f0 = M == kNegInf ? 0.0f : exp2_hw(M - mn);
+        // NaN statistics (a non-finite query) come with reference -inf: kept
+        const float f1 = mc == kNegInf ? 0.0f : exp2_hw(mc - mn);
+        M = mn;
+        L = L * f0 + lc * f1;
+        acc.x = acc.x * f0 + v.x * f1;
+        acc.y = acc.y * f0 + v.y * f1;
+        acc.z = acc.z * f0 + v.z * f1;
+        acc.w = acc.w * f0 + v.w * f1;
+      }
     }
     if constexpr (PG > 1) {
-      so[rw][pg][qd] = acc;
-      if (qd == 0) { sm[rw][pg] = M; sl[rw][pg] = L; }
+      if (mine) {
+        so[rw][pg][qd] = acc;
+        if (qd == 0) { sm[rw][pg] = M; sl[rw][pg] = L; }
+      }
+      __syncthreads();
+      if (mine && pg == 0) {
+        M = kNegInf;
+#pragma unroll
+        for (int i = 0; i < PG; ++i) M = fmaxf(M, sm[rw][i]);
+        L = 0.0f;
+        acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < PG; ++i) {
+          const float f = sm[rw][i] == kNegInf ? 0.0f : exp2_hw(sm[rw][i] - M);
+          const float4 v = so[rw][i][qd];
+          L += f * sl[rw][i];
+          acc.x += f * v.x;
+          acc.y += f * v.y;
+          acc.z += f * v.z;
+          acc.w += f * v.w;
+        }
+      }
+      __syncthreads();
+    }
+    if (mine && pg == 0) {
+      using R = Rows<D, 1, 1, true>;
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+      const int row = qt * TQ + ri;
+      const int64_t orow = (int64_t)(s.q0 + row / a.r) * a.hq + h * a.r + row % a.r;
+      *(uint2*)(a.out + orow * D + qd * 4) = make_uint2(R::pack_out(a.bf16, acc.x * inv, acc.y * inv),
+                                                        R::pack_out(a.bf16, acc.z * inv, acc.w * inv));
+      if (a.lse && qd == 0) a.lse[orow] = R::lse_of(M, L);
     }
   }
-  if constexpr (PG > 1) {
-    __syncthreads();
-    if (pg != 0) return;
-  }
-  if (rw >= RW || ri >= rows || ri >= TQ) return;
-  if constexpr (PG > 1) {
-    M = kNegInf;
-#pragma unroll
-    for (int i = 0; i < PG; ++i) M = fmaxf(M, sm[rw][i]);
-    L = 0.0f;
-    acc = make_float4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < PG; ++i) {
-      const float f = sm[rw][i] == kNegInf ? 0.0f : exp2_hw(sm[rw][i] - M);
-      const float4 v = so[rw][i][qd];
-      L += f * sl[rw][i];
-      acc.x += f * v.x;
-      acc.y += f * v.y;
-      acc.z += f * v.z;
-      acc.w += f * v.w;
-    }
-  }
-  using R = Rows<D, 1, 1, true>;
-  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-  const int row = qt * TQ + ri;
-  const int64_t orow = (int64_t)(s.q0 + row / a.r) * a.hq + h * a.r + row % a.r;
-  *(uint2*)(a.out + orow * D + qd * 4) =
-      make_uint2(R::pack_out(a.bf16, acc.x * inv, acc.y * inv), R::pack_out(a.bf16, acc.z * inv, acc.w * inv));
-  if (a.lse && qd == 0) a.lse[orow] = R::lse_of(M, L);
 }
 
 template <int D, int TQ, int PG>
-hipError_t launch_join(const Kv4Attn& a, hipStream_t s) {
+hipError_t launch_join(const Kv4Attn& a, int rows, hipStream_t s) {
   constexpr int RW = 256 / (D / 4 * PG);
-  hipLaunchKernelGGL((kv4_join_kernel<D, TQ, PG>), dim3(a.workers, (TQ + RW - 1) / RW), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((kv4_join_kernel<D, TQ, PG>), dim3(a.workers, (rows + RW - 1) / RW), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -811,7 +891,7 @@ hipError_t launch_rows(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
   hipLaunchKernelGGL((kv4_rows_kernel<D, NG, NQ, SYM>), dim3((unsigned)n), dim3(kWaves * 64), 0, s, a,
                      (int)(p.grid_q <= 4));
   if (hipError_t e = hipGetLastError()) return e;
-  return p.split ? launch_join<D, 16 * NQ, 256 / (D / 4)>(a, s) : hipSuccess;
+  return p.split ? launch_join<D, 16 * NQ, 256 / (D / 4)>(a, p.tile_rows, s) : hipSuccess;
 }
 
 template <int D, int NG>

@@ -97,7 +97,7 @@ struct Tile {
 
   // Keys: the exact integers c - z; their scales wait for the finished scores.
   // Keys that no row sees count as zeros, whatever their memory holds.
-  static __device__ __forceinline__ void expand_k(Codes& c, const Span& sp, uint8_t* buf, int blk, int m,
+  static __device__ __forceinline__ void expand_k(const Nibbles& nib, Codes& c, const Span& sp, uint8_t* buf, int blk, int m,
                                                   int kg) {
     const bool live = c.ok && c.pos + m >= sp.lo && c.pos + m < sp.hi;
 #pragma unroll
@@ -111,7 +111,7 @@ struct Tile {
 #pragma unroll
       for (int s = g * SPG; s < (g + 1) * SPG; ++s) {
         const uint32_t d = c.d[s], e = d >> 8;
-        const u32x4 w = {minus_zero_lo(d, n1), minus_zero_hi(d, n2), minus_zero_lo(e, n1), minus_zero_hi(e, n2)};
+        const u32x4 w = {nib.lo(d, n1), nib.hi(d, n2), nib.lo(e, n1), nib.hi(e, n2)};
         *(u32x4*)(buf + (blk * 16 + m) * KP + s * 64 + kg * 16) = w;
       }
     }
@@ -128,7 +128,7 @@ struct Tile {
   // Values: x^ / 2^E as fp16, rounded once (2^-11); E is the exponent of the
   // largest scale of the 16, so that they lie in fp16's normal range whatever
   // the scales are.  2^E comes back in the exponent of P.
-  static __device__ __forceinline__ void expand_v(Codes& c, const Span& sp, uint8_t* buf, int blk, int m,
+  static __device__ __forceinline__ void expand_v(const Nibbles& nib, Codes& c, const Span& sp, uint8_t* buf, int blk, int m,
                                                   int kg) {
     uint32_t top = 0;
 #pragma unroll
@@ -174,8 +174,8 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t w = byte_pair<NS>(c.d, 2 * i * NS + b, (2 * i + 1) * NS + b);
-          lo[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, minus_zero_lo(w, n1[i])) * S2[i]);
-          hi[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, minus_zero_hi(w, n2[i])) * S2[i]);
+          lo[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, nib.lo(w, n1[i])) * S2[i]);
+          hi[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, nib.hi(w, n2[i])) * S2[i]);
         }
         *(uint2*)(vb + (32 * b + 2 * m) * VP) = make_uint2(lo[0], lo[1]);
         *(uint2*)(vb + (32 * b + 2 * m + 1) * VP) = make_uint2(hi[0], hi[1]);
@@ -358,10 +358,11 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
   const int w = worker_of(blockIdx.x, a.workers);
   const int ps = a.c.page_shift;
   T st;
+  const Nibbles nib;
   const int64_t total = all_tiles<T::TQ, kTK>(a, lane, few != 0, -1, nullptr);
   int64_t at = total * w / a.workers;
   const int64_t end = total * (w + 1) / a.workers;
-  int32_t head_valid = 0, head_ends = 0, tail_valid = 0;
+  int last = -1;
   Cursor cur{0, 0, 0, 0};
   if (at < end) {
     all_tiles<T::TQ, kTK>(a, lane, few != 0, at, &cur);
@@ -392,12 +393,12 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
       };
       auto expand = [&](uint8_t* buf) {
         if constexpr (kBoth) {
-          T::expand_k(ck, sp, buf, blk, m, kg);
-          T::expand_v(cv, sp, buf, blk, m, kg);
+          T::expand_k(nib, ck, sp, buf, blk, m, kg);
+          T::expand_v(nib, cv, sp, buf, blk, m, kg);
         } else if (is_k) {
-          T::expand_k(ck, sp, buf, blk, m, kg);
+          T::expand_k(nib, ck, sp, buf, blk, m, kg);
         } else {
-          T::expand_v(ck, sp, buf, blk, m, kg);
+          T::expand_v(nib, ck, sp, buf, blk, m, kg);
         }
       };
       st.load_q(a, s, cur.h, row0 + n, hf);
@@ -418,7 +419,7 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
       float* part = nullptr;
       if (!(starts && ends)) {
         part = a.part + ((int64_t)2 * w + (starts ? 1 : 0)) * (T::TQ * (D + 2));
-        if (starts) { tail_valid = 1; } else { head_valid = 1; head_ends = ends; }
+        if (starts) last = worker_with(at + sp.cnt - 1, total, a.workers);
       }
       st.finish(a, s, cur.h, cur.qt, wave * 32 + n, part, hf);
       at += j1 - j0;
@@ -434,15 +435,7 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
       }
     }
   }
-  if (threadIdx.x == 0) {
-    int32_t* mt = a.meta + (int64_t)w * kMetaInts;
-    mt[0] = head_valid;
-    mt[1] = head_ends;
-    mt[2] = tail_valid;
-    mt[3] = (int32_t)cur.b;
-    mt[4] = cur.h;
-    mt[5] = cur.qt;
-  }
+  if (threadIdx.x == 0) leave_meta(a, w, last, cur, total);
 }
 
 template <int D, int NG>
@@ -453,7 +446,7 @@ hipError_t launch_tile(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
   else
     hipLaunchKernelGGL((kv4_tile_kernel<D, NG, false>), dim3(a.workers), dim3(Tile<D, NG, true>::NW * 64), 0, s, a, few);
   if (hipError_t e = hipGetLastError()) return e;
-  return launch_join<D, Tile<D, NG, true>::TQ, 1>(a, s);
+  return launch_join<D, Tile<D, NG, true>::TQ, 1>(a, p.tile_rows, s);
 }
 
 }  // namespace kv4
