@@ -78,7 +78,7 @@ struct Kv4Attn {
 // Waves per SIMD of the rows kernel: as many as its registers allow without
 // spilling (d channels in ng groups, nq tiles of 16 rows).
 constexpr int kv4_rows_waves(int d, int ng, int nq) {
-  return d * nq > 256 ? 1 : d > 128 || nq > 1 || ng > 2 ? 2 : 3;
+  return d * nq > 256 ? 1 : d > 128 || nq > 1 ? 2 : ng == 1 || d <= 64 ? 4 : 3;
 }
 
 struct Kv4Plan {

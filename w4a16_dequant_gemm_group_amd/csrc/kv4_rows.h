@@ -171,6 +171,41 @@ __device__ int64_t all_tiles(const Kv4Attn& a, int lane, bool few, int64_t find,
   return base;
 }
 
+// The sequence b that the whole wave works on, in scalar registers.
+__device__ __forceinline__ Seq wave_seq(const Kv4Attn& a, int64_t b) {
+  Seq s = get_seq(a, b);
+  s.q0 = __builtin_amdgcn_readfirstlane(s.q0);
+  s.n = __builtin_amdgcn_readfirstlane(s.n);
+  s.kv = __builtin_amdgcn_readfirstlane(s.kv);
+  return s;
+}
+
+// A row of the page table, which no kernel writes: read through the scalar
+// unit, so that the loads of the keys are not waited for along with it.
+typedef const int32_t __attribute__((address_space(4))) * PageRow;
+__device__ __forceinline__ PageRow page_row(const Kv4Attn& a, int64_t b) {
+  return (PageRow)(a.table + b * a.table_pages);
+}
+
+// 16 bytes per lane from p + voff to LDS at lds + 16 * lane, without registers
+// between.  The wait for it is the caller's (wait_dma).
+__device__ __forceinline__ void dma16(const uint8_t* p, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds), "v"(voff), "s"(p)
+               : "memory");
+}
+// Until at most N of the wave's loads are under way.
+template <int N>
+__device__ __forceinline__ void wait_dma() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+// Until the wave's reads of LDS have arrived: what they read may be overwritten.
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
 // N dwords from a 4-byte (N = 1, 3) or 8 / 16-byte aligned address.
 template <int N>
 __device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t (&w)[N]) {
@@ -303,6 +338,10 @@ struct Rows {
   static constexpr int DH = D > 128 ? 128 : D;       // columns of a join pass
   static constexpr int kSmemRow = DH + 4;
   static constexpr int kSmemFloats = kWaves * 16 * kSmemRow + 2 * kWaves * 16;
+  static constexpr int kSub = 2 * (8 * D + 16 * NG * (SYM ? 2 : 4));   // bytes of a sub-block
+  static constexpr int kLoads = 2 * ((kSub + 1023) / 1024);            // wave-wide loads of a unit
+  // two units per wave, later the waves' results
+  static constexpr int kSmem = kWaves * 4 * kSub > 4 * kSmemFloats ? kWaves * 4 * kSub : 4 * kSmemFloats;
 
   f16x8 q[NQ][NS];
   float A[NQ];                      // score factor
@@ -551,64 +590,82 @@ struct Rows {
     }
   }
 
-  // Key tiles j0 .. j1 - 1 of the span.  The next unit's keys are fetched once
-  // the present ones are multiplied, its values once the present ones are: no
-  // register more than one unit needs, and each load has the other half of the
-  // work to arrive.  Page numbers are fetched a unit earlier still.
+  // Key tiles j0 .. j1 - 1 of the span.  A wave's units pass through LDS, two
+  // at a time: a sub-block is one contiguous piece there as in the cache, and
+  // loads that need no registers leave those to more waves.  Load by load into
+  // registers, with half a unit's work to arrive, it was 45 us where this is
+  // MEASURED_DMA us (one token over 128 K keys).
   __device__ __forceinline__ void keys(const Kv4Attn& a, const Seq& s, const Span& sp, int64_t b, int h,
-                                       int qt, int j0, int j1, int wave, int m, int kg) {
-    const int32_t* row = a.table + b * a.table_pages;
+                                       int qt, int j0, int j1, uint8_t* smem, int wave, int m, int kg) {
+    const PageRow row = page_row(a, b);
     const int ps = a.c.page_shift;
     int u = (sp.t0 + j0) * kTile + wave * kUnit;
     int end = (sp.t0 + j1) * kTile;
     end = end < sp.hi ? end : sp.hi;
     if (u + kUnit <= sp.lo) u += kTile;      // only the first tile can hold keys before the span
+    load_q(a, s, h, qt, m, kg);
+    reset();
     if (u >= end) return;
-    struct Place { const uint8_t* p; bool ok; };
-    auto page_of = [&](int pos) -> int32_t {
-      return pos < sp.hi && pos + 16 > sp.lo ? row[pos >> ps] : -1;
+    const uint32_t voff = (threadIdx.x & 63) * 16u;
+    uint8_t* const own = smem + wave * (4 * kSub);
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_offset(own));
+    // bit t: sub-block t exists and some row sees keys of it
+    auto fetch = [&](int u, int buf) -> int {
+      int ok = 0;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int pos = u + 16 * t;
+        int64_t page = -1;
+        if (pos < sp.hi && pos + 16 > sp.lo) page = row[pos >> ps];
+        const bool is = page >= 0 && page < a.c.n_pages;
+        ok |= is ? 1 << t : 0;
+        // one that does not is read from the first page; its keys are not seen
+        const uint8_t* p = a.c.cache + kv4_block_offset(a.c, is ? page : 0, h, is ? pos & ((1 << ps) - 1) : 0);
+        const uint32_t dst = lds + (2 * buf + t) * kSub;
+#pragma unroll
+        for (int i = 0; i < kSub; i += 1024) {
+          if (i + 1024 <= kSub)
+            dma16(p + i, voff, dst + i);
+          else if (voff < (uint32_t)(kSub - i))
+            dma16(p + i, voff, dst + i);
+        }
+      }
+      return ok;
     };
-    auto place = [&](int32_t page, int pos) {
-      Place w;
-      w.ok = page >= 0 && page < a.c.n_pages;
-      w.p = a.c.cache + kv4_block_offset(a.c, w.ok ? page : 0, h, w.ok ? pos & ((1 << ps) - 1) : 0);
-      return w;
-    };
-    const uint32_t to_v = 8 * D + a.c.meta;
-    KeyBlock<D, NG, SYM> kb[2];
-    ValueBlock<D, NG, SYM> vb[2];
-    Place w0 = place(page_of(u), u), w1 = place(page_of(u + 16), u + 16);
-    kb[0].load(w0.p, m, kg);
-    kb[1].load(w1.p, m, kg);
-    vb[0].load(w0.p + to_v, m, kg);
-    vb[1].load(w1.p + to_v, m, kg);
-    int32_t pg0 = page_of(u + kTile), pg1 = page_of(u + kTile + 16);
-    for (;;) {
+    int ok = fetch(u, 0), oknext = 0;
+    if (u + kTile < end) oknext = fetch(u + kTile, 1);
+    for (int buf = 0;; buf ^= 1) {
       const int un = u + kTile;
-      const bool more = un < end;
+      if (un < end)
+        wait_dma<kLoads>();
+      else
+        wait_dma<0>();
       // every row sees every key: all before the first query's position and
       // inside the last one's window
-      bool full = w0.ok && w1.ok && u + kUnit <= s.kv;
+      bool full = ok == 3 && u + kUnit <= s.kv;
       if (a.causal) full = full && u + kUnit - 1 <= sp.p0;
       if (a.window > 0) full = full && u > sp.p1 - a.window;
-      const bool ok0 = w0.ok, ok1 = w1.ok;
+      const uint8_t* blk = own + buf * (2 * kSub);
       float x[NQ][2][4];
-      scores(kb, x);
-      if (more) {
-        w0 = place(pg0, un);
-        w1 = place(pg1, un + 16);
-        kb[0].load(w0.p, m, kg);
-        kb[1].load(w1.p, m, kg);
-        pg0 = page_of(un + kTile);
-        pg1 = page_of(un + kTile + 16);
+      {
+        KeyBlock<D, NG, SYM> kb[2];
+        kb[0].load(blk, m, kg);
+        kb[1].load(blk + kSub, m, kg);
+        scores(kb, x);
       }
-      if (!full) clear_unseen(sp, u, ok0, ok1, vb, kg);
-      weights(a, s, qt, u, !full, ok0, ok1, vb, x, kg);
+      ValueBlock<D, NG, SYM> vb[2];
+      vb[0].load(blk + kSub / 2, m, kg);
+      vb[1].load(blk + kSub / 2 + kSub, m, kg);
+      if (!full) clear_unseen(sp, u, ok & 1, ok & 2, vb, kg);
+      weights(a, s, qt, u, !full, ok & 1, ok & 2, vb, x, kg);
       values(vb, x);
-      if (!more) break;
-      vb[0].load(w0.p + to_v, m, kg);
-      vb[1].load(w1.p + to_v, m, kg);
+      if (un >= end) break;
       u = un;
+      ok = oknext;
+      if (un + kTile < end) {
+        wait_lds();
+        oknext = fetch(un + kTile, buf);
+      }
     }
   }
 
@@ -736,7 +793,7 @@ template <int D, int NG, int NQ, bool SYM>
 __global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NG, NQ)) void kv4_rows_kernel(Kv4Attn a,
                                                                                              int few) {
   using R = Rows<D, NG, NQ, SYM>;
-  __shared__ __attribute__((aligned(16))) float smem[R::kSmemFloats];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[R::kSmem];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, kg = lane >> 4;
@@ -759,22 +816,21 @@ __global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NG, NQ)) void kv4_ro
     cur.b = id / ((int64_t)a.grid_q * a.c.hkv);
   }
   int last = -1;
-  Seq s = get_seq(a, cur.b);
+  Seq s = wave_seq(a, cur.b);
   int nqt = (s.n * a.r + R::TQ - 1) / R::TQ;
   while (split ? at < end : cur.qt < nqt) {
     const Span sp = get_span<R::TQ, kTile>(a, s, cur.qt);
     const int j0 = (int)cur.off;
     const int j1 = !split || sp.cnt - j0 < end - at ? sp.cnt : j0 + (int)(end - at);
     const bool starts = j0 == 0, ends = j1 == sp.cnt;
-    st.load_q(a, s, cur.h, cur.qt, m, kg);
-    st.reset();
-    st.keys(a, s, sp, cur.b, cur.h, cur.qt, j0, j1, wave, m, kg);
+    st.keys(a, s, sp, cur.b, cur.h, cur.qt, j0, j1, smem, wave, m, kg);
     float* part = nullptr;
     if (!(starts && ends)) {
       part = a.part + ((int64_t)2 * w + (starts ? 1 : 0)) * (R::TQ * (D + 2));
       if (starts) last = worker_with(at + sp.cnt - 1, total, a.workers);
     }
-    st.finish(a, s, cur.h, cur.qt, part, smem, wave, m, kg);
+    st.finish(a, s, cur.h, cur.qt, part, (float*)smem, wave, m, kg);
+    __syncthreads();   // the results have been read: the buffers are free again
     if (!split) {
       cur.qt += a.grid_q;
       continue;
@@ -787,7 +843,7 @@ __global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NG, NQ)) void kv4_ro
       cur.qt = 0;
       if (++cur.h == a.c.hkv) {
         cur.h = 0;
-        do { ++cur.b; s = get_seq(a, cur.b); } while (s.n == 0);
+        do { ++cur.b; s = wave_seq(a, cur.b); } while (s.n == 0);
         nqt = (s.n * a.r + R::TQ - 1) / R::TQ;
       }
     }
@@ -811,7 +867,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
   const int last = mt[0];
   if (last < 0) return;
   const int h = mt[2], qt = mt[3], busy = mt[4];
-  const Seq s = get_seq(a, mt[1]);
+  const Seq s = wave_seq(a, mt[1]);
   const int left = s.n * a.r - qt * TQ, rows = left < TQ ? left : TQ;
   const int tid = threadIdx.x;
   const int rw = tid / (QD * PG), pg = tid / QD % PG, qd = tid % QD;
@@ -821,11 +877,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
     float M = kNegInf, L = 0.0f;
     float4 acc = make_float4(0, 0, 0, 0);
     if (mine) {
-#pragma unroll 4
-      for (int c = w + pg; c <= last; c += PG) {
-        // a worker in between that had no tile wrote nothing
-        if (busy < a.workers && c != w && (int64_t)busy * c / a.workers == (int64_t)busy * (c + 1) / a.workers)
-          continue;
+      auto add = [&](int c) {
         const float* p = a.part + (2 * (int64_t)c + (c == w ? 1 : 0)) * kSlot;
         const float mc = p[TQ * D + ri], lc = p[TQ * D + TQ + ri];
         const float4 v = *(const float4*)(p + ri * D + qd * 4);
@@ -839,6 +891,14 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
         acc.y = acc.y * f0 + v.y * f1;
         acc.z = acc.z * f0 + v.z * f1;
         acc.w = acc.w * f0 + v.w * f1;
+      };
+      if (busy == a.workers) {
+#pragma unroll 4
+        for (int c = w + pg; c <= last; c += PG) add(c);
+      } else {
+        // a worker in between that had no tile wrote nothing
+        for (int c = w + pg; c <= last; c += PG)
+          if (c == w || (int64_t)busy * c / a.workers != (int64_t)busy * (c + 1) / a.workers) add(c);
       }
     }
     if constexpr (PG > 1) {

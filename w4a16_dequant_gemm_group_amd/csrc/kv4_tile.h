@@ -366,14 +366,14 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
   Cursor cur{0, 0, 0, 0};
   if (at < end) {
     all_tiles<T::TQ, kTK>(a, lane, few != 0, at, &cur);
-    Seq s = get_seq(a, cur.b);
+    Seq s = wave_seq(a, cur.b);
     for (;;) {
       const Span sp = get_span<T::TQ, kTK>(a, s, cur.qt);
       const int j0 = (int)cur.off;
       const int j1 = sp.cnt - j0 < end - at ? sp.cnt : j0 + (int)(end - at);
       const bool starts = j0 == 0, ends = j1 == sp.cnt;
       const int row0 = cur.qt * T::TQ + wave * 32;
-      const int32_t* table = a.table + cur.b * a.table_pages;
+      const PageRow table = page_row(a, cur.b);
       // page of this wave's 16 keys of tile j, -1 where no row sees them
       auto page_of = [&](int j) -> int64_t {
         const int pos = (sp.t0 + j) * kTK + blk * 16;
@@ -430,7 +430,7 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
         cur.qt = 0;
         if (++cur.h == a.c.hkv) {
           cur.h = 0;
-          do { ++cur.b; s = get_seq(a, cur.b); } while (s.n == 0);
+          do { ++cur.b; s = wave_seq(a, cur.b); } while (s.n == 0);
         }
       }
     }
