@@ -59,6 +59,7 @@ struct Kv4Attn {
   const uint16_t* q;
   int64_t q_ts, q_hs, q_tokens;
   int32_t hq, r;                     // query heads, query heads per kv head
+  uint32_t r_mul, r_shift;           // n / r = (2 n * r_mul >> 32) >> r_shift for n < 2^31
   int32_t bf16;                      // 1: bf16 q and out, 0: fp16
   const int32_t* table;
   int64_t batch, table_pages;
@@ -70,6 +71,8 @@ struct Kv4Attn {
   float* lse;
   // the split over workgroups
   int32_t workers;                   // workgroups of a split launch
+  int32_t grain;                     // log2 of the keys of a tile of the split
+  int32_t few;                       // few row tiles per sequence: lanes share the sequences
   int32_t grid_q;                    // row tiles in an unsplit launch's grid
   int32_t* meta;                     // [workers][8] which row tiles were left open
   float* part;                       // [2 * workers][rows][D + 2] partial results
@@ -88,6 +91,8 @@ struct Kv4Plan {
   int workers;         // workgroups when split
   int grid_q;          // row tiles per (sequence, head) when not split
   int tile_rows;       // rows of a row tile, as far as max_q_len tells
+  int grain;           // log2 of the keys of a tile of the split
+  bool few;            // few row tiles per sequence
   size_t ws_bytes;
 };
 

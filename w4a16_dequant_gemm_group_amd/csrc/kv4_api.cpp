@@ -86,11 +86,19 @@ Kv4Plan kv4_plan(const gq_kv4_attention_args& a) {
   p.nq = rows <= 16 ? 1 : 2;
   p.tile = rows > 32;
   const int tq = p.tile ? (d > 128 ? 128 : 256) : 16 * p.nq;    // rows of a row tile
-  const int keys = p.tile ? 64 : 128;                           // keys of a tile of the split
   p.grid_q = (int)((rows + tq - 1) / tq);
   p.tile_rows = (int)std::min<int64_t>(rows, tq);
+  // lanes that share the sequences walk over the row tiles of each, lanes that
+  // share the row tiles walk over the sequences (a load and a scan for each)
+  p.few = p.grid_q <= 8 * std::min<int64_t>(a.batch, 64);
+  // The kernels count tiles in 32 bits: a coarser grain where there might be
+  // more (never more than q_tokens sequences have rows, so it ends).
+  const int64_t cap = a.table_pages * a.layout.page_size;
+  const int64_t row_tiles = (a.q_tokens * r / tq + std::min(a.batch, a.q_tokens)) * a.layout.kv_heads;
+  p.grain = p.tile ? 6 : 7;
+  while (p.grain < 30 && row_tiles * ((cap >> p.grain) + 1) >= INT32_MAX) ++p.grain;
   const int64_t segs = a.batch * a.layout.kv_heads * p.grid_q;
-  const int64_t tiles = segs * std::max<int64_t>(1, (a.max_kv_len + keys - 1) / keys);
+  const int64_t tiles = segs * std::max<int64_t>(1, (a.max_kv_len + (1 << p.grain) - 1) >> p.grain);
   p.split = p.tile || a.max_kv_len > 1024 || segs > INT32_MAX;
   if (p.split) {
     // as many workgroups (a wave on each SIMD) as run at once
@@ -218,7 +226,12 @@ gq_status gq_kv4_attention(const gq_kv4_attention_args* args, void* workspace,
   k.scale_log2 = a.scale * 1.4426950408889634f;
   k.out = (uint16_t*)a.out;
   k.lse = a.lse;
+  k.r_shift = 0;
+  while ((1 << k.r_shift) < k.r) ++k.r_shift;
+  k.r_mul = (uint32_t)((((uint64_t)1 << (31 + k.r_shift)) + k.r - 1) / k.r);
   k.workers = p.workers;
+  k.grain = p.grain;
+  k.few = p.few;
   k.grid_q = p.grid_q;
   k.meta = (int32_t*)workspace;
   k.part = p.split ? (float*)((uint8_t*)workspace + (size_t)p.workers * 32) : nullptr;

@@ -55,122 +55,6 @@ __device__ __forceinline__ Seq get_seq(const Kv4Attn& a, int64_t b) {
   return s;
 }
 
-// The keys that a row tile can see: positions lo .. hi - 1, tiles of T keys
-// t0 .. t0 + cnt - 1 (one empty tile where nothing is seen, so that every row
-// tile is visited and written).
-struct Span {
-  int p0, p1;   // positions of the first and last query
-  int lo, hi, t0, cnt;
-};
-
-template <int TQ, int T>
-__device__ __forceinline__ Span get_span(const Kv4Attn& a, const Seq& s, int qt) {
-  const int rows = s.n * a.r;
-  const int last = (qt + 1) * TQ < rows ? (qt + 1) * TQ - 1 : rows - 1;
-  Span p;
-  p.p0 = s.kv - s.n + qt * TQ / a.r;
-  p.p1 = s.kv - s.n + last / a.r;
-  p.hi = a.causal ? (p.p1 + 1 < s.kv ? p.p1 + 1 : s.kv) : s.kv;
-  p.hi = p.hi < 0 ? 0 : p.hi;
-  p.lo = a.window > 0 && p.p0 - a.window + 1 > 0 ? p.p0 - a.window + 1 : 0;
-  p.t0 = p.lo / T;
-  const int t1 = (p.hi + T - 1) / T;
-  p.cnt = t1 > p.t0 ? t1 - p.t0 : 1;
-  return p;
-}
-
-// Where the split stands: sequence, head, row tile, and the key tiles j0 .. j1
-// of its cnt that are this workgroup's.
-struct Cursor {
-  int64_t b;
-  int h, qt;
-  int64_t off;   // tiles of the row tile that lie before
-};
-
-__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t u = __shfl_up(v, d);
-    if (lane >= d) v += u;
-  }
-  return v;
-}
-
-__device__ __forceinline__ int64_t uniform64(int64_t v, int lane) {
-  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane);
-  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)((uint64_t)v >> 32), lane);
-  return (int64_t)(((uint64_t)hi << 32) | lo);
-}
-
-// Key tiles of one head over all row tiles of a sequence; lanes share the row
-// tiles.  With `find` >= 0: the row tile that holds tile number `find`.
-template <int TQ, int T>
-__device__ int64_t seq_tiles(const Kv4Attn& a, const Seq& s, int lane, int64_t find, Cursor* cur) {
-  const int nqt = (s.n * a.r + TQ - 1) / TQ;
-  int64_t base = 0;
-  for (int q = 0; q < nqt; q += 64) {
-    const int64_t v = q + lane < nqt ? get_span<TQ, T>(a, s, q + lane).cnt : 0;
-    const int64_t sc = wave_scan(v, lane);
-    if (find >= 0) {
-      const uint64_t hit = __ballot(base + sc > find);
-      if (hit) {
-        const int l = __builtin_ctzll(hit);
-        cur->qt = q + l;
-        cur->off = find - base - uniform64(sc - v, l);
-        return 0;
-      }
-    }
-    base += uniform64(sc, 63);
-  }
-  return base;
-}
-
-// All key tiles of the call, in the order sequence, head, row tile, key tile;
-// with `find` >= 0 the place of tile number `find`.  Few row tiles: lanes share
-// the sequences.  Many: lanes share the row tiles of one sequence at a time.
-template <int TQ, int T>
-__device__ int64_t all_tiles(const Kv4Attn& a, int lane, bool few, int64_t find, Cursor* cur) {
-  int64_t base = 0;
-  if (few) {
-    for (int64_t b0 = 0; b0 < a.batch; b0 += 64) {
-      int64_t v = 0;
-      if (b0 + lane < a.batch) {
-        const Seq s = get_seq(a, b0 + lane);
-        const int nqt = (s.n * a.r + TQ - 1) / TQ;
-        for (int q = 0; q < nqt; ++q) v += get_span<TQ, T>(a, s, q).cnt;
-        v *= a.c.hkv;
-      }
-      const int64_t sc = wave_scan(v, lane);
-      if (find >= 0) {
-        const uint64_t hit = __ballot(base + sc > find);
-        if (hit) {
-          const int l = __builtin_ctzll(hit);
-          cur->b = b0 + l;
-          const int64_t per = uniform64(v, l) / a.c.hkv;
-          const int64_t rem = find - base - uniform64(sc - v, l);
-          cur->h = (int)(rem / per);
-          seq_tiles<TQ, T>(a, get_seq(a, cur->b), lane, rem - cur->h * per, cur);
-          return 0;
-        }
-      }
-      base += uniform64(sc, 63);
-    }
-    return base;
-  }
-  for (int64_t b = 0; b < a.batch; ++b) {
-    const Seq s = get_seq(a, b);
-    const int64_t per = seq_tiles<TQ, T>(a, s, lane, -1, nullptr);
-    if (find >= 0 && base + per * a.c.hkv > find) {
-      cur->b = b;
-      cur->h = (int)((find - base) / per);
-      seq_tiles<TQ, T>(a, s, lane, find - base - cur->h * per, cur);
-      return 0;
-    }
-    base += per * a.c.hkv;
-  }
-  return base;
-}
-
 // The sequence b that the whole wave works on, in scalar registers.
 __device__ __forceinline__ Seq wave_seq(const Kv4Attn& a, int64_t b) {
   Seq s = get_seq(a, b);
@@ -178,6 +62,181 @@ __device__ __forceinline__ Seq wave_seq(const Kv4Attn& a, int64_t b) {
   s.n = __builtin_amdgcn_readfirstlane(s.n);
   s.kv = __builtin_amdgcn_readfirstlane(s.kv);
   return s;
+}
+
+// n / r, the query heads per key/value head, for n < 2^31.
+__device__ __forceinline__ int div_r(const Kv4Attn& a, int n) {
+  return (int)(__umulhi(2u * (uint32_t)n, a.r_mul) >> a.r_shift);
+}
+__device__ __forceinline__ int row_tiles(const Kv4Attn& a, const Seq& s, int tq) {
+  return (s.n * a.r + tq - 1) / tq;
+}
+
+// Row of `out` and `lse` that row `row` of a sequence's rows of head h is.
+__device__ __forceinline__ int64_t out_row(const Kv4Attn& a, const Seq& s, int h, int row) {
+  const int tok = div_r(a, row);
+  return (int64_t)(s.q0 + tok) * a.hq + h * a.r + row - tok * a.r;
+}
+
+// The keys that row tile qt can see: positions lo .. hi - 1, tiles t0 ..
+// t0 + cnt - 1 of 2^grain keys (one at least: a row without keys is written too).
+struct Span {
+  int p0, p1;   // positions of the first and last query
+  int lo, hi, t0, cnt;
+};
+
+template <int TQ>
+__device__ __forceinline__ Span get_span(const Kv4Attn& a, const Seq& s, int qt) {
+  const int rows = s.n * a.r;
+  const int last = (qt + 1) * TQ < rows ? (qt + 1) * TQ - 1 : rows - 1;
+  Span p;
+  p.p0 = s.kv - s.n + div_r(a, qt * TQ);
+  p.p1 = s.kv - s.n + div_r(a, last);
+  p.hi = a.causal ? (p.p1 + 1 < s.kv ? p.p1 + 1 : s.kv) : s.kv;
+  p.hi = p.hi < 0 ? 0 : p.hi;
+  p.lo = a.window > 0 && p.p0 - a.window + 1 > 0 ? p.p0 - a.window + 1 : 0;
+  p.t0 = p.lo >> a.grain;
+  const int t1 = (p.hi + (1 << a.grain) - 1) >> a.grain;
+  p.cnt = t1 > p.t0 ? t1 - p.t0 : 1;
+  return p;
+}
+
+// Where the split stands: sequence, head, row tile, and the key tiles of the
+// row tile that lie before.
+struct Cursor {
+  int b, h, qt, off;
+};
+
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t u = __shfl_up(v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+// Key tiles of one head over all row tiles of a sequence; lanes share the row
+// tiles.  With `find`: the row tile that holds tile number i.
+template <int TQ>
+__device__ __forceinline__ uint32_t seq_tiles(const Kv4Attn& a, const Seq& s, int lane, bool find, uint32_t i,
+                                              Cursor* cur) {
+  const int nqt = row_tiles(a, s, TQ);
+  uint32_t base = 0;
+  for (int q = 0; q < nqt; q += 64) {
+    const uint32_t v = q + lane < nqt ? get_span<TQ>(a, s, q + lane).cnt : 0;
+    const uint32_t sc = wave_scan(v, lane);
+    if (find) {
+      const uint64_t hit = __ballot(base + sc > i);
+      if (hit) {
+        const int l = __builtin_ctzll(hit);
+        cur->qt = q + l;
+        cur->off = (int)(i - base - lane_of(sc - v, l));
+        return 0;
+      }
+    }
+    base += lane_of(sc, 63);
+  }
+  return base;
+}
+
+// All key tiles of the call, in the order sequence, head, row tile, key tile,
+// are cut into one run per worker, as equal as whole tiles allow.
+struct Share {
+  uint32_t total, at, end;   // tiles of the call; this worker's
+  int busy;                  // workers that have any
+  int w;                     // this one's number
+  Cursor cur;                // where tile `at` is
+
+  // The worker numbers are dealt such that each of the 8 dies (workgroups go
+  // round robin over them) works on neighbouring runs: its L2 cache sees
+  // neighbouring keys.
+  __device__ __forceinline__ void cut(const Kv4Attn& a) {
+    busy = total < (uint32_t)a.workers ? (int)total : a.workers;
+    const int per_die = (busy + 7) >> 3, x = blockIdx.x >> 3;
+    w = (blockIdx.x & 7) * per_die + x;
+    at = end = 0;
+    if (x >= per_die || w >= busy) return;
+    const uint32_t q = total / busy, m = total % busy;   // the first m have one more
+    at = q * w + (w < (int)m ? w : m);
+    end = at + q + (w < (int)m ? 1 : 0);
+  }
+  // the worker that has tile i
+  __device__ __forceinline__ int worker_with(uint32_t i) const {
+    const uint32_t q = total / busy, m = total % busy, big = (q + 1) * m;
+    return (int)(i < big ? i / (q + 1) : m + (i - big) / q);
+  }
+};
+
+template <int TQ>
+__device__ __forceinline__ Share find_share(const Kv4Attn& a, int lane) {
+  Share sh{};
+  sh.cur = Cursor{0, 0, 0, 0};
+  const int batch = (int)a.batch, heads = a.c.hkv;
+  uint32_t base = 0;
+  if (a.few) {
+    uint32_t v = 0, sc = 0;
+    auto scan = [&](int b0) {
+      v = 0;
+      if (b0 + lane < batch) {
+        const Seq s = get_seq(a, b0 + lane);
+        const int nqt = row_tiles(a, s, TQ);
+        for (int q = 0; q < nqt; ++q) v += get_span<TQ>(a, s, q).cnt;
+      }
+      sc = wave_scan(v, lane);
+    };
+    for (int b0 = 0; b0 < batch; b0 += 64) {
+      scan(b0);
+      base += lane_of(sc, 63);
+    }
+    sh.total = base * heads;
+    sh.cut(a);
+    if (sh.at == sh.end) return sh;
+    base = 0;
+    for (int b0 = 0;; b0 += 64) {
+      if (batch > 64) scan(b0);
+      const uint64_t hit = __ballot((base + sc) * heads > sh.at);
+      if (hit) {
+        const int l = __builtin_ctzll(hit);
+        const uint32_t per = lane_of(v, l);
+        const uint32_t i = sh.at - (base + lane_of(sc - v, l)) * heads;
+        sh.cur.b = b0 + l;
+        sh.cur.h = (int)(i / per);
+        seq_tiles<TQ>(a, wave_seq(a, sh.cur.b), lane, true, i % per, &sh.cur);
+        return sh;
+      }
+      base += lane_of(sc, 63);
+    }
+  }
+  for (int b = 0; b < batch; ++b) base += seq_tiles<TQ>(a, wave_seq(a, b), lane, false, 0, nullptr);
+  sh.total = base * heads;
+  sh.cut(a);
+  if (sh.at == sh.end) return sh;
+  base = 0;
+  for (int b = 0;; ++b) {
+    const Seq s = wave_seq(a, b);
+    const uint32_t per = seq_tiles<TQ>(a, s, lane, false, 0, nullptr), i = sh.at - base * heads;
+    if (i < per * heads) {
+      sh.cur.b = b;
+      sh.cur.h = (int)(i / per);
+      seq_tiles<TQ>(a, s, lane, true, i % per, &sh.cur);
+      return sh;
+    }
+    base += per;
+  }
+}
+
+// What the join has to know of a worker: the row tile that it left open (last:
+// the last of the workers after it that hold the rest), or none (last < 0).
+__device__ __forceinline__ void leave_meta(const Kv4Attn& a, const Share& sh, int last, const Cursor& cur) {
+  if ((int)blockIdx.x >= sh.busy) a.meta[(int64_t)blockIdx.x * kMetaInts] = -1;   // a number nobody has
+  if (sh.at == sh.end) return;
+  int32_t* mt = a.meta + (int64_t)sh.w * kMetaInts;
+  mt[0] = last;
+  mt[1] = cur.b;
+  mt[2] = cur.h;
+  mt[3] = cur.qt;
 }
 
 // A row of the page table, which no kernel writes: read through the scalar
@@ -357,15 +416,14 @@ struct Rows {
 
   __device__ __forceinline__ void load_q(const Kv4Attn& a, const Seq& s, int h, int qt, int m, int kg) {
     const int rows = s.n * a.r;
-    rest = NQ == 1 && !a.bf16 && rows <= 8;
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) {
-      const int row = qt * TQ + nq * 16 + row_of_lane();
+      const int row = qt * TQ + nq * 16 + row_of_lane(), tok = div_r(a, row);
       float x[NS][8];
       float mx = 0.0f;
       const bool ok = row < rows;
       const uint16_t* p = a.q;
-      if (ok) p += (int64_t)(s.q0 + row / a.r) * a.q_ts + (int64_t)(h * a.r + row % a.r) * a.q_hs;
+      if (ok) p += (int64_t)(s.q0 + tok) * a.q_ts + (int64_t)(h * a.r + row - tok * a.r) * a.q_hs;
 #pragma unroll
       for (int st = 0; st < NS; ++st) {
         uint4 v = make_uint4(0, 0, 0, 0);
@@ -490,7 +548,7 @@ struct Rows {
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[t][i] = __builtin_fmaf(x[nq][t][i], A[nq], lv[t][i]);
       if (masked) {
-        const int tok = (qt * TQ + nq * 16 + row_of_lane()) / a.r;
+        const int tok = div_r(a, qt * TQ + nq * 16 + row_of_lane());
         const int pos = s.kv - s.n + tok;
         const int last = a.causal && pos < s.kv - 1 ? pos : s.kv - 1;
         const int first = a.window > 0 ? pos - a.window + 1 : 0;
@@ -599,24 +657,36 @@ struct Rows {
                                        int qt, int j0, int j1, uint8_t* smem, int wave, int m, int kg) {
     const PageRow row = page_row(a, b);
     const int ps = a.c.page_shift;
-    int u = (sp.t0 + j0) * kTile + wave * kUnit;
-    int end = (sp.t0 + j1) * kTile;
-    end = end < sp.hi ? end : sp.hi;
-    if (u + kUnit <= sp.lo) u += kTile;      // only the first tile can hold keys before the span
-    load_q(a, s, h, qt, m, kg);
+    int u = (sp.t0 + j0) << a.grain;
+    const int64_t cut = (int64_t)(sp.t0 + j1) << a.grain;
+    const int end = cut < sp.hi ? (int)cut : sp.hi;
+    if (u < sp.lo) u = sp.lo & ~(kTile - 1);   // only the first tile can hold keys before the span
+    u += wave * kUnit;
+    if (u + kUnit <= sp.lo) u += kTile;
+    rest = NQ == 1 && !a.bf16 && s.n * a.r <= 8;
     reset();
     if (u >= end) return;
     const uint32_t voff = (threadIdx.x & 63) * 16u;
     uint8_t* const own = smem + wave * (4 * kSub);
     const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_offset(own));
-    // bit t: sub-block t exists and some row sees keys of it
-    auto fetch = [&](int u, int buf) -> int {
+    // pages of the sub-blocks of a unit, -1 where no row sees keys of one
+    struct Pages { int32_t p[2]; };
+    auto pages = [&](int u) {
+      Pages r = {{-1, -1}};
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int pos = u + 16 * t;
+        if (pos < end && pos + 16 > sp.lo) r.p[t] = row[pos >> ps];
+      }
+      return r;
+    };
+    // bit t: sub-block t exists
+    auto fetch = [&](const Pages& pg, int u, int buf) -> int {
       int ok = 0;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int pos = u + 16 * t;
-        int64_t page = -1;
-        if (pos < sp.hi && pos + 16 > sp.lo) page = row[pos >> ps];
+        const int64_t page = pg.p[t];
         const bool is = page >= 0 && page < a.c.n_pages;
         ok |= is ? 1 << t : 0;
         // one that does not is read from the first page; its keys are not seen
@@ -632,10 +702,14 @@ struct Rows {
       }
       return ok;
     };
-    int ok = fetch(u, 0), oknext = 0;
-    if (u + kTile < end) oknext = fetch(u + kTile, 1);
+    const Pages first = pages(u);
+    Pages next = pages(u + kTile);
+    int ok = fetch(first, u, 0), oknext = 0;
+    if (u + kTile < end) oknext = fetch(next, u + kTile, 1);
+    load_q(a, s, h, qt, m, kg);
     for (int buf = 0;; buf ^= 1) {
       const int un = u + kTile;
+      next = pages(un + kTile);
       if (un < end)
         wait_dma<kLoads>();
       else
@@ -664,7 +738,7 @@ struct Rows {
       ok = oknext;
       if (un + kTile < end) {
         wait_lds();
-        oknext = fetch(un + kTile, buf);
+        oknext = fetch(next, un + kTile, buf);
       }
     }
   }
@@ -737,7 +811,7 @@ struct Rows {
               part[TQ * D + TQ + nq * 16 + rr] = L;
             }
           } else {
-            const int64_t orow = (int64_t)(s.q0 + row / a.r) * a.hq + h * a.r + row % a.r;
+            const int64_t orow = out_row(a, s, h, row);
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
             uint16_t* po = a.out + orow * D + half * DH + c0;
 #pragma unroll
@@ -765,33 +839,8 @@ struct Rows {
   }
 };
 
-// XCD-aware order: workgroups go round robin over the 8 dies, so worker
-// numbers are dealt such that each die works on one run of the tiles and its
-// L2 cache sees neighbouring keys.
-__device__ __forceinline__ int worker_of(int bid, int workers) {
-  return workers % 8 == 0 ? (bid & 7) * (workers >> 3) + (bid >> 3) : bid;
-}
-
-// The worker whose share of the `total` tiles (total * w / workers ..) holds tile i.
-__device__ __forceinline__ int worker_with(int64_t i, int64_t total, int workers) {
-  return (int)(((i + 1) * workers + total - 1) / total) - 1;
-}
-
-// What the join has to know of worker w: the row tile that it left open, if
-// any, and the last of the workers after it that hold the rest of that tile.
-__device__ __forceinline__ void leave_meta(const Kv4Attn& a, int w, int last, const Cursor& cur, int64_t total) {
-  int32_t* mt = a.meta + (int64_t)w * kMetaInts;
-  mt[0] = last;
-  mt[1] = (int32_t)cur.b;
-  mt[2] = cur.h;
-  mt[3] = cur.qt;
-  // fewer tiles than workers: some had none
-  mt[4] = total < a.workers ? (int32_t)total : a.workers;
-}
-
 template <int D, int NG, int NQ, bool SYM>
-__global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NG, NQ)) void kv4_rows_kernel(Kv4Attn a,
-                                                                                             int few) {
+__global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NG, NQ)) void kv4_rows_kernel(Kv4Attn a) {
   using R = Rows<D, NG, NQ, SYM>;
   __shared__ __attribute__((aligned(16))) uint8_t smem[R::kSmem];
   const int lane = threadIdx.x & 63;
@@ -799,35 +848,33 @@ __global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NG, NQ)) void kv4_ro
   const int m = lane & 15, kg = lane >> 4;
   R st;
   const bool split = a.workers > 0;
-  int w = 0;
-  int64_t at = 0, end = 0, total = 0;
-  Cursor cur{0, 0, 0, 0};
+  Share sh{};
+  Cursor cur{};
   if (split) {
-    w = worker_of(blockIdx.x, a.workers);
-    total = all_tiles<R::TQ, kTile>(a, lane, few != 0, -1, nullptr);
-    at = total * w / a.workers;
-    end = total * (w + 1) / a.workers;
-    if (at < end) all_tiles<R::TQ, kTile>(a, lane, few != 0, at, &cur);
+    sh = find_share<R::TQ>(a, lane);
+    cur = sh.cur;
   } else {
     // one workgroup per (sequence, head, row tile)
-    const int64_t id = blockIdx.x;
-    cur.qt = (int)(id % a.grid_q);
-    cur.h = (int)(id / a.grid_q % a.c.hkv);
-    cur.b = id / ((int64_t)a.grid_q * a.c.hkv);
+    const int id = blockIdx.x, bh = id / a.grid_q;
+    cur.qt = id % a.grid_q;
+    cur.h = bh % a.c.hkv;
+    cur.b = bh / a.c.hkv;
+    cur.off = 0;
   }
+  uint32_t at = sh.at;
   int last = -1;
   Seq s = wave_seq(a, cur.b);
-  int nqt = (s.n * a.r + R::TQ - 1) / R::TQ;
-  while (split ? at < end : cur.qt < nqt) {
-    const Span sp = get_span<R::TQ, kTile>(a, s, cur.qt);
-    const int j0 = (int)cur.off;
-    const int j1 = !split || sp.cnt - j0 < end - at ? sp.cnt : j0 + (int)(end - at);
+  int nqt = row_tiles(a, s, R::TQ);
+  while (split ? at < sh.end : cur.qt < nqt) {
+    const Span sp = get_span<R::TQ>(a, s, cur.qt);
+    const int j0 = cur.off, left = (int)(sh.end - at);
+    const int j1 = !split || sp.cnt - j0 < left ? sp.cnt : j0 + left;
     const bool starts = j0 == 0, ends = j1 == sp.cnt;
     st.keys(a, s, sp, cur.b, cur.h, cur.qt, j0, j1, smem, wave, m, kg);
     float* part = nullptr;
     if (!(starts && ends)) {
-      part = a.part + ((int64_t)2 * w + (starts ? 1 : 0)) * (R::TQ * (D + 2));
-      if (starts) last = worker_with(at + sp.cnt - 1, total, a.workers);
+      part = a.part + ((int64_t)2 * sh.w + (starts ? 1 : 0)) * (R::TQ * (D + 2));
+      if (starts) last = sh.worker_with(at + sp.cnt - 1);
     }
     st.finish(a, s, cur.h, cur.qt, part, (float*)smem, wave, m, kg);
     __syncthreads();   // the results have been read: the buffers are free again
@@ -836,7 +883,7 @@ __global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NG, NQ)) void kv4_ro
       continue;
     }
     at += j1 - j0;
-    if (at >= end) break;
+    if (at >= sh.end) break;
     // the next row tile, head, sequence that has rows
     cur.off = 0;
     if (++cur.qt == nqt) {
@@ -844,11 +891,11 @@ __global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NG, NQ)) void kv4_ro
       if (++cur.h == a.c.hkv) {
         cur.h = 0;
         do { ++cur.b; s = wave_seq(a, cur.b); } while (s.n == 0);
-        nqt = (s.n * a.r + R::TQ - 1) / R::TQ;
+        nqt = row_tiles(a, s, R::TQ);
       }
     }
   }
-  if (split && threadIdx.x == 0) leave_meta(a, w, last, cur, total);
+  if (split && threadIdx.x == 0) leave_meta(a, sh, last, cur);
 }
 
 // Joins the partial results of the row tiles that were split.  Worker w left
@@ -866,7 +913,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
   const int32_t* mt = a.meta + (int64_t)w * kMetaInts;
   const int last = mt[0];
   if (last < 0) return;
-  const int h = mt[2], qt = mt[3], busy = mt[4];
+  const int h = mt[2], qt = mt[3];
   const Seq s = wave_seq(a, mt[1]);
   const int left = s.n * a.r - qt * TQ, rows = left < TQ ? left : TQ;
   const int tid = threadIdx.x;
@@ -892,14 +939,8 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
         acc.z = acc.z * f0 + v.z * f1;
         acc.w = acc.w * f0 + v.w * f1;
       };
-      if (busy == a.workers) {
 #pragma unroll 4
-        for (int c = w + pg; c <= last; c += PG) add(c);
-      } else {
-        // a worker in between that had no tile wrote nothing
-        for (int c = w + pg; c <= last; c += PG)
-          if (c == w || (int64_t)busy * c / a.workers != (int64_t)busy * (c + 1) / a.workers) add(c);
-      }
+      for (int c = w + pg; c <= last; c += PG) add(c);
     }
     if constexpr (PG > 1) {
       if (mine) {
@@ -930,7 +971,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
       using R = Rows<D, 1, 1, true>;
       const float inv = L == 0.0f ? 0.0f : 1.0f / L;
       const int row = qt * TQ + ri;
-      const int64_t orow = (int64_t)(s.q0 + row / a.r) * a.hq + h * a.r + row % a.r;
+      const int64_t orow = out_row(a, s, h, row);
       *(uint2*)(a.out + orow * D + qd * 4) = make_uint2(R::pack_out(a.bf16, acc.x * inv, acc.y * inv),
                                                         R::pack_out(a.bf16, acc.z * inv, acc.w * inv));
       if (a.lse && qd == 0) a.lse[orow] = R::lse_of(M, L);
@@ -948,8 +989,7 @@ hipError_t launch_join(const Kv4Attn& a, int rows, hipStream_t s) {
 template <int D, int NG, int NQ, bool SYM>
 hipError_t launch_rows(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
   const int64_t n = p.split ? a.workers : (int64_t)p.grid_q * a.c.hkv * a.batch;
-  hipLaunchKernelGGL((kv4_rows_kernel<D, NG, NQ, SYM>), dim3((unsigned)n), dim3(kWaves * 64), 0, s, a,
-                     (int)(p.grid_q <= 4));
+  hipLaunchKernelGGL((kv4_rows_kernel<D, NG, NQ, SYM>), dim3((unsigned)n), dim3(kWaves * 64), 0, s, a);
   if (hipError_t e = hipGetLastError()) return e;
   return p.split ? launch_join<D, 16 * NQ, 256 / (D / 4)>(a, p.tile_rows, s) : hipSuccess;
 }

@@ -186,7 +186,8 @@ struct Tile {
   __device__ __forceinline__ void load_q(const Kv4Attn& a, const Seq& s, int h, int row, int hf) {
     const bool ok = row < s.n * a.r;
     const uint16_t* p = a.q;
-    if (ok) p += (int64_t)(s.q0 + row / a.r) * a.q_ts + (int64_t)(h * a.r + row % a.r) * a.q_hs;
+    const int tok = div_r(a, row);
+    if (ok) p += (int64_t)(s.q0 + tok) * a.q_ts + (int64_t)(h * a.r + row - tok * a.r) * a.q_hs;
     float mx = 0.0f;
 #pragma unroll
     for (int st = 0; st < D / 16; ++st) {
@@ -254,10 +255,10 @@ struct Tile {
     const int rows = s.n * a.r;
     const int lastrow = row0 + 32 < rows ? row0 + 31 : rows - 1;
     bool full = u + kTK <= s.kv;
-    if (a.causal) full = full && u + kTK - 1 <= s.kv - s.n + row0 / a.r;
-    if (a.window > 0) full = full && u > s.kv - s.n + lastrow / a.r - a.window;
+    if (a.causal) full = full && u + kTK - 1 <= s.kv - s.n + div_r(a, row0);
+    if (a.window > 0) full = full && u > s.kv - s.n + div_r(a, lastrow) - a.window;
     if (!full) {
-      const int pos = s.kv - s.n + (row0 + n) / a.r;
+      const int pos = s.kv - s.n + div_r(a, row0 + n);
       const int last = a.causal && pos < s.kv - 1 ? pos : s.kv - 1;
       const int first = a.window > 0 ? pos - a.window + 1 : 0;
 #pragma unroll
@@ -332,7 +333,7 @@ struct Tile {
       }
       return;
     }
-    const int64_t orow = (int64_t)(s.q0 + row / a.r) * a.hq + h * a.r + row % a.r;
+    const int64_t orow = out_row(a, s, h, row);
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
     for (int d = 0; d < NS; ++d)
@@ -346,7 +347,7 @@ struct Tile {
 };
 
 template <int D, int NG, bool SYM>
-__global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_tile_kernel(Kv4Attn a, int few) {
+__global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_tile_kernel(Kv4Attn a) {
   using T = Tile<D, NG, SYM>;
   constexpr bool kBoth = T::NW == 4;   // a wave expands keys and values of its block; else one of them
   __shared__ __attribute__((aligned(16))) uint8_t smem[2 * T::kBuf];
@@ -355,33 +356,35 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
   const int m = lane & 15, kg = lane >> 4, n = lane & 31, hf = lane >> 5;
   const int blk = wave & 3;            // the 16 keys of a tile that this wave expands
   const bool is_k = wave < 4;
-  const int w = worker_of(blockIdx.x, a.workers);
   const int ps = a.c.page_shift;
   T st;
   const Nibbles nib;
-  const int64_t total = all_tiles<T::TQ, kTK>(a, lane, few != 0, -1, nullptr);
-  int64_t at = total * w / a.workers;
-  const int64_t end = total * (w + 1) / a.workers;
+  const Share sh = find_share<T::TQ>(a, lane);
+  uint32_t at = sh.at;
   int last = -1;
-  Cursor cur{0, 0, 0, 0};
-  if (at < end) {
-    all_tiles<T::TQ, kTK>(a, lane, few != 0, at, &cur);
+  Cursor cur = sh.cur;
+  if (at < sh.end) {
     Seq s = wave_seq(a, cur.b);
     for (;;) {
-      const Span sp = get_span<T::TQ, kTK>(a, s, cur.qt);
-      const int j0 = (int)cur.off;
-      const int j1 = sp.cnt - j0 < end - at ? sp.cnt : j0 + (int)(end - at);
+      const Span sp = get_span<T::TQ>(a, s, cur.qt);
+      const int j0 = cur.off, left = (int)(sh.end - at);
+      const int j1 = sp.cnt - j0 < left ? sp.cnt : j0 + left;
       const bool starts = j0 == 0, ends = j1 == sp.cnt;
       const int row0 = cur.qt * T::TQ + wave * 32;
+      // the run's keys, 64 at a time
+      const int64_t cut = (int64_t)(sp.t0 + j1) << a.grain;
+      const int stop = cut < sp.hi ? (int)cut : sp.hi;
+      int u0 = (sp.t0 + j0) << a.grain;
+      if (u0 < sp.lo) u0 = sp.lo & ~(kTK - 1);
       const PageRow table = page_row(a, cur.b);
-      // page of this wave's 16 keys of tile j, -1 where no row sees them
-      auto page_of = [&](int j) -> int64_t {
-        const int pos = (sp.t0 + j) * kTK + blk * 16;
-        return j < j1 && pos < sp.hi && pos + 16 > sp.lo ? table[pos >> ps] : -1;
+      // page of this wave's 16 of the 64 keys from u on, -1 where no row sees them
+      auto page_of = [&](int u) -> int64_t {
+        const int pos = u + blk * 16;
+        return pos < stop && pos + 16 > sp.lo ? table[pos >> ps] : -1;
       };
       typename T::Codes ck, cv;   // a wave that expands one of them uses ck for it
-      auto fetch = [&](int64_t page, int j) {
-        const int u = (sp.t0 + j) * kTK + blk * 16;
+      auto fetch = [&](int64_t page, int u) {
+        u += blk * 16;
         if constexpr (kBoth) {
           ck.load_k(a, page, cur.h, u, m, kg);
           cv.load_v(a, page, cur.h, u, m, kg);
@@ -402,30 +405,30 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
         }
       };
       st.load_q(a, s, cur.h, row0 + n, hf);
-      fetch(page_of(j0), j0);
+      fetch(page_of(u0), u0);
       expand(smem);
-      int64_t next = page_of(j0 + 1);
+      int64_t next = page_of(u0 + kTK);
       __syncthreads();
-      for (int j = j0; j < j1; ++j) {
-        const int b = (j - j0) & 1;
-        if (j + 1 < j1) {
-          fetch(next, j + 1);
-          next = page_of(j + 2);
+      for (int u = u0, b = 0; u < stop; u += kTK, b ^= 1) {
+        const bool more = u + kTK < stop;
+        if (more) {
+          fetch(next, u + kTK);
+          next = page_of(u + 2 * kTK);
         }
-        if (row0 < s.n * a.r) st.attend(a, s, row0, (sp.t0 + j) * kTK, smem + b * T::kBuf, n, hf);
-        if (j + 1 < j1) expand(smem + (b ^ 1) * T::kBuf);
+        if (row0 < s.n * a.r) st.attend(a, s, row0, u, smem + b * T::kBuf, n, hf);
+        if (more) expand(smem + (b ^ 1) * T::kBuf);
         __syncthreads();
       }
       float* part = nullptr;
       if (!(starts && ends)) {
-        part = a.part + ((int64_t)2 * w + (starts ? 1 : 0)) * (T::TQ * (D + 2));
-        if (starts) last = worker_with(at + sp.cnt - 1, total, a.workers);
+        part = a.part + ((int64_t)2 * sh.w + (starts ? 1 : 0)) * (T::TQ * (D + 2));
+        if (starts) last = sh.worker_with(at + sp.cnt - 1);
       }
       st.finish(a, s, cur.h, cur.qt, wave * 32 + n, part, hf);
       at += j1 - j0;
-      if (at >= end) break;
+      if (at >= sh.end) break;
       cur.off = 0;
-      const int nqt = (s.n * a.r + T::TQ - 1) / T::TQ;
+      const int nqt = row_tiles(a, s, T::TQ);
       if (++cur.qt == nqt) {
         cur.qt = 0;
         if (++cur.h == a.c.hkv) {
@@ -435,16 +438,15 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
       }
     }
   }
-  if (threadIdx.x == 0) leave_meta(a, w, last, cur, total);
+  if (threadIdx.x == 0) leave_meta(a, sh, last, cur);
 }
 
 template <int D, int NG>
 hipError_t launch_tile(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
-  const int few = p.grid_q <= 4;
   if (a.c.sym)
-    hipLaunchKernelGGL((kv4_tile_kernel<D, NG, true>), dim3(a.workers), dim3(Tile<D, NG, true>::NW * 64), 0, s, a, few);
+    hipLaunchKernelGGL((kv4_tile_kernel<D, NG, true>), dim3(a.workers), dim3(Tile<D, NG, true>::NW * 64), 0, s, a);
   else
-    hipLaunchKernelGGL((kv4_tile_kernel<D, NG, false>), dim3(a.workers), dim3(Tile<D, NG, true>::NW * 64), 0, s, a, few);
+    hipLaunchKernelGGL((kv4_tile_kernel<D, NG, false>), dim3(a.workers), dim3(Tile<D, NG, true>::NW * 64), 0, s, a);
   if (hipError_t e = hipGetLastError()) return e;
   return launch_join<D, Tile<D, NG, true>::TQ, 1>(a, p.tile_rows, s);
 }
