@@ -8,6 +8,8 @@
 //   value codes  [4 token quads][16 m][4 tokens][NS] bytes
 //   value params S fp16 [NG][16 tokens] (symmetric), or [NG][4 token quads] of
 //                {S of 4 tokens, z of 4 tokens} fp16
+// A zero point z (an integer 0 .. 15) is kept as -(1024 + z), what a code takes
+// on as fp16 bits 0x6400 | c is short of c - z by.
 // Both code orders are those in which the 16x16x32 matrix product takes its first
 // operand, whose lane (m = lane % 16, kg = lane / 16) holds row m and 8
 // consecutive k:
@@ -39,6 +41,10 @@ struct Kv4Geo {
   uint32_t meta;        // bytes of one parameter section: 16 * ng * (sym ? 2 : 4)
   uint32_t sb;          // bytes of a sub-block: 2 * (8 d + meta)
 };
+
+// A zero point as it is stored, and back.
+__device__ __forceinline__ uint16_t kv4_zero_bits(int z) { return (uint16_t)(0xE400u | (uint32_t)z); }
+__device__ __forceinline__ float kv4_zero(uint16_t b) { return -1024.0f - f16_to_f32(b); }
 
 // Byte offset of the sub-block that holds `slot` for `head`.
 __device__ __forceinline__ int64_t kv4_block_offset(const Kv4Geo& c, int64_t page, int head,

@@ -351,7 +351,7 @@ __device__ __forceinline__ uint32_t byte_pair(const uint32_t (&w)[N], int i, int
 
 // A pair of codes, masked in place, to fp16 c - z.  lo: nibbles at bits 0..3 of
 // each half, where 0x6400 | c is 1024 + c; hi: at bits 4..7, where 0x5400 | c is
-// 64 + c.  n: -(1024 + z), or -(64 + z).  Every step is exact.
+// 64 + c.  n: -(1024 + z) as it is stored, or -(64 + z).  Every step is exact.
 // The masks live in vector registers and the exponents in scalar ones: an
 // instruction takes one scalar and no literal besides, so mask and exponent
 // as constants would make two of each and-or.
@@ -469,12 +469,12 @@ struct Rows {
         f32x4 acc[NQ];
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) acc[nq] = f32x4{0, 0, 0, 0};
-        f16x2 z2 = {(_Float16)8.0f, (_Float16)8.0f};
+        f16x2 n1 = {(_Float16)-1032.0f, (_Float16)-1032.0f};
         if constexpr (!SYM) {
           const _Float16 z = __builtin_bit_cast(_Float16, (uint16_t)(kb[t].z[g / 2] >> (16 * (g & 1))));
-          z2 = f16x2{z, z};
+          n1 = f16x2{z, z};
         }
-        const f16x2 n1 = (_Float16)-1024.0f - z2, n2 = (_Float16)-64.0f - z2;
+        const f16x2 n2 = n1 + (_Float16)960.0f;
 #pragma unroll
         for (int st = g * SPG; st < (g + 1) * SPG; ++st) {
           const uint32_t d = kb[t].c[st], e = d >> 8;
@@ -494,7 +494,7 @@ struct Rows {
   }
 
   // Keys that no row of the tile sees: whatever their memory holds counts as
-  // value scale and zero point 0 (their scores are dropped in `weights`).
+  // value scale 0 and a finite zero point (their scores are dropped in `weights`).
   static __device__ __forceinline__ void clear_unseen(const Span& sp, int u, bool ok0, bool ok1,
                                                       ValueBlock<D, NG, SYM> (&vb)[2], int kg) {
 #pragma unroll
@@ -624,10 +624,9 @@ struct Rows {
       f16x2 n1[4], n2[4];   // by token pair
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const f16x2 z = SYM ? f16x2{(_Float16)8.0f, (_Float16)8.0f}
-                            : __builtin_bit_cast(f16x2, vb[i >> 1].z[SYM ? 0 : g][i & 1]);
-        n1[i] = (_Float16)-1024.0f - z;
-        n2[i] = (_Float16)-64.0f - z;
+        n1[i] = SYM ? f16x2{(_Float16)-1032.0f, (_Float16)-1032.0f}
+                    : __builtin_bit_cast(f16x2, vb[i >> 1].z[SYM ? 0 : g][i & 1]);
+        n2[i] = n1[i] + (_Float16)960.0f;
       }
 #pragma unroll
       for (int b = g * SPG; b < (g + 1) * SPG; ++b) {

@@ -1,11 +1,12 @@
 // Writing keys and values into the 4-bit cache, and reading them back.
 //
-// Both are one pass over the data and bound by it.  A lane holds 8 consecutive
-// channels of one (token, head) row: 16 bytes of 16-bit values, one dword of
-// codes; D / 8 lanes make a row (padded to 16 for D = 96).  A workgroup takes
-// the same head of consecutive tokens, so that the pieces of 16 bytes that a
-// token leaves in the value order are completed by the same workgroup, in the
-// L2 cache, for consecutive slots.
+// Both are one pass over the data.  A lane holds 8 consecutive channels of one
+// (token, head) row, of its key and of its value: 16 bytes of 16-bit values, one
+// dword of codes each; D / 8 lanes make a row (padded to 16 for D = 96).  Key and
+// value in one lane share the slot and the address and keep twice the loads
+// under way.  A workgroup takes the same head of consecutive tokens, so that the
+// pieces of 16 bytes that a token leaves in the value order are completed by
+// the same workgroup, in the L2 cache, for consecutive slots.
 #include "kv4.h"
 #include "stream_util.h"
 
@@ -13,6 +14,9 @@ namespace gq {
 namespace {
 
 using stream_util::dpp_f32;
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
 
@@ -49,15 +53,68 @@ __device__ __forceinline__ uint16_t group_scale(float hi, float lo, double n, fl
   return rd > 0.0 ? scale_to_f16(rd / n) : (uint16_t)0x3C00u;   // 1.0: an all-zero group
 }
 
-// round(x / S), half to even, for a 16-bit float x and an fp16 S: the quotient
-// of two 11-bit numbers is either k + 1/2 exactly or at least 2^-14 away from
-// it, so an fp32 quotient good to a few units in the last place decides every
-// case but the ties; one residual step (exact by FMA) makes those exact.
-// |x / S| beyond 64 is only ever clamped: it is cut there.
-__device__ __forceinline__ float div_round(float x, float S, float inv) {
-  float q = __builtin_amdgcn_fmed3f(x * inv, -64.0f, 64.0f);
+// round(x / S), half to even, for a 16-bit float x and an fp16 S, held in
+// lo .. hi (integers), as 1.5 2^23 + the result: the quotient of two 11-bit
+// numbers is either k + 1/2 exactly or at least 2^-14 away from it, so an fp32
+// quotient good to a few units in the last place decides every case but the
+// ties; one residual step (exact by FMA) makes those exact.  The sum rounds.
+__device__ __forceinline__ float div_round(float x, float S, float inv, float lo, float hi) {
+  float q = x * inv;
   q = __builtin_fmaf(__builtin_fmaf(-q, S, x), inv, q);
-  return __builtin_rintf(q);
+  return __builtin_amdgcn_fmed3f(q, lo, hi) + 12582912.0f;
+}
+
+__device__ __forceinline__ void widen(uint4 raw, int bf16, float (&x)[8]) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16 ? __uint_as_float(w[i] << 16) : f16_to_f32((uint16_t)(w[i] & 0xFFFFu));
+    x[2 * i + 1] = bf16 ? __uint_as_float(w[i] & 0xFFFF0000u) : f16_to_f32((uint16_t)(w[i] >> 16));
+  }
+}
+
+struct Quant {
+  uint16_t S;       // fp16 bits
+  int z;            // zero point (8: symmetric)
+  uint32_t codes;   // nibble at[i] is channel i's
+};
+
+// 8 channels of a row, the lanes of a group together.  at: where each code goes
+// in the dword, 4 bits each from the lowest.
+__device__ __forceinline__ Quant quantise(float (&x)[8], int sym, int g, uint32_t at) {
+  float hi = 0.0f, lo = 0.0f;
+  if (sym) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) hi = fmaxf(hi, fabsf(x[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) { hi = fmaxf(hi, x[i]); lo = fmaxf(lo, -x[i]); }
+    lo = group_max(lo, g);
+  }
+  hi = group_max(hi, g);
+  Quant r;
+  r.S = sym ? group_scale(hi, 0.0f, 7.0, 1.0f / 7.0f) : group_scale(hi, -lo, 15.0, 1.0f / 15.0f);
+  if (r.S == 0x7BFFu) {
+    // a saturated scale: infinities become finite, beyond any code all the same
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_fmed3f(x[i], -4194304.0f, 4194304.0f);
+    lo = fminf(lo, 4194304.0f);
+  }
+  const float S = f16_to_f32(r.S);
+  const float inv = __builtin_amdgcn_rcpf(S);
+  const float zf = sym ? 8.0f : div_round(lo, S, inv, 0.0f, 15.0f) - 12582912.0f;
+  r.z = (int)zf;
+  // the bits of 1.5 2^23 + n are 0x4B400000 + n: shifted sums of them leave the
+  // codes and a constant
+  uint32_t sum = (uint32_t)r.z * 0x11111111u, extra = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t sh = (at >> (4 * i)) & 15u;
+    sum += __float_as_uint(div_round(x[i], S, inv, -zf, 15.0f - zf)) << (4 * sh);
+    extra += 0x4B400000u << (4 * sh);
+  }
+  r.codes = sum - extra;
+  return r;
 }
 
 template <int D>
@@ -67,82 +124,34 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(
     Kv4Geo c) {
   constexpr int NS = D / 32, P = Row<D>::kPitch, L = Row<D>::kLanes;
   __shared__ uint32_t sv[kThreads];
-  const int is_v = blockIdx.z;
   const int head = blockIdx.y;
   const int lane = threadIdx.x % P;
   const int row = threadIdx.x / P;
   const int64_t t = (int64_t)blockIdx.x * Row<D>::kRows + row;
-  const bool live = t < tokens && lane < L;
-  uint4 raw = make_uint4(0, 0, 0, 0);
+  uint4 kr = make_uint4(0, 0, 0, 0), vr = kr;
   int64_t slot = -1;
-  if (live) {
-    const uint16_t* p = is_v ? v + t * v_ts + head * v_hs : k + t * k_ts + head * k_hs;
-    raw = *(const uint4*)(p + lane * 8);
+  if (t < tokens && lane < L) {
+    kr = *(const uint4*)(k + t * k_ts + head * k_hs + lane * 8);
+    vr = *(const uint4*)(v + t * v_ts + head * v_hs + lane * 8);
     slot = slots[t];
   }
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   float x[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16 ? bf16_to_f32(w[i] & 0xFFFFu) : f16_to_f32((uint16_t)(w[i] & 0xFFFFu));
-    x[2 * i + 1] = bf16 ? __uint_as_float(w[i] & 0xFFFF0000u) : f16_to_f32((uint16_t)(w[i] >> 16));
-  }
-  float hi = 0.0f, lo = 0.0f;
-  if (c.sym) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) hi = fmaxf(hi, fabsf(x[i]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) { hi = fmaxf(hi, x[i]); lo = fmaxf(lo, -x[i]); }
-    lo = group_max(lo, c.g);
-  }
-  hi = group_max(hi, c.g);
-  const uint16_t sh = c.sym ? group_scale(hi, 0.0f, 7.0, 1.0f / 7.0f)
-                            : group_scale(hi, -lo, 15.0, 1.0f / 15.0f);
-  const float S = f16_to_f32(sh);
-  const float inv = __builtin_amdgcn_rcpf(S);
-  // the zero point, and the range of round(x / S) that keeps codes in 0..15
-  const float z = c.sym ? 8.0f : fminf(fmaxf(div_round(lo, S, inv), 0.0f), 15.0f);
-  uint32_t q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    q[i] = (uint32_t)fminf(fmaxf(div_round(x[i], S, inv) + z, 0.0f), 15.0f);
-
-  const int64_t page = slot >> c.page_shift;
-  const bool ok = live && slot >= 0 && page < c.n_pages;
-  const int tp = (int)(slot & ((1 << c.page_shift) - 1));
-  uint8_t* blk = c.cache + (ok ? kv4_block_offset(c, page, head, tp) : 0);
-  if (is_v) blk += 8 * D + c.meta;
-  const int ts = tp & 15;
-  if (ok && (lane * 8) % c.g == 0) {   // first lane of a group: its parameters
-    const int gi = lane * 8 / c.g;
-    const uint16_t zh = __builtin_bit_cast(uint16_t, (_Float16)z);
-    uint16_t* m = (uint16_t*)(blk + 8 * D);
-    if (c.sym) {
-      m[gi * 16 + ts] = sh;
-    } else if (is_v) {
-      m += gi * 32 + (ts >> 2) * 8 + (ts & 3);
-      m[0] = sh;
-      m[4] = zh;
-    } else {
-      m[gi * 16 + ts] = sh;
-      m[16 * c.ng + ts * c.ng + gi] = zh;
-    }
-  }
-  if (!is_v) {
-    // nibbles 0, 4, 1, 5, 2, 6, 3, 7
-    const uint32_t d = q[0] | q[1] << 16 | q[2] << 4 | q[3] << 20 | q[4] << 8 | q[5] << 24 |
-                       q[6] << 12 | q[7] << 28;
-    if (ok) *(uint32_t*)(blk + ts * (D / 2) + ((lane & 3) * NS + (lane >> 2)) * 4) = d;
-    return;
-  }
-  // natural packed dword (bytes 4 lane .. of the row) -> bytes (m, b)
-  sv[threadIdx.x] = q[0] | q[1] << 4 | q[2] << 8 | q[3] << 12 | q[4] << 16 | q[5] << 20 |
-                    q[6] << 24 | q[7] << 28;
+  widen(kr, bf16, x);
+  const Quant qk = quantise(x, c.sym, c.g, 0x73625140u);
+  widen(vr, bf16, x);
+  const Quant qv = quantise(x, c.sym, c.g, 0x76543210u);
+  // natural order (bytes 4 lane .. of the row) -> bytes (m, b)
+  sv[threadIdx.x] = qv.codes;
   __syncthreads();
-  if (!ok) return;
+  const int64_t page = slot >> c.page_shift;
+  if (slot < 0 || page >= c.n_pages) return;
+  const int tp = (int)(slot & ((1 << c.page_shift) - 1));
+  uint8_t* blk = c.cache + kv4_block_offset(c, page, head, tp);
+  uint8_t* blv = blk + 8 * D + c.meta;
+  const int ts = tp & 15;
+  *(uint32_t*)(blk + ts * (D / 2) + ((lane & 3) * NS + (lane >> 2)) * 4) = qk.codes;
   const uint8_t* rowb = (const uint8_t*)(sv + row * P);
-  uint8_t* quad = blk + (ts >> 2) * (64 * NS) + (ts & 3) * NS;
+  uint8_t* quad = blv + (ts >> 2) * (64 * NS) + (ts & 3) * NS;
   for (int m = lane; m < 16; m += L) {
     uint8_t* o = quad + m * (4 * NS);
     if (NS == 2) {
@@ -157,6 +166,20 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(
                             rowb[64 * i + 32 + m] << 16 | (uint32_t)rowb[64 * i + 48 + m] << 24;
     }
   }
+  if ((lane * 8) % c.g == 0) {   // first lane of a group: its parameters
+    const int gi = lane * 8 / c.g;
+    uint16_t* mk = (uint16_t*)(blk + 8 * D);
+    uint16_t* mv = (uint16_t*)(blv + 8 * D);
+    mk[gi * 16 + ts] = qk.S;
+    if (c.sym) {
+      mv[gi * 16 + ts] = qv.S;
+    } else {
+      mk[16 * c.ng + ts * c.ng + gi] = kv4_zero_bits(qk.z);
+      mv += gi * 32 + (ts >> 2) * 8 + (ts & 3);
+      mv[0] = qv.S;
+      mv[4] = kv4_zero_bits(qv.z);
+    }
+  }
 }
 
 template <int D>
@@ -164,75 +187,89 @@ __global__ __launch_bounds__(kThreads) void kv4_read_kernel(Kv4Geo c, const int6
                                                           int64_t tokens, void* __restrict__ k,
                                                           void* __restrict__ v, gq_dtype odt) {
   constexpr int NS = D / 32, P = Row<D>::kPitch, L = Row<D>::kLanes;
-  const int is_v = blockIdx.z;
+  __shared__ uint32_t sv[kThreads];
   const int head = blockIdx.y;
   const int lane = threadIdx.x % P;
-  const int64_t t = (int64_t)blockIdx.x * Row<D>::kRows + threadIdx.x / P;
-  if (t >= tokens || lane >= L) return;
-  const int64_t slot = slots[t];
+  const int row = threadIdx.x / P;
+  const int64_t t = (int64_t)blockIdx.x * Row<D>::kRows + row;
+  const bool live = t < tokens && lane < L;
+  const int64_t slot = live ? slots[t] : -1;
   const int64_t page = slot >> c.page_shift;
-  const bool ok = slot >= 0 && page < c.n_pages;
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-  if (ok) {
+  uint8_t* rowb = (uint8_t*)(sv + row * P);
+  uint32_t kc = 0;
+  // 0 (S) times anything: a slot out of range reads as zeros
+  float S[2] = {0.0f, 0.0f}, z[2] = {8.0f, 8.0f};
+  if (slot >= 0 && page < c.n_pages) {
     const int tp = (int)(slot & ((1 << c.page_shift) - 1));
     const uint8_t* blk = c.cache + kv4_block_offset(c, page, head, tp);
-    if (is_v) blk += 8 * D + c.meta;
+    const uint8_t* blv = blk + 8 * D + c.meta;
     const int ts = tp & 15;
     const int gi = lane * 8 / c.g;
-    const uint16_t* m = (const uint16_t*)(blk + 8 * D);
-    float S, z = 8.0f;
+    kc = *(const uint32_t*)(blk + ts * (D / 2) + ((lane & 3) * NS + (lane >> 2)) * 4);
+    const uint16_t* mk = (const uint16_t*)(blk + 8 * D);
+    const uint16_t* mv = (const uint16_t*)(blv + 8 * D);
+    S[0] = f16_to_f32(mk[gi * 16 + ts]);
     if (c.sym) {
-      S = f16_to_f32(m[gi * 16 + ts]);
-    } else if (is_v) {
-      m += gi * 32 + (ts >> 2) * 8 + (ts & 3);
-      S = f16_to_f32(m[0]);
-      z = f16_to_f32(m[4]);
+      S[1] = f16_to_f32(mv[gi * 16 + ts]);
     } else {
-      S = f16_to_f32(m[gi * 16 + ts]);
-      z = f16_to_f32(m[16 * c.ng + ts * c.ng + gi]);
+      z[0] = kv4_zero(mk[16 * c.ng + ts * c.ng + gi]);
+      mv += gi * 32 + (ts >> 2) * 8 + (ts & 3);
+      S[1] = f16_to_f32(mv[0]);
+      z[1] = kv4_zero(mv[4]);
     }
-    uint32_t q[8];
-    if (!is_v) {
-      const uint32_t d = *(const uint32_t*)(blk + ts * (D / 2) + ((lane & 3) * NS + (lane >> 2)) * 4);
+    // bytes (m, b) -> natural order, byte 16 b + m of the row
+    const uint8_t* quad = blv + (ts >> 2) * (64 * NS) + (ts & 3) * NS;
+    for (int m = lane; m < 16; m += L) {
+      const uint8_t* o = quad + m * (4 * NS);
+      uint32_t w[(NS + 3) / 4];
+      if (NS == 2) {
+        w[0] = *(const uint16_t*)o;
+      } else if (NS == 3) {
+        w[0] = o[0] | o[1] << 8 | (uint32_t)o[2] << 16;
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = (d >> (4 * ((i >> 1) + 4 * (i & 1)))) & 15u;
+        for (int i = 0; i < NS / 4; ++i) w[i] = ((const uint32_t*)o)[i];
+      }
+#pragma unroll
+      for (int b = 0; b < NS; ++b) rowb[16 * b + m] = (uint8_t)(w[b / 4] >> (8 * (b % 4)));
+    }
+  }
+  __syncthreads();
+  if (!live) return;
+  const uint32_t vc = sv[threadIdx.x];
+  const int64_t o = (t * c.hkv + head) * D + lane * 8;
+#pragma unroll
+  for (int is_v = 0; is_v < 2; ++is_v) {
+    const float nz = -z[is_v] * S[is_v];
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = is_v ? i : (i >> 1) + 4 * (i & 1);         // nibble of channel i
+      const uint32_t c = ((is_v ? vc : kc) >> (at & 1 ? 4 : 0)) & 0x0F0F0F0Fu;
+      x[i] = __builtin_fmaf(S[is_v], (float)(c >> (8 * (at >> 1)) & 0xFFu), nz);   // exact: 11 bits times 5
+    }
+    void* out = is_v ? v : k;
+    if (odt == GQ_F32) {
+      float4* p = (float4*)((float*)out + o);
+      p[0] = make_float4(x[0], x[1], x[2], x[3]);
+      p[1] = make_float4(x[4], x[5], x[6], x[7]);
     } else {
-      // bytes 4 lane .. 4 lane + 3 of the row: m = 4 (lane % 4) + i, b = lane / 4
-      const uint8_t* o = blk + (ts >> 2) * (64 * NS) + (ts & 3) * NS + (lane & 3) * (16 * NS) + (lane >> 2);
+      uint32_t h[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t b = o[i * 4 * NS];
-        q[2 * i] = b & 15u;
-        q[2 * i + 1] = b >> 4;
+        if (odt == GQ_BF16)
+          h[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)x[2 * i], (__bf16)x[2 * i + 1]});
+        else
+          h[i] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)x[2 * i], (_Float16)x[2 * i + 1]});
       }
+      *(uint4*)((uint16_t*)out + o) = make_uint4(h[0], h[1], h[2], h[3]);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = S * ((float)q[i] - z);   // exact: 11 bits times 5
-  }
-  const int64_t o = (t * c.hkv + head) * D + lane * 8;
-  void* out = is_v ? v : k;
-  if (odt == GQ_F32) {
-    float4* p = (float4*)((float*)out + o);
-    p[0] = make_float4(x[0], x[1], x[2], x[3]);
-    p[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-    uint32_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t a = odt == GQ_BF16 ? f32_to_bf16_rne(x[2 * i]) : stream_util::f32_to_f16_rne(x[2 * i]);
-      const uint32_t b =
-          odt == GQ_BF16 ? f32_to_bf16_rne(x[2 * i + 1]) : stream_util::f32_to_f16_rne(x[2 * i + 1]);
-      h[i] = a | (b << 16);
-    }
-    *(uint4*)((uint16_t*)out + o) = make_uint4(h[0], h[1], h[2], h[3]);
   }
 }
 
 template <int D>
 dim3 grid_of(int64_t tokens, int heads) {
-  return dim3((unsigned)((tokens + Row<D>::kRows - 1) / Row<D>::kRows), (unsigned)heads, 2);
+  return dim3((unsigned)((tokens + Row<D>::kRows - 1) / Row<D>::kRows), (unsigned)heads);
 }
 
 }  // namespace

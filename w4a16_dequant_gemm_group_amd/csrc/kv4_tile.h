@@ -102,12 +102,12 @@ struct Tile {
     const bool live = c.ok && c.pos + m >= sp.lo && c.pos + m < sp.hi;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      f16x2 z2 = {(_Float16)8.0f, (_Float16)8.0f};
+      f16x2 n1 = {(_Float16)-1032.0f, (_Float16)-1032.0f};
       if constexpr (!SYM) {
         const _Float16 z = __builtin_bit_cast(_Float16, (uint16_t)(live ? c.p[g][1] : 0u));
-        z2 = f16x2{z, z};
+        n1 = f16x2{z, z};
       }
-      const f16x2 n1 = (_Float16)-1024.0f - z2, n2 = (_Float16)-64.0f - z2;
+      const f16x2 n2 = n1 + (_Float16)960.0f;
 #pragma unroll
       for (int s = g * SPG; s < (g + 1) * SPG; ++s) {
         const uint32_t d = c.d[s], e = d >> 8;
@@ -163,10 +163,9 @@ struct Tile {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         S2[i] = f16x2{(_Float16)(lo_f16(c.p[g][i]) * inv), (_Float16)(hi_f16(c.p[g][i]) * inv)};
-        f16x2 z = {(_Float16)8.0f, (_Float16)8.0f};
-        if constexpr (!SYM) z = __builtin_bit_cast(f16x2, c.p[g][2 + i]);
-        n1[i] = (_Float16)-1024.0f - z;
-        n2[i] = (_Float16)-64.0f - z;
+        n1[i] = f16x2{(_Float16)-1032.0f, (_Float16)-1032.0f};
+        if constexpr (!SYM) n1[i] = __builtin_bit_cast(f16x2, c.p[g][2 + i]);
+        n2[i] = n1[i] + (_Float16)960.0f;
       }
 #pragma unroll
       for (int b = g * SPG; b < (g + 1) * SPG; ++b) {
