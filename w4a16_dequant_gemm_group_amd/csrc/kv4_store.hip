@@ -182,94 +182,120 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(
   }
 }
 
-template <int D>
+// U rows per lane: the loads of all of them are under way together.
+template <int D, int U>
 __global__ __launch_bounds__(kThreads) void kv4_read_kernel(Kv4Geo c, const int64_t* __restrict__ slots,
                                                           int64_t tokens, void* __restrict__ k,
                                                           void* __restrict__ v, gq_dtype odt) {
   constexpr int NS = D / 32, P = Row<D>::kPitch, L = Row<D>::kLanes;
-  __shared__ uint32_t sv[kThreads];
+  constexpr int kPieces = (16 + L - 1) / L;        // pieces (m, all b) of a value row per lane
+  __shared__ uint32_t sv[U][kThreads];
   const int head = blockIdx.y;
   const int lane = threadIdx.x % P;
   const int row = threadIdx.x / P;
-  const int64_t t = (int64_t)blockIdx.x * Row<D>::kRows + row;
-  const bool live = t < tokens && lane < L;
-  const int64_t slot = live ? slots[t] : -1;
-  const int64_t page = slot >> c.page_shift;
-  uint8_t* rowb = (uint8_t*)(sv + row * P);
-  uint32_t kc = 0;
+  const int64_t t0 = (int64_t)blockIdx.x * (U * Row<D>::kRows) + row;
+  int64_t slot[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t t = t0 + u * Row<D>::kRows;
+    slot[u] = t < tokens && lane < L ? slots[t] : -1;
+  }
+  uint32_t kc[U], vw[U][kPieces][(NS + 3) / 4];
   // 0 (S) times anything: a slot out of range reads as zeros
-  float S[2] = {0.0f, 0.0f}, z[2] = {8.0f, 8.0f};
-  if (slot >= 0 && page < c.n_pages) {
-    const int tp = (int)(slot & ((1 << c.page_shift) - 1));
+  uint16_t S[U][2], z[U][2];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t page = slot[u] >> c.page_shift;
+    kc[u] = 0;
+    S[u][0] = S[u][1] = 0;
+    z[u][0] = z[u][1] = kv4_zero_bits(8);
+    if (slot[u] < 0 || page >= c.n_pages) continue;
+    const int tp = (int)(slot[u] & ((1 << c.page_shift) - 1));
     const uint8_t* blk = c.cache + kv4_block_offset(c, page, head, tp);
     const uint8_t* blv = blk + 8 * D + c.meta;
     const int ts = tp & 15;
     const int gi = lane * 8 / c.g;
-    kc = *(const uint32_t*)(blk + ts * (D / 2) + ((lane & 3) * NS + (lane >> 2)) * 4);
-    const uint16_t* mk = (const uint16_t*)(blk + 8 * D);
-    const uint16_t* mv = (const uint16_t*)(blv + 8 * D);
-    S[0] = f16_to_f32(mk[gi * 16 + ts]);
-    if (c.sym) {
-      S[1] = f16_to_f32(mv[gi * 16 + ts]);
-    } else {
-      z[0] = kv4_zero(mk[16 * c.ng + ts * c.ng + gi]);
-      mv += gi * 32 + (ts >> 2) * 8 + (ts & 3);
-      S[1] = f16_to_f32(mv[0]);
-      z[1] = kv4_zero(mv[4]);
-    }
-    // bytes (m, b) -> natural order, byte 16 b + m of the row
+    kc[u] = *(const uint32_t*)(blk + ts * (D / 2) + ((lane & 3) * NS + (lane >> 2)) * 4);
     const uint8_t* quad = blv + (ts >> 2) * (64 * NS) + (ts & 3) * NS;
-    for (int m = lane; m < 16; m += L) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int m = lane + i * L;
+      if (16 % L != 0 && m >= 16) continue;
       const uint8_t* o = quad + m * (4 * NS);
-      uint32_t w[(NS + 3) / 4];
       if (NS == 2) {
-        w[0] = *(const uint16_t*)o;
+        vw[u][i][0] = *(const uint16_t*)o;
       } else if (NS == 3) {
-        w[0] = o[0] | o[1] << 8 | (uint32_t)o[2] << 16;
+        vw[u][i][0] = o[0] | o[1] << 8 | (uint32_t)o[2] << 16;
       } else {
 #pragma unroll
-        for (int i = 0; i < NS / 4; ++i) w[i] = ((const uint32_t*)o)[i];
+        for (int j = 0; j < NS / 4; ++j) vw[u][i][j] = ((const uint32_t*)o)[j];
       }
+    }
+    const uint16_t* mk = (const uint16_t*)(blk + 8 * D);
+    const uint16_t* mv = (const uint16_t*)(blv + 8 * D);
+    S[u][0] = mk[gi * 16 + ts];
+    if (c.sym) {
+      S[u][1] = mv[gi * 16 + ts];
+    } else {
+      z[u][0] = mk[16 * c.ng + ts * c.ng + gi];
+      mv += gi * 32 + (ts >> 2) * 8 + (ts & 3);
+      S[u][1] = mv[0];
+      z[u][1] = mv[4];
+    }
+  }
+  // bytes (m, b) -> natural order, byte 16 b + m of the row
 #pragma unroll
-      for (int b = 0; b < NS; ++b) rowb[16 * b + m] = (uint8_t)(w[b / 4] >> (8 * (b % 4)));
+  for (int u = 0; u < U; ++u) {
+    uint8_t* rowb = (uint8_t*)(sv[u] + row * P);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int m = lane + i * L;
+      if (lane >= L || m >= 16) continue;
+#pragma unroll
+      for (int b = 0; b < NS; ++b) rowb[16 * b + m] = (uint8_t)(vw[u][i][b / 4] >> (8 * (b % 4)));
     }
   }
   __syncthreads();
-  if (!live) return;
-  const uint32_t vc = sv[threadIdx.x];
-  const int64_t o = (t * c.hkv + head) * D + lane * 8;
 #pragma unroll
-  for (int is_v = 0; is_v < 2; ++is_v) {
-    const float nz = -z[is_v] * S[is_v];
-    float x[8];
+  for (int u = 0; u < U; ++u) {
+    const int64_t t = t0 + u * Row<D>::kRows;
+    if (t >= tokens || lane >= L) break;
+    const uint32_t vc = sv[u][threadIdx.x];
+    const int64_t o = (t * c.hkv + head) * D + lane * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = is_v ? i : (i >> 1) + 4 * (i & 1);         // nibble of channel i
-      const uint32_t c = ((is_v ? vc : kc) >> (at & 1 ? 4 : 0)) & 0x0F0F0F0Fu;
-      x[i] = __builtin_fmaf(S[is_v], (float)(c >> (8 * (at >> 1)) & 0xFFu), nz);   // exact: 11 bits times 5
-    }
-    void* out = is_v ? v : k;
-    if (odt == GQ_F32) {
-      float4* p = (float4*)((float*)out + o);
-      p[0] = make_float4(x[0], x[1], x[2], x[3]);
-      p[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-      uint32_t h[4];
+    for (int is_v = 0; is_v < 2; ++is_v) {
+      const float Sf = f16_to_f32(S[u][is_v]), nz = -kv4_zero(z[u][is_v]) * Sf;
+      float x[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (odt == GQ_BF16)
-          h[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)x[2 * i], (__bf16)x[2 * i + 1]});
-        else
-          h[i] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)x[2 * i], (_Float16)x[2 * i + 1]});
+      for (int i = 0; i < 8; ++i) {
+        const int at = is_v ? i : (i >> 1) + 4 * (i & 1);         // nibble of channel i
+        const uint32_t q = ((is_v ? vc : kc[u]) >> (at & 1 ? 4 : 0)) & 0x0F0F0F0Fu;
+        x[i] = __builtin_fmaf(Sf, (float)(q >> (8 * (at >> 1)) & 0xFFu), nz);   // exact: 11 bits times 5
       }
-      *(uint4*)((uint16_t*)out + o) = make_uint4(h[0], h[1], h[2], h[3]);
+      void* out = is_v ? v : k;
+      if (odt == GQ_F32) {
+        float4* p = (float4*)((float*)out + o);
+        p[0] = make_float4(x[0], x[1], x[2], x[3]);
+        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+      } else {
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (odt == GQ_BF16)
+            h[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)x[2 * i], (__bf16)x[2 * i + 1]});
+          else
+            h[i] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)x[2 * i], (_Float16)x[2 * i + 1]});
+        }
+        *(uint4*)((uint16_t*)out + o) = make_uint4(h[0], h[1], h[2], h[3]);
+      }
     }
   }
 }
 
 template <int D>
-dim3 grid_of(int64_t tokens, int heads) {
-  return dim3((unsigned)((tokens + Row<D>::kRows - 1) / Row<D>::kRows), (unsigned)heads);
+dim3 grid_of(int64_t tokens, int heads, int u) {
+  const int64_t n = u * Row<D>::kRows;
+  return dim3((unsigned)((tokens + n - 1) / n), (unsigned)heads);
 }
 
 }  // namespace
@@ -278,7 +304,7 @@ hipError_t launch_kv4_write(const void* k, int64_t k_ts, int64_t k_hs, const voi
                             int64_t v_hs, gq_dtype dt, int64_t tokens, const int64_t* slots,
                             const Kv4Geo& c, hipStream_t s) {
 #define GQ_KV4_WRITE(D)                                                                        \
-  hipLaunchKernelGGL(kv4_write_kernel<D>, grid_of<D>(tokens, c.hkv), dim3(kThreads), 0, s,     \
+  hipLaunchKernelGGL(kv4_write_kernel<D>, grid_of<D>(tokens, c.hkv, 1), dim3(kThreads), 0, s,  \
                      (const uint16_t*)k, k_ts, k_hs, (const uint16_t*)v, v_ts, v_hs,           \
                      (int)(dt == GQ_BF16), tokens, slots, c)
   if (c.d == 64) GQ_KV4_WRITE(64);
@@ -291,13 +317,21 @@ hipError_t launch_kv4_write(const void* k, int64_t k_ts, int64_t k_hs, const voi
 
 hipError_t launch_kv4_read(const Kv4Geo& c, const int64_t* slots, int64_t tokens, void* k, void* v,
                            gq_dtype odt, hipStream_t s) {
-#define GQ_KV4_READ(D)                                                                            \
-  hipLaunchKernelGGL(kv4_read_kernel<D>, grid_of<D>(tokens, c.hkv), dim3(kThreads), 0, s, c, slots, \
-                     tokens, k, v, odt)
-  if (c.d == 64) GQ_KV4_READ(64);
-  else if (c.d == 96) GQ_KV4_READ(96);
-  else if (c.d == 128) GQ_KV4_READ(128);
-  else GQ_KV4_READ(256);
+  // few rows: one per lane, spread over the most workgroups
+  const bool many = tokens * c.hkv >= 65536;
+#define GQ_KV4_READ(D)                                                                                \
+  if (many)                                                                                           \
+    hipLaunchKernelGGL((kv4_read_kernel<D, 4>), grid_of<D>(tokens, c.hkv, 4), dim3(kThreads), 0, s, c, \
+                       slots, tokens, k, v, odt);                                                     \
+  else                                                                                                \
+    hipLaunchKernelGGL((kv4_read_kernel<D, 1>), grid_of<D>(tokens, c.hkv, 1), dim3(kThreads), 0, s, c, \
+                       slots, tokens, k, v, odt)
+  switch (c.d) {
+    case 64: GQ_KV4_READ(64); break;
+    case 96: GQ_KV4_READ(96); break;
+    case 128: GQ_KV4_READ(128); break;
+    default: GQ_KV4_READ(256); break;
+  }
 #undef GQ_KV4_READ
   return hipGetLastError();
 }
