@@ -78,6 +78,7 @@ struct Kv4Attn {
   // the split over workgroups
   int32_t workers;                   // workgroups of a split launch
   int32_t grain;                     // log2 of the keys of a tile of the split
+  int32_t over;                      // what a row tile costs besides its keys, in such tiles
   int32_t few;                       // few row tiles per sequence: lanes share the sequences
   int32_t grid_q;                    // row tiles in an unsplit launch's grid
   int32_t* meta;                     // [workers][8] which row tiles were left open

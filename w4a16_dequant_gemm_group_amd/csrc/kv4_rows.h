@@ -78,8 +78,10 @@ __device__ __forceinline__ int64_t out_row(const Kv4Attn& a, const Seq& s, int h
   return (int64_t)(s.q0 + tok) * a.hq + h * a.r + row - tok * a.r;
 }
 
-// The keys that row tile qt can see: positions lo .. hi - 1, tiles t0 ..
-// t0 + cnt - 1 of 2^grain keys (one at least: a row without keys is written too).
+// The keys that row tile qt can see: positions lo .. hi - 1, in tiles of 2^grain
+// keys from tile t0 on.  cnt: these tiles after `over` that hold no keys and
+// stand for the work that a row tile is besides (a row without keys is written
+// too), so that the split evens out both.
 struct Span {
   int p0, p1;   // positions of the first and last query
   int lo, hi, t0, cnt;
@@ -97,8 +99,12 @@ __device__ __forceinline__ Span get_span(const Kv4Attn& a, const Seq& s, int qt)
   p.lo = a.window > 0 && p.p0 - a.window + 1 > 0 ? p.p0 - a.window + 1 : 0;
   p.t0 = p.lo >> a.grain;
   const int t1 = (p.hi + (1 << a.grain) - 1) >> a.grain;
-  p.cnt = t1 > p.t0 ? t1 - p.t0 : 1;
+  p.cnt = a.over + (t1 > p.t0 ? t1 - p.t0 : 0);
   return p;
+}
+// Position where tile j of a span begins.
+__device__ __forceinline__ int64_t tile_start(const Kv4Attn& a, const Span& sp, int j) {
+  return (int64_t)(sp.t0 + (j > a.over ? j - a.over : 0)) << a.grain;
 }
 
 // Where the split stands: sequence, head, row tile, and the key tiles of the
@@ -656,8 +662,8 @@ struct Rows {
                                        int qt, int j0, int j1, uint8_t* smem, int wave, int m, int kg) {
     const PageRow row = page_row(a, b);
     const int ps = a.c.page_shift;
-    int u = (sp.t0 + j0) << a.grain;
-    const int64_t cut = (int64_t)(sp.t0 + j1) << a.grain;
+    int u = (int)tile_start(a, sp, j0);
+    const int64_t cut = tile_start(a, sp, j1);
     const int end = cut < sp.hi ? (int)cut : sp.hi;
     if (u < sp.lo) u = sp.lo & ~(kTile - 1);   // only the first tile can hold keys before the span
     u += wave * kUnit;

@@ -24,16 +24,20 @@ constexpr int kTK = 64;   // keys per tile
 // matrix products.
 constexpr int tile_waves(int d) { return d > 128 ? 4 : 8; }
 
-template <int D, int NG, bool SYM>
+template <int D, int NG, bool SYM, bool SPLIT>
 struct Tile {
   static constexpr int NS = D / 32, SPG = NS / NG;
   static constexpr int NW = tile_waves(D);
   static constexpr int TQ = NW * 32;                  // rows of a workgroup
   static constexpr int KP = D * 2 + 16;               // LDS row of a key: padded, 16 lanes
   static constexpr int VP = kTK * 2 + 16;             //   reading 16 rows hit all banks
-  static constexpr int kScale = kTK * KP + D * VP;    // key scales fp16 [NG][2][2][16]
-  static constexpr int kEx = kScale + NG * kTK * 2;   // floats {E, 2^-E} of the values' blocks
-  static constexpr int kBuf = kEx + 32;               // bytes of one buffer
+  // How the keys go to the matrix cores, exactly either way: as the integers
+  // c - z, with a scale per group applied to the scores (SPLIT false), or as
+  // x^ / 2^E in two fp16 parts (true).
+  static constexpr int kV = kTK * KP * (SPLIT ? 2 : 1);   // the values, behind the keys and their lower parts
+  static constexpr int kScale = kV + D * VP;              // key scales fp16 [NG][2][2][16]
+  static constexpr int kEx = kScale + (SPLIT ? 0 : NG * kTK * 2);   // floats {E, 2^-E} of the values' blocks of
+  static constexpr int kBuf = kEx + 48;                   //   16, 2^E of the keys'; bytes of one buffer
 
   f16x8 q[D / 16];
   float A, mref, l;
@@ -95,11 +99,39 @@ struct Tile {
     return x > y ? x : y;
   }
 
-  // Keys: the exact integers c - z; their scales wait for the finished scores.
-  // Keys that no row sees count as zeros, whatever their memory holds.
-  static __device__ __forceinline__ void expand_k(const Nibbles& nib, Codes& c, const Span& sp, uint8_t* buf, int blk, int m,
-                                                  int kg) {
+  // Exponent field of the largest of the wave's fp16 scales, and 2^-E for it; E
+  // = 0 where all are subnormal: they stay as they are.
+  static __device__ __forceinline__ uint32_t top_exponent(uint32_t top) { return wave_max(top) >> 10; }
+  static __device__ __forceinline__ float pow2_neg(uint32_t e) {
+    return __uint_as_float((e ? 142 - e : 127) << 23);
+  }
+
+  // Keys.  Parts: x^ / 2^E as fp16, E the exponent of the largest scale of the
+  // 16, and what its rounding left, as fp16 too: together x^ to 2^-22.  2^E
+  // comes back in the factor of the scores.  Keys that no row sees count as
+  // zeros, whatever their memory holds.
+  static __device__ __forceinline__ void expand_k(const Nibbles& nib, Codes& c, const Span& sp, uint8_t* buf,
+                                                  int blk, int m, int kg) {
     const bool live = c.ok && c.pos + m >= sp.lo && c.pos + m < sp.hi;
+    uint32_t top = 0;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      c.p[g][0] = live ? c.p[g][0] : 0u;
+      top = c.p[g][0] > top ? c.p[g][0] : top;
+    }
+    float inv = 1.0f;
+    if constexpr (SPLIT) {
+      const uint32_t e = top_exponent(top);
+      inv = pow2_neg(e);
+      if (m == 0 && kg == 0) ((float*)(buf + kEx))[8 + blk] = __uint_as_float((e ? 112 + e : 127) << 23);
+    } else if (kg == 0) {
+      // scale of token m: the lanes of one result half take 16 tokens of 32 in
+      // the order 8 (i / 4) + 4 half + i % 4
+      const int r = (blk & 1) * 16 + m;
+      uint16_t* sc = (uint16_t*)(buf + kScale) + (blk >> 1) * 32 + ((r >> 2) & 1) * 16 + (r >> 3) * 4 + (r & 3);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) sc[g * kTK] = (uint16_t)c.p[g][0];
+    }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       f16x2 n1 = {(_Float16)-1032.0f, (_Float16)-1032.0f};
@@ -108,20 +140,25 @@ struct Tile {
         n1 = f16x2{z, z};
       }
       const f16x2 n2 = n1 + (_Float16)960.0f;
+      const _Float16 S = (_Float16)(lo_f16(c.p[g][0]) * inv);
+      const f16x2 S2 = {S, S};
 #pragma unroll
       for (int s = g * SPG; s < (g + 1) * SPG; ++s) {
-        const uint32_t d = c.d[s], e = d >> 8;
-        const u32x4 w = {nib.lo(d, n1), nib.hi(d, n2), nib.lo(e, n1), nib.hi(e, n2)};
-        *(u32x4*)(buf + (blk * 16 + m) * KP + s * 64 + kg * 16) = w;
-      }
-    }
-    // scale of token m: the lanes of one result half take 16 tokens of 32 in
-    // the order 8 (i / 4) + 4 half + i % 4
-    if (kg == 0) {
-      const int r = (blk & 1) * 16 + m;
-      uint16_t* sc = (uint16_t*)(buf + kScale) + (blk >> 1) * 32 + ((r >> 2) & 1) * 16 + (r >> 3) * 4 + (r & 3);
+        const uint32_t d = c.d[s], d8 = d >> 8;
+        u32x4 w = {nib.lo(d, n1), nib.hi(d, n2), nib.lo(d8, n1), nib.hi(d8, n2)};
+        uint8_t* o = buf + (blk * 16 + m) * KP + s * 64 + kg * 16;
+        if constexpr (SPLIT) {
+          u32x4 low;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) sc[g * kTK] = live ? (uint16_t)c.p[g][0] : (uint16_t)0;
+          for (int i = 0; i < 4; ++i) {
+            const f16x2 k = __builtin_bit_cast(f16x2, (uint32_t)w[i]), h = k * S2;
+            w[i] = __builtin_bit_cast(uint32_t, h);
+            low[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(k, S2, -h));
+          }
+          *(u32x4*)(o + kTK * KP) = low;
+        }
+        *(u32x4*)o = w;
+      }
     }
   }
 
@@ -145,18 +182,15 @@ struct Tile {
         top = y > top ? y : top;
       }
     }
-    top = wave_max(top);
-    // exponent field of the largest scale; where all are subnormal they stay
-    // as they are
-    const uint32_t e = top >> 10;
-    const float inv = __uint_as_float((e ? 142 - e : 127) << 23);
+    const uint32_t e = top_exponent(top);
+    const float inv = pow2_neg(e);
     if (m == 0 && kg == 0) {
       float* ex = (float*)(buf + kEx);
       // -inf takes keys that do not exist out of the softmax
       ex[blk] = c.ok ? (e ? (float)((int)e - 15) : 0.0f) : kNegInf;
       ex[4 + blk] = inv;
     }
-    uint8_t* vb = buf + kTK * KP + blk * 32 + (kg & 1) * 16 + (kg >> 1) * 8;
+    uint8_t* vb = buf + kV + blk * 32 + (kg & 1) * 16 + (kg >> 1) * 8;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       f16x2 S2[2], n1[2], n2[2];
@@ -227,29 +261,82 @@ struct Tile {
   }
 
   // One tile of 64 keys from position u on: scores, weights, sums.
+  //
+  // The order is written out, product by product, and held by the scheduling
+  // fences (left alone, the scheduler saves registers and waits out the latency
+  // of every read of LDS, one read per product): operands are read kAhead
+  // products before their use, and the vector work that is independent of a
+  // product stands behind it, where it runs beside the matrix unit: the scales
+  // of one run of scores beside the next run's products, the exponentials of
+  // 16 keys beside the products of the 16 before.
   __device__ __forceinline__ void attend(const Kv4Attn& a, const Seq& s, int row0, int u, const uint8_t* buf,
                                          int n, int hf) {
+    constexpr int kAhead = 4;
+    f16x8 ring[kAhead];
     f32x16 x[2];
+    if constexpr (SPLIT) {
+      // both halves of the keys, their lower parts, then the next channels
+      constexpr int kAll = D / 4;
+      auto read = [&](int r) {
+        return *(const f16x8*)(buf + ((r >> 1 & 1) * kTK + 32 * (r & 1) + n) * KP + (r / 4) * 32 + hf * 16);
+      };
 #pragma unroll
-    for (int tt = 0; tt < 2; ++tt)
+      for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        f32x16 acc;
+        for (int i = 0; i < 16; ++i) x[tt][i] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+      for (int r = 0; r < kAhead; ++r) ring[r] = read(r);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int st = 2 * g * SPG; st < 2 * (g + 1) * SPG; ++st) {
-          const f16x8 kf = *(const f16x8*)(buf + (32 * tt + n) * KP + st * 32 + hf * 16);
-          acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[st], acc, 0, 0, 0);
-        }
-        const f16x8* sc = (const f16x8*)(buf + kScale + g * (kTK * 2) + tt * 64 + hf * 32);
-        const f16x8 s0 = sc[0], s1 = sc[1];
+      for (int r = 0; r < kAll; ++r) {
+        x[r & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[r % kAhead], q[r / 4], x[r & 1], 0, 0, 0);
+        if (r + kAhead < kAll) ring[r % kAhead] = read(r + kAhead);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+      // runs of products with one scale per key: (half of the keys, group)
+      constexpr int kRun = 2 * SPG, kRuns = 2 * NG, kAll = kRun * kRuns;
+      auto read = [&](int r) {
+        const int tt = r / (kRun * NG), st = r % (kRun * NG);
+        return *(const f16x8*)(buf + (32 * tt + n) * KP + st * 32 + hf * 16);
+      };
+      f32x16 acc[2];
+      f16x8 sc[2][2];
+      // elements from .. to - 1 of run i's scores, scaled
+      auto scale = [&](int i, int from, int to) {
+        const int tt = i / NG, g = i % NG;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float S = (float)(i < 8 ? s0[i & 7] : s1[i & 7]);
-          x[tt][i] = g == 0 ? S * acc[i] : __builtin_fmaf(S, acc[i], x[tt][i]);
+        for (int e = 0; e < 16; ++e)
+          if (e >= from && e < to)
+            x[tt][e] = __builtin_fmaf((float)sc[i & 1][e >> 3][e & 7], acc[i & 1][e], g == 0 ? 0.0f : x[tt][e]);
+      };
+#pragma unroll
+      for (int r = 0; r < kAhead; ++r) ring[r] = read(r);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < kRuns; ++i) {
+        const f16x8* sp = (const f16x8*)(buf + kScale + (i % NG) * (kTK * 2) + (i / NG) * 64 + hf * 32);
+        sc[i & 1][0] = sp[0];
+        sc[i & 1][1] = sp[1];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i & 1][e] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < kRun; ++st) {
+          const int r = i * kRun + st;
+          acc[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[r % kAhead], q[r % (kRun * NG)], acc[i & 1], 0, 0, 0);
+          if (r + kAhead < kAll) ring[r % kAhead] = read(r + kAhead);
+          if (i > 0) scale(i - 1, 16 * st / kRun, 16 * (st + 1) / kRun);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
+      scale(kRuns - 1, 0, 16);
+    }
+    const uint8_t* vb = buf + kV;
+    auto read_v = [&](int r) {   // 16 keys r / NS, channels 32 (r % NS) ..
+      return *(const f16x8*)(vb + (32 * (r % NS) + n) * VP + (r / NS) * 32 + hf * 16);
+    };
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) ring[r] = read_v(r);
     // whether every row of the wave sees all 64 keys
     const int rows = s.n * a.r;
     const int lastrow = row0 + 32 < rows ? row0 + 31 : rows - 1;
@@ -268,16 +355,21 @@ struct Tile {
           x[tt][i] = j <= last && j >= first ? x[tt][i] : kNegInf;
         }
     }
-    // per 16 keys, P gets the factor 2^E of their values
+    // per 16 keys, the scores have the factor 2^E of the keys and P that of the values
     const float4 ev = *(const float4*)(buf + kEx), ei = *(const float4*)(buf + kEx + 16);
     const float evv[4] = {ev.x, ev.y, ev.z, ev.w}, eiv[4] = {ei.x, ei.y, ei.z, ei.w};
+    float Ab[4] = {A, A, A, A};
+    if constexpr (SPLIT) {
+      const float4 ek = *(const float4*)(buf + kEx + 32);
+      Ab[0] *= ek.x; Ab[1] *= ek.y; Ab[2] *= ek.z; Ab[3] *= ek.w;
+    }
     float top = kNegInf;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       float t = x[b >> 1][8 * (b & 1)];
 #pragma unroll
       for (int i = 1; i < 8; ++i) t = fmaxf(t, x[b >> 1][8 * (b & 1) + i]);
-      top = fmaxf(top, __builtin_fmaf(t, A, evv[b]));
+      top = fmaxf(top, __builtin_fmaf(t, Ab[b], evv[b]));
     }
     if (__any(top > mref + kSlack)) {
       top = fmaxf(top, __shfl_xor(top, 32));
@@ -290,26 +382,31 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] *= f;
     }
-    f16x8 pw[4];
+    const float base = mref == kNegInf ? 0.0f : mref;
+    f16x8 pw[2];
+    float sum[2];
+    // weights from .. to - 1 of 16 keys' 8 in this lane
+    auto weigh = [&](int b, int from, int to) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const float nm = evv[b] - (mref == kNegInf ? 0.0f : mref);
-      float sum = 0.0f;
+      for (int i = 0; i < 8; ++i)
+        if (i >= from && i < to) {
+          const float e = exp2_hw(__builtin_fmaf(x[b >> 1][8 * (b & 1) + i], Ab[b], evv[b] - base));
+          sum[b & 1] = i == 0 ? e : sum[b & 1] + e;
+          pw[b & 1][i] = (_Float16)e;
+          if (i == 7) l = __builtin_fmaf(sum[b & 1], eiv[b], l);
+        }
+    };
+    weigh(0, 0, 8);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float e = exp2_hw(__builtin_fmaf(x[b >> 1][8 * (b & 1) + i], A, nm));
-        sum += e;
-        pw[b][i] = (_Float16)e;
-      }
-      l = __builtin_fmaf(sum, eiv[b], l);
-    }
-    const uint8_t* vb = buf + kTK * KP;
-#pragma unroll
-    for (int st = 0; st < 4; ++st)
+    for (int b = 0; b < 4; ++b)
 #pragma unroll
       for (int d = 0; d < NS; ++d) {
-        const f16x8 vf = *(const f16x8*)(vb + (32 * d + n) * VP + st * 32 + hf * 16);
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pw[st], o[d], 0, 0, 0);
+        const int r = b * NS + d;
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[r % kAhead], pw[b & 1], o[d], 0, 0, 0);
+        if (r + kAhead < 4 * NS) ring[r % kAhead] = read_v(r + kAhead);
+        if (b < 3) weigh(b + 1, 8 * d / NS, 8 * (d + 1) / NS);
+        __builtin_amdgcn_sched_barrier(0);
       }
   }
 
@@ -345,9 +442,9 @@ struct Tile {
   }
 };
 
-template <int D, int NG, bool SYM>
+template <int D, int NG, bool SYM, bool SPLIT>
 __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_tile_kernel(Kv4Attn a) {
-  using T = Tile<D, NG, SYM>;
+  using T = Tile<D, NG, SYM, SPLIT>;
   constexpr bool kBoth = T::NW == 4;   // a wave expands keys and values of its block; else one of them
   __shared__ __attribute__((aligned(16))) uint8_t smem[2 * T::kBuf];
   const int lane = threadIdx.x & 63;
@@ -371,9 +468,9 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
       const bool starts = j0 == 0, ends = j1 == sp.cnt;
       const int row0 = cur.qt * T::TQ + wave * 32;
       // the run's keys, 64 at a time
-      const int64_t cut = (int64_t)(sp.t0 + j1) << a.grain;
+      const int64_t cut = tile_start(a, sp, j1);
       const int stop = cut < sp.hi ? (int)cut : sp.hi;
-      int u0 = (sp.t0 + j0) << a.grain;
+      int u0 = (int)tile_start(a, sp, j0);
       if (u0 < sp.lo) u0 = sp.lo & ~(kTK - 1);
       const PageRow table = page_row(a, cur.b);
       // page of this wave's 16 of the 64 keys from u on, -1 where no row sees them
@@ -440,14 +537,22 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
   if (threadIdx.x == 0) leave_meta(a, sh, last, cur);
 }
 
+template <int D, int NG, bool SYM, bool SPLIT>
+hipError_t launch_tile_as(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
+  using T = Tile<D, NG, SYM, SPLIT>;
+  hipLaunchKernelGGL((kv4_tile_kernel<D, NG, SYM, SPLIT>), dim3(a.workers), dim3(T::NW * 64), 0, s, a);
+  if (hipError_t e = hipGetLastError()) return e;
+  return launch_join<D, T::TQ, 1>(a, p.tile_rows, s);
+}
+
 template <int D, int NG>
 hipError_t launch_tile(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
-  if (a.c.sym)
-    hipLaunchKernelGGL((kv4_tile_kernel<D, NG, true>), dim3(a.workers), dim3(Tile<D, NG, true>::NW * 64), 0, s, a);
-  else
-    hipLaunchKernelGGL((kv4_tile_kernel<D, NG, false>), dim3(a.workers), dim3(Tile<D, NG, true>::NW * 64), 0, s, a);
-  if (hipError_t e = hipGetLastError()) return e;
-  return launch_join<D, Tile<D, NG, true>::TQ, 1>(a, p.tile_rows, s);
+  // Three groups and more of scales, and two sets of unfinished scores, do not
+  // fit the registers: two parts are then twice the first products but no
+  // scales (128 channels, 4 groups: 158 us where spills made it 560; 1 group:
+  // 246 us where scales take 218).  At 256 channels LDS has no room for them.
+  constexpr bool kSplit = D <= 128 && NG > 2;
+  return a.c.sym ? launch_tile_as<D, NG, true, kSplit>(a, p, s) : launch_tile_as<D, NG, false, kSplit>(a, p, s);
 }
 
 }  // namespace kv4
