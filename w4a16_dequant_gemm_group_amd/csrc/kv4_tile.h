@@ -39,6 +39,10 @@ struct Tile {
   static constexpr int kEx = kScale + (SPLIT ? 0 : NG * kTK * 2);   // floats {E, 2^-E} of the values' blocks of
   static constexpr int kBuf = kEx + 48;                   //   16, 2^E of the keys'; bytes of one buffer
 
+  // Two buffers, so that one is filled while the other is read; 256 channels in
+  // two parts have room for one.
+  static constexpr int kBufs = 2 * kBuf <= 160 * 1024 ? 2 : 1;
+
   f16x8 q[D / 16];
   float A, mref, l;
   f32x16 o[NS];
@@ -446,7 +450,7 @@ template <int D, int NG, bool SYM, bool SPLIT>
 __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_tile_kernel(Kv4Attn a) {
   using T = Tile<D, NG, SYM, SPLIT>;
   constexpr bool kBoth = T::NW == 4;   // a wave expands keys and values of its block; else one of them
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * T::kBuf];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[T::kBufs * T::kBuf];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, kg = lane >> 4, n = lane & 31, hf = lane >> 5;
@@ -505,14 +509,15 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
       expand(smem);
       int64_t next = page_of(u0 + kTK);
       __syncthreads();
-      for (int u = u0, b = 0; u < stop; u += kTK, b ^= 1) {
+      for (int u = u0, b = 0; u < stop; u += kTK, b ^= T::kBufs - 1) {
         const bool more = u + kTK < stop;
         if (more) {
           fetch(next, u + kTK);
           next = page_of(u + 2 * kTK);
         }
         if (row0 < s.n * a.r) st.attend(a, s, row0, u, smem + b * T::kBuf, n, hf);
-        if (more) expand(smem + (b ^ 1) * T::kBuf);
+        if (T::kBufs == 1) __syncthreads();
+        if (more) expand(smem + (b ^ (T::kBufs - 1)) * T::kBuf);
         __syncthreads();
       }
       float* part = nullptr;
@@ -547,11 +552,11 @@ hipError_t launch_tile_as(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
 
 template <int D, int NG>
 hipError_t launch_tile(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
-  // Three groups and more of scales, and two sets of unfinished scores, do not
-  // fit the registers: two parts are then twice the first products but no
-  // scales (128 channels, 4 groups: 158 us where spills made it 560; 1 group:
-  // 246 us where scales take 218).  At 256 channels LDS has no room for them.
-  constexpr bool kSplit = D <= 128 && NG > 2;
+  // Several scales a key and two sets of unfinished scores do not fit the
+  // registers: two parts are then twice the first products but no scales.
+  // Prompts of 4096 and 2048: 128 channels, 1 group 218 us with scales, 246
+  // in parts; 4 groups 158 in parts, 560 with scales (which spill).
+  constexpr bool kSplit = NG > (D <= 128 ? 2 : 1);
   return a.c.sym ? launch_tile_as<D, NG, true, kSplit>(a, p, s) : launch_tile_as<D, NG, false, kSplit>(a, p, s);
 }
 
