@@ -215,6 +215,26 @@ __device__ __forceinline__ Share find_share(const Kv4Attn& a, int lane) {
       base += lane_of(sc, 63);
     }
   }
+  if (batch == 1) {
+    // one sequence: its lengths are loaded once, and up to 64 row tiles scanned once
+    const Seq s = wave_seq(a, 0);
+    const int nqt = row_tiles(a, s, TQ);
+    const uint32_t v = lane < nqt ? get_span<TQ>(a, s, lane).cnt : 0, sc = wave_scan(v, lane);
+    const uint32_t per = nqt <= 64 ? lane_of(sc, 63) : seq_tiles<TQ>(a, s, lane, false, 0, nullptr);
+    sh.total = per * heads;
+    sh.cut(a);
+    if (sh.at == sh.end) return sh;
+    sh.cur.h = (int)(sh.at / per);
+    const uint32_t i = sh.at % per;
+    if (nqt <= 64) {
+      const int l = __builtin_ctzll(__ballot(sc > i));
+      sh.cur.qt = l;
+      sh.cur.off = (int)(i - lane_of(sc - v, l));
+    } else {
+      seq_tiles<TQ>(a, s, lane, true, i, &sh.cur);
+    }
+    return sh;
+  }
   for (int b = 0; b < batch; ++b) base += seq_tiles<TQ>(a, wave_seq(a, b), lane, false, 0, nullptr);
   sh.total = base * heads;
   sh.cut(a);

@@ -27,15 +27,22 @@ struct Row {
   static constexpr int kRows = kThreads / kPitch;       // rows per pass of a workgroup
 };
 
+// The larger of two, in one instruction: fmaxf first quiets its operands.
+__device__ __forceinline__ float max2(float a, float b) {
+  float r;
+  asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+
 // Largest value over the lanes of a group of g channels (g / 8 lanes; the 12
 // of g = 96 lie in a row of 16 whose last 4 hold zeros, which the callers'
 // ranges include).
 __device__ __forceinline__ float group_max(float v, int g) {
-  v = fmaxf(v, dpp_f32<0xB1, 0xF>(v));    // quad_perm [1,0,3,2]
-  v = fmaxf(v, dpp_f32<0x4E, 0xF>(v));    // quad_perm [2,3,0,1]
-  if (g > 32) v = fmaxf(v, dpp_f32<0x141, 0xF>(v));   // row_half_mirror: 8 lanes
-  if (g > 64) v = fmaxf(v, dpp_f32<0x140, 0xF>(v));   // row_mirror: 16 lanes
-  if (g > 128) v = fmaxf(v, __shfl_xor(v, 16));
+  v = max2(v, dpp_f32<0xB1, 0xF>(v));    // quad_perm [1,0,3,2]
+  v = max2(v, dpp_f32<0x4E, 0xF>(v));    // quad_perm [2,3,0,1]
+  if (g > 32) v = max2(v, dpp_f32<0x141, 0xF>(v));   // row_half_mirror: 8 lanes
+  if (g > 64) v = max2(v, dpp_f32<0x140, 0xF>(v));   // row_mirror: 16 lanes
+  if (g > 128) v = max2(v, __shfl_xor(v, 16));
   return v;
 }
 
@@ -64,12 +71,13 @@ __device__ __forceinline__ float div_round(float x, float S, float inv, float lo
   return __builtin_amdgcn_fmed3f(q, lo, hi) + 12582912.0f;
 }
 
-__device__ __forceinline__ void widen(uint4 raw, int bf16, float (&x)[8]) {
+template <bool BF16>
+__device__ __forceinline__ void widen(uint4 raw, float (&x)[8]) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16 ? __uint_as_float(w[i] << 16) : f16_to_f32((uint16_t)(w[i] & 0xFFFFu));
-    x[2 * i + 1] = bf16 ? __uint_as_float(w[i] & 0xFFFF0000u) : f16_to_f32((uint16_t)(w[i] >> 16));
+    x[2 * i] = BF16 ? __uint_as_float(w[i] << 16) : f16_to_f32((uint16_t)(w[i] & 0xFFFFu));
+    x[2 * i + 1] = BF16 ? __uint_as_float(w[i] & 0xFFFF0000u) : f16_to_f32((uint16_t)(w[i] >> 16));
   }
 }
 
@@ -81,14 +89,16 @@ struct Quant {
 
 // 8 channels of a row, the lanes of a group together.  at: where each code goes
 // in the dword, 4 bits each from the lowest.
-__device__ __forceinline__ Quant quantise(float (&x)[8], int sym, int g, uint32_t at) {
+template <bool SYM>
+__device__ __forceinline__ Quant quantise(float (&x)[8], int g, uint32_t at) {
+  constexpr bool sym = SYM;
   float hi = 0.0f, lo = 0.0f;
   if (sym) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) hi = fmaxf(hi, fabsf(x[i]));
+    for (int i = 0; i < 8; ++i) hi = max2(hi, fabsf(x[i]));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) { hi = fmaxf(hi, x[i]); lo = fmaxf(lo, -x[i]); }
+    for (int i = 0; i < 8; ++i) { hi = max2(hi, x[i]); lo = max2(lo, -x[i]); }
     lo = group_max(lo, g);
   }
   hi = group_max(hi, g);
@@ -117,10 +127,10 @@ __device__ __forceinline__ Quant quantise(float (&x)[8], int sym, int g, uint32_
   return r;
 }
 
-template <int D>
+template <int D, bool SYM, bool BF16>
 __global__ __launch_bounds__(kThreads) void kv4_write_kernel(
     const uint16_t* __restrict__ k, int64_t k_ts, int64_t k_hs, const uint16_t* __restrict__ v,
-    int64_t v_ts, int64_t v_hs, int bf16, int64_t tokens, const int64_t* __restrict__ slots,
+    int64_t v_ts, int64_t v_hs, int64_t tokens, const int64_t* __restrict__ slots,
     Kv4Geo c) {
   constexpr int NS = D / 32, P = Row<D>::kPitch, L = Row<D>::kLanes;
   __shared__ uint32_t sv[kThreads];
@@ -136,10 +146,10 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(
     slot = slots[t];
   }
   float x[8];
-  widen(kr, bf16, x);
-  const Quant qk = quantise(x, c.sym, c.g, 0x73625140u);
-  widen(vr, bf16, x);
-  const Quant qv = quantise(x, c.sym, c.g, 0x76543210u);
+  widen<BF16>(kr, x);
+  const Quant qk = quantise<SYM>(x, c.g, 0x73625140u);
+  widen<BF16>(vr, x);
+  const Quant qv = quantise<SYM>(x, c.g, 0x76543210u);
   // natural order (bytes 4 lane .. of the row) -> bytes (m, b)
   sv[threadIdx.x] = qv.codes;
   __syncthreads();
@@ -171,7 +181,7 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(
     uint16_t* mk = (uint16_t*)(blk + 8 * D);
     uint16_t* mv = (uint16_t*)(blv + 8 * D);
     mk[gi * 16 + ts] = qk.S;
-    if (c.sym) {
+    if (SYM) {
       mv[gi * 16 + ts] = qv.S;
     } else {
       mk[16 * c.ng + ts * c.ng + gi] = kv4_zero_bits(qk.z);
@@ -303,14 +313,21 @@ dim3 grid_of(int64_t tokens, int heads, int u) {
 hipError_t launch_kv4_write(const void* k, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_ts,
                             int64_t v_hs, gq_dtype dt, int64_t tokens, const int64_t* slots,
                             const Kv4Geo& c, hipStream_t s) {
-#define GQ_KV4_WRITE(D)                                                                        \
-  hipLaunchKernelGGL(kv4_write_kernel<D>, grid_of<D>(tokens, c.hkv, 1), dim3(kThreads), 0, s,  \
-                     (const uint16_t*)k, k_ts, k_hs, (const uint16_t*)v, v_ts, v_hs,           \
-                     (int)(dt == GQ_BF16), tokens, slots, c)
-  if (c.d == 64) GQ_KV4_WRITE(64);
-  else if (c.d == 96) GQ_KV4_WRITE(96);
-  else if (c.d == 128) GQ_KV4_WRITE(128);
-  else GQ_KV4_WRITE(256);
+#define GQ_KV4_WRITE(D, SYM, BF16)                                                                       \
+  hipLaunchKernelGGL((kv4_write_kernel<D, SYM, BF16>), grid_of<D>(tokens, c.hkv, 1), dim3(kThreads), 0, s, \
+                     (const uint16_t*)k, k_ts, k_hs, (const uint16_t*)v, v_ts, v_hs, tokens, slots, c)
+#define GQ_KV4_WRITE_D(D)                                      \
+  if (c.sym && dt == GQ_BF16) GQ_KV4_WRITE(D, true, true);     \
+  else if (c.sym) GQ_KV4_WRITE(D, true, false);                \
+  else if (dt == GQ_BF16) GQ_KV4_WRITE(D, false, true);        \
+  else GQ_KV4_WRITE(D, false, false)
+  switch (c.d) {
+    case 64: GQ_KV4_WRITE_D(64); break;
+    case 96: GQ_KV4_WRITE_D(96); break;
+    case 128: GQ_KV4_WRITE_D(128); break;
+    default: GQ_KV4_WRITE_D(256); break;
+  }
+#undef GQ_KV4_WRITE_D
 #undef GQ_KV4_WRITE
   return hipGetLastError();
 }

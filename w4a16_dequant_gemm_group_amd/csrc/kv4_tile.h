@@ -311,8 +311,11 @@ struct Tile {
         const int tt = i / NG, g = i % NG;
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (e >= from && e < to)
-            x[tt][e] = __builtin_fmaf((float)sc[i & 1][e >> 3][e & 7], acc[i & 1][e], g == 0 ? 0.0f : x[tt][e]);
+          if (e >= from && e < to) {
+            float v = __builtin_fmaf((float)sc[i & 1][e >> 3][e & 7], acc[i & 1][e], g == 0 ? 0.0f : x[tt][e]);
+            asm volatile("" : "+v"(v));   // here, not where it is used first
+            x[tt][e] = v;
+          }
       };
 #pragma unroll
       for (int r = 0; r < kAhead; ++r) ring[r] = read(r);
@@ -504,20 +507,27 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
           T::expand_v(nib, ck, sp, buf, blk, m, kg);
         }
       };
-      st.load_q(a, s, cur.h, row0 + n, hf);
       fetch(page_of(u0), u0);
+      st.load_q(a, s, cur.h, row0 + n, hf);   // beside the codes
       expand(smem);
-      int64_t next = page_of(u0 + kTK);
+      fetch(page_of(u0 + kTK), u0 + kTK);
+      int64_t next = page_of(u0 + 2 * kTK);
       __syncthreads();
+      // Codes are fetched a tile before they are expanded.  The waves of keys
+      // expand before their products and those of values after: of the two
+      // waves of a SIMD one has vector work while the other multiplies.
       for (int u = u0, b = 0; u < stop; u += kTK, b ^= T::kBufs - 1) {
         const bool more = u + kTK < stop;
-        if (more) {
-          fetch(next, u + kTK);
-          next = page_of(u + 2 * kTK);
-        }
+        auto refill = [&] {
+          if (!more) return;
+          expand(smem + (b ^ (T::kBufs - 1)) * T::kBuf);
+          fetch(next, u + 2 * kTK);
+          next = page_of(u + 3 * kTK);
+        };
+        if (!kBoth && is_k) refill();
         if (row0 < s.n * a.r) st.attend(a, s, row0, u, smem + b * T::kBuf, n, hf);
         if (T::kBufs == 1) __syncthreads();
-        if (more) expand(smem + (b ^ (T::kBufs - 1)) * T::kBuf);
+        if (kBoth || !is_k) refill();
         __syncthreads();
       }
       float* part = nullptr;
