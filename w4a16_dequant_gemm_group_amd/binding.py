@@ -130,13 +130,15 @@ def _ok(status: int, where: str) -> None:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
+    """Handle of a stream (default: the current device's current one, taken without
+    building a Stream object around it, a third of a small call's host time)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _need(t, name: str, dtypes, shape=None):
@@ -710,7 +712,8 @@ def gq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
         None if lse is None else lse.data_ptr())
     ref = ctypes.byref(a)
     size = ctypes.c_size_t()
-    _ok(lib().gq_kv4_attention_workspace_size(ref, ctypes.byref(size)), "gq_kv4_attention_workspace_size")
+    L = lib()
+    _ok(L.gq_kv4_attention_workspace_size(ref, ctypes.byref(size)), "gq_kv4_attention_workspace_size")
     need = size.value
     if workspace is not None and workspace.numel() < need:
         raise ValueError(f"workspace has {workspace.numel()} bytes, the call needs {need}")
@@ -723,6 +726,6 @@ def gq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
         else:
             with torch.cuda.stream(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _ok(lib().gq_kv4_attention(ref, _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                               _stream(stream)), "gq_kv4_attention")
+    _ok(L.gq_kv4_attention(ref, _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                           _stream(stream)), "gq_kv4_attention")
     return (out, lse) if return_lse else out
