@@ -24,7 +24,7 @@ constexpr int kTK = 64;   // keys per tile
 // matrix products.
 constexpr int tile_waves(int d) { return d > 128 ? 4 : 8; }
 
-template <int D, int NG, bool SYM, bool SPLIT>
+template <int D, int NG, bool SYM, bool SPLIT, bool F16>
 struct Tile {
   static constexpr int NS = D / 32, SPG = NS / NG;
   static constexpr int NW = tile_waves(D);
@@ -35,7 +35,10 @@ struct Tile {
   // c - z, with a scale per group applied to the scores (SPLIT false), or as
   // x^ / 2^E in two fp16 parts (true).
   static constexpr int kV = kTK * KP * (SPLIT ? 2 : 1);   // the values, behind the keys and their lower parts
-  static constexpr int kScale = kV + D * VP;              // key scales fp16 [NG][2][2][16]
+  // The rounding of a value to fp16 (2^-11) is far below that of a bf16 result,
+  // but as large as that of an fp16 one: F16 adds what it left, as a second part.
+  static constexpr int kParts = F16 ? 2 : 1;
+  static constexpr int kScale = kV + kParts * D * VP;     // key scales fp16 [NG][2][2][16]
   static constexpr int kEx = kScale + (SPLIT ? 0 : NG * kTK * 2);   // floats {E, 2^-E} of the values' blocks of
   static constexpr int kBuf = kEx + 48;                   //   16, 2^E of the keys'; bytes of one buffer
 
@@ -166,7 +169,7 @@ struct Tile {
     }
   }
 
-  // Values: x^ / 2^E as fp16, rounded once (2^-11); E is the exponent of the
+  // Values: x^ / 2^E as fp16 (F16: and what the rounding left); E is the exponent of the
   // largest scale of the 16, so that they lie in fp16's normal range whatever
   // the scales are.  2^E comes back in the exponent of P.
   static __device__ __forceinline__ void expand_v(const Nibbles& nib, Codes& c, const Span& sp, uint8_t* buf, int blk, int m,
@@ -207,15 +210,25 @@ struct Tile {
       }
 #pragma unroll
       for (int b = g * SPG; b < (g + 1) * SPG; ++b) {
-        uint32_t lo[2], hi[2];
+        f16x2 v[2][2], x[2][2];   // channel 2 m or 2 m + 1, token pair
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t w = byte_pair<NS>(c.d, 2 * i * NS + b, (2 * i + 1) * NS + b);
-          lo[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, nib.lo(w, n1[i])) * S2[i]);
-          hi[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, nib.hi(w, n2[i])) * S2[i]);
+          v[0][i] = __builtin_bit_cast(f16x2, nib.lo(w, n1[i]));
+          v[1][i] = __builtin_bit_cast(f16x2, nib.hi(w, n2[i]));
         }
-        *(uint2*)(vb + (32 * b + 2 * m) * VP) = make_uint2(lo[0], lo[1]);
-        *(uint2*)(vb + (32 * b + 2 * m + 1) * VP) = make_uint2(hi[0], hi[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint8_t* row = vb + (32 * b + 2 * m + j) * VP;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) x[j][i] = v[j][i] * S2[i];
+          *(uint2*)row = make_uint2(__builtin_bit_cast(uint32_t, x[j][0]), __builtin_bit_cast(uint32_t, x[j][1]));
+          if constexpr (F16) {
+            const f16x2 r0 = __builtin_elementwise_fma(v[j][0], S2[0], -x[j][0]);
+            const f16x2 r1 = __builtin_elementwise_fma(v[j][1], S2[1], -x[j][1]);
+            *(uint2*)(row + D * VP) = make_uint2(__builtin_bit_cast(uint32_t, r0), __builtin_bit_cast(uint32_t, r1));
+          }
+        }
       }
     }
   }
@@ -339,8 +352,9 @@ struct Tile {
       scale(kRuns - 1, 0, 16);
     }
     const uint8_t* vb = buf + kV;
-    auto read_v = [&](int r) {   // 16 keys r / NS, channels 32 (r % NS) ..
-      return *(const f16x8*)(vb + (32 * (r % NS) + n) * VP + (r / NS) * 32 + hf * 16);
+    auto read_v = [&](int r) {   // 16 keys, part, channels 32 d ..
+      const int b = r / (kParts * NS), d = r % (kParts * NS);
+      return *(const f16x8*)(vb + (32 * d + n) * VP + b * 32 + hf * 16);
     };
 #pragma unroll
     for (int r = 0; r < kAhead; ++r) ring[r] = read_v(r);
@@ -408,11 +422,11 @@ struct Tile {
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
-      for (int d = 0; d < NS; ++d) {
-        const int r = b * NS + d;
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[r % kAhead], pw[b & 1], o[d], 0, 0, 0);
-        if (r + kAhead < 4 * NS) ring[r % kAhead] = read_v(r + kAhead);
-        if (b < 3) weigh(b + 1, 8 * d / NS, 8 * (d + 1) / NS);
+      for (int d = 0; d < kParts * NS; ++d) {
+        const int r = b * (kParts * NS) + d;
+        o[d % NS] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[r % kAhead], pw[b & 1], o[d % NS], 0, 0, 0);
+        if (r + kAhead < 4 * kParts * NS) ring[r % kAhead] = read_v(r + kAhead);
+        if (b < 3) weigh(b + 1, 8 * d / (kParts * NS), 8 * (d + 1) / (kParts * NS));
         __builtin_amdgcn_sched_barrier(0);
       }
   }
@@ -449,9 +463,9 @@ struct Tile {
   }
 };
 
-template <int D, int NG, bool SYM, bool SPLIT>
+template <int D, int NG, bool SYM, bool SPLIT, bool F16>
 __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_tile_kernel(Kv4Attn a) {
-  using T = Tile<D, NG, SYM, SPLIT>;
+  using T = Tile<D, NG, SYM, SPLIT, F16>;
   constexpr bool kBoth = T::NW == 4;   // a wave expands keys and values of its block; else one of them
   __shared__ __attribute__((aligned(16))) uint8_t smem[T::kBufs * T::kBuf];
   const int lane = threadIdx.x & 63;
@@ -552,10 +566,10 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
   if (threadIdx.x == 0) leave_meta(a, sh, last, cur);
 }
 
-template <int D, int NG, bool SYM, bool SPLIT>
+template <int D, int NG, bool SYM, bool SPLIT, bool F16>
 hipError_t launch_tile_as(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
-  using T = Tile<D, NG, SYM, SPLIT>;
-  hipLaunchKernelGGL((kv4_tile_kernel<D, NG, SYM, SPLIT>), dim3(a.workers), dim3(T::NW * 64), 0, s, a);
+  using T = Tile<D, NG, SYM, SPLIT, F16>;
+  hipLaunchKernelGGL((kv4_tile_kernel<D, NG, SYM, SPLIT, F16>), dim3(a.workers), dim3(T::NW * 64), 0, s, a);
   if (hipError_t e = hipGetLastError()) return e;
   return launch_join<D, T::TQ, 1>(a, p.tile_rows, s);
 }
@@ -567,7 +581,11 @@ hipError_t launch_tile(const Kv4Attn& a, const Kv4Plan& p, hipStream_t s) {
   // Prompts of 4096 and 2048: 128 channels, 1 group 218 us with scales, 246
   // in parts; 4 groups 158 in parts, 560 with scales (which spill).
   constexpr bool kSplit = NG > (D <= 128 ? 2 : 1);
-  return a.c.sym ? launch_tile_as<D, NG, true, kSplit>(a, p, s) : launch_tile_as<D, NG, false, kSplit>(a, p, s);
+  if (a.bf16)
+    return a.c.sym ? launch_tile_as<D, NG, true, kSplit, false>(a, p, s)
+                   : launch_tile_as<D, NG, false, kSplit, false>(a, p, s);
+  return a.c.sym ? launch_tile_as<D, NG, true, kSplit, true>(a, p, s)
+                 : launch_tile_as<D, NG, false, kSplit, true>(a, p, s);
 }
 
 }  // namespace kv4
