@@ -91,17 +91,16 @@ struct Tile {
     }
   };
 
-  // Largest of a non-negative value over the wave, as a scalar.
+  // Largest value over the wave, as a scalar.
+  template <int CTRL>
+  static __device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+    const uint32_t u = __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+    return u > v ? u : v;
+  }
   static __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-    float f = __uint_as_float(v);   // bit patterns of non-negative halfs order as floats do
-    f = fmaxf(f, stream_util::dpp_f32<0xB1, 0xF>(f));
-    f = fmaxf(f, stream_util::dpp_f32<0x4E, 0xF>(f));
-    f = fmaxf(f, stream_util::dpp_f32<0x141, 0xF>(f));
-    f = fmaxf(f, stream_util::dpp_f32<0x140, 0xF>(f));
-    const uint32_t a = __builtin_amdgcn_readlane(__float_as_uint(f), 0);
-    const uint32_t b = __builtin_amdgcn_readlane(__float_as_uint(f), 16);
-    const uint32_t c = __builtin_amdgcn_readlane(__float_as_uint(f), 32);
-    const uint32_t d = __builtin_amdgcn_readlane(__float_as_uint(f), 48);
+    v = max_dpp<0x140>(max_dpp<0x141>(max_dpp<0x4E>(max_dpp<0xB1>(v))));   // over rows of 16 lanes
+    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+    const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
     const uint32_t x = a > b ? a : b, y = c > d ? c : d;
     return x > y ? x : y;
   }
@@ -119,12 +118,18 @@ struct Tile {
   // zeros, whatever their memory holds.
   static __device__ __forceinline__ void expand_k(const Nibbles& nib, Codes& c, const Span& sp, uint8_t* buf,
                                                   int blk, int m, int kg) {
-    const bool live = c.ok && c.pos + m >= sp.lo && c.pos + m < sp.hi;
-    uint32_t top = 0;
+    if (!(c.ok && c.pos >= sp.lo && c.pos + 16 <= sp.hi)) {
+      const bool live = c.ok && c.pos + m >= sp.lo && c.pos + m < sp.hi;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      c.p[g][0] = live ? c.p[g][0] : 0u;
-      top = c.p[g][0] > top ? c.p[g][0] : top;
+      for (int g = 0; g < NG; ++g) {
+        c.p[g][0] = live ? c.p[g][0] : 0u;
+        if constexpr (!SYM) c.p[g][1] = live ? c.p[g][1] : 0u;
+      }
+    }
+    uint32_t top = 0;
+    if constexpr (SPLIT) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) top = c.p[g][0] > top ? c.p[g][0] : top;
     }
     float inv = 1.0f;
     if constexpr (SPLIT) {
@@ -143,7 +148,7 @@ struct Tile {
     for (int g = 0; g < NG; ++g) {
       f16x2 n1 = {(_Float16)-1032.0f, (_Float16)-1032.0f};
       if constexpr (!SYM) {
-        const _Float16 z = __builtin_bit_cast(_Float16, (uint16_t)(live ? c.p[g][1] : 0u));
+        const _Float16 z = __builtin_bit_cast(_Float16, (uint16_t)c.p[g][1]);
         n1 = f16x2{z, z};
       }
       const f16x2 n2 = n1 + (_Float16)960.0f;
@@ -174,21 +179,25 @@ struct Tile {
   // the scales are.  2^E comes back in the exponent of P.
   static __device__ __forceinline__ void expand_v(const Nibbles& nib, Codes& c, const Span& sp, uint8_t* buf, int blk, int m,
                                                   int kg) {
-    uint32_t top = 0;
+    if (!(c.ok && c.pos >= sp.lo && c.pos + 16 <= sp.hi)) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int p = c.pos + 4 * kg + 2 * i;
-      const uint32_t live = (c.ok && p >= sp.lo && p < sp.hi ? 0xFFFFu : 0u) |
-                            (c.ok && p + 1 >= sp.lo && p + 1 < sp.hi ? 0xFFFF0000u : 0u);
+      for (int i = 0; i < 2; ++i) {
+        const int p = c.pos + 4 * kg + 2 * i;
+        const uint32_t live = (c.ok && p >= sp.lo && p < sp.hi ? 0xFFFFu : 0u) |
+                              (c.ok && p + 1 >= sp.lo && p + 1 < sp.hi ? 0xFFFF0000u : 0u);
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        c.p[g][i] &= live;
-        if constexpr (!SYM) c.p[g][2 + i] &= live;
-        const uint32_t x = c.p[g][i] & 0xFFFFu, y = c.p[g][i] >> 16;
-        top = x > top ? x : top;
-        top = y > top ? y : top;
+        for (int g = 0; g < NG; ++g) {
+          c.p[g][i] &= live;
+          if constexpr (!SYM) c.p[g][2 + i] &= live;
+        }
       }
     }
+    u16x2 most = {0, 0};
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, c.p[g][i]));
+    const uint32_t top = most[0] > most[1] ? most[0] : most[1];
     const uint32_t e = top_exponent(top);
     const float inv = pow2_neg(e);
     if (m == 0 && kg == 0) {
