@@ -155,12 +155,13 @@ def _need(t, name: str, dtypes, shape=None):
 
 def _on_device(dev, **tensors) -> None:
     """Every given tensor is a GPU tensor on `dev` (checked after all shapes)."""
+    index = None if dev is None else dev.index
     for name, t in tensors.items():
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError(f"{name} must be a GPU tensor")
-        if dev is not None and t.device != dev:
+        if index is not None and t.get_device() != index:
             raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
@@ -562,9 +563,21 @@ def gq_kv4_empty(n_pages: int, kv_heads: int, head_dim: int, page_size: int = 64
                        dtype=torch.uint8, device=device)
 
 
+# layouts of the cache shapes seen so far (checked once each)
+_kv4_layouts = {}
+
+
 def _kv4_cache(cache, head_dim: int, group_size: int, symmetric: bool):
     """Check a cache against head_dim and the quantisation; its layout."""
     _need(cache, "cache", (torch.uint8,))
+    key = (cache.shape, head_dim, group_size, bool(symmetric))
+    lay = _kv4_layouts.get(key)
+    if lay is None:
+        lay = _kv4_layouts[key] = _kv4_layout(cache, head_dim, group_size, symmetric)
+    return lay
+
+
+def _kv4_layout(cache, head_dim: int, group_size: int, symmetric: bool):
     _kv4_shape(head_dim, group_size)
     blk = _kv4_block_bytes(head_dim, group_size, symmetric)
     if cache.dim() != 4 or cache.shape[3] != blk:
@@ -581,14 +594,16 @@ def _rows16(t, name: str, dtypes, heads=None, dim=None):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or \
-            (dim is not None and t.shape[2] != dim):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (tokens, "
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or \
+            (dim is not None and shape[2] != dim):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected (tokens, "
                          f"{'heads' if heads is None else heads}, {'dim' if dim is None else dim})")
     # the stride of a dimension of one element is never walked
-    ts = t.stride(0) if t.shape[0] > 1 else 0
-    hs = t.stride(1) if t.shape[1] > 1 else 0
-    if (t.shape[2] > 1 and t.stride(2) != 1) or ts % 8 or hs % 8:
+    ts, hs, ds = t.stride()
+    ts = ts if shape[0] > 1 else 0
+    hs = hs if shape[1] > 1 else 0
+    if (shape[2] > 1 and ds != 1) or ts % 8 or hs % 8:
         raise ValueError(f"{name}: strides {t.stride()}; the last must be 1, the others multiples of 8")
     return ts, hs
 
@@ -636,7 +651,7 @@ def gq_kv4_read(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, group_s
     if k is None:
         k = torch.empty(shape, dtype=out_dtype, device=cache.device)
     if v is None:
-        v = torch.empty(shape, dtype=out_dtype, device=cache.device)
+        v = torch.empty_like(k)
     _ok(lib().gq_kv4_read(_ptr(cache), cache.shape[0], lay, _ptr(slots), slots.shape[0], _ptr(k),
                           _ptr(v), _DT[out_dtype], _stream(stream)), "gq_kv4_read")
     return k, v
@@ -701,7 +716,7 @@ def gq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
     _on_device(q.device, cache=cache, page_table=page_table, kv_lens=kv_lens, q_starts=q_starts,
                out=out, lse=lse, workspace=workspace)
     if out is None:
-        out = torch.empty((T, HQ, D), dtype=q.dtype, device=q.device)
+        out = q.new_empty((T, HQ, D))
     if lse is None and return_lse:
         lse = torch.empty((T, HQ), dtype=torch.float32, device=q.device)
     a = GqKv4AttentionArgs(
