@@ -100,8 +100,11 @@ gq_status gq_kv4_read(const uint8_t* cache, int64_t n_pages, gq_kv4_layout layou
  *   scale      factor of the scores, finite and > 0; 1 / sqrt(head_dim) by custom
  *   out        [q_tokens, q_heads, head_dim] of dtype, contiguous, 16-byte aligned
  *   lse        [q_tokens, q_heads] float, or NULL
- * Scores, softmax statistics and outputs are kept in fp32; the matrix cores
- * take the codes as exact integers or fp16 (see the kernels). */
+ * Scores, softmax statistics and outputs are kept in fp32.  The matrix cores
+ * take keys exactly (integers, or two fp16 parts); weights, and for more than 32
+ * rows per key/value head values too, are rounded to fp16 once (2^-11), for
+ * fp16 results of at most 8 rows the weights and of more than 32 rows the
+ * values not at all. */
 typedef struct {
   const void* q;
   int64_t q_token_stride, q_head_stride;
