@@ -442,6 +442,26 @@ struct Rows {
   // costs an fp16 result no accuracy.  The columns would be idle otherwise.
   bool rest;
   Nibbles nib;
+  // The workgroups of a compute unit have equal work, but a SIMD serves its
+  // oldest wave first: without more, the first of three ended at 21 us, the
+  // others, ever fewer waves to hide their loads, at 26 and 32 (one token over
+  // 128 K keys).  So a wave begins with the highest priority and steps down
+  // with every quarter of its work: whoever is behind is served first.
+  int left = 0, next = -1, quarter = 0;   // tiles left, those at which to step down
+  __device__ __forceinline__ void begin_share(uint32_t tiles) {
+    left = __builtin_amdgcn_readfirstlane((int)tiles);
+    quarter = (left >> 2) + 1;
+    next = left - quarter;
+    __builtin_amdgcn_s_setprio(3);
+  }
+  __device__ __forceinline__ void tile_done() {
+    left = __builtin_amdgcn_readfirstlane(left - 1);
+    if (left != next) return;
+    next = __builtin_amdgcn_readfirstlane(next - quarter);
+    if (left > 2 * quarter) __builtin_amdgcn_s_setprio(2);
+    else if (left > quarter) __builtin_amdgcn_s_setprio(1);
+    else __builtin_amdgcn_s_setprio(0);
+  }
 
   __device__ __forceinline__ int row_of_lane() const { return threadIdx.x & (rest ? 7 : 15); }
 
@@ -764,6 +784,7 @@ struct Rows {
       if (!full) clear_unseen(sp, u, ok & 1, ok & 2, vb, kg);
       weights(a, s, qt, u, !full, ok & 1, ok & 2, vb, x, kg);
       values(vb, x);
+      tile_done();
       if (un >= end) break;
       u = un;
       ok = oknext;
@@ -884,6 +905,7 @@ __global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NG, NQ)) void kv4_ro
   if (split) {
     sh = find_share<R::TQ>(a, lane);
     cur = sh.cur;
+    st.begin_share(sh.end - sh.at);
   } else {
     // one workgroup per (sequence, head, row tile)
     const int id = blockIdx.x, bh = id / a.grid_q;
