@@ -255,14 +255,13 @@ __device__ __forceinline__ Share find_share(const Kv4Attn& a, int lane) {
 
 // What the join has to know of a worker: the row tile that it left open (last:
 // the last of the workers after it that hold the rest), or none (last < 0).
-__device__ __forceinline__ void leave_meta(const Kv4Attn& a, const Share& sh, int last, const Cursor& cur) {
+__device__ __forceinline__ void leave_meta(const Kv4Attn& a, const Share& sh, int last, const Cursor& cur,
+                                           const Seq& s) {
   if ((int)blockIdx.x >= sh.busy) a.meta[(int64_t)blockIdx.x * kMetaInts] = -1;   // a number nobody has
   if (sh.at == sh.end) return;
-  int32_t* mt = a.meta + (int64_t)sh.w * kMetaInts;
-  mt[0] = last;
-  mt[1] = cur.b;
-  mt[2] = cur.h;
-  mt[3] = cur.qt;
+  int4* mt = (int4*)(a.meta + (int64_t)sh.w * kMetaInts);
+  mt[0] = make_int4(last, cur.h, cur.qt, 0);
+  mt[1] = make_int4(s.q0, s.n, 0, 0);
 }
 
 // A row of the page table, which no kernel writes: read through the scalar
@@ -948,7 +947,7 @@ __global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NG, NQ)) void kv4_ro
       }
     }
   }
-  if (split && threadIdx.x == 0) leave_meta(a, sh, last, cur);
+  if (split && threadIdx.x == 0) leave_meta(a, sh, last, cur, s);
 }
 
 // Joins the partial results of the row tiles that were split: 4 to 6 us for
@@ -965,11 +964,11 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
   __shared__ float4 so[RW][PG][QD];
   __shared__ float sm[RW][PG], sl[RW][PG];
   const int w = blockIdx.x;
-  const int32_t* mt = a.meta + (int64_t)w * kMetaInts;
-  const int last = mt[0];
+  const int4* mt = (const int4*)(a.meta + (int64_t)w * kMetaInts);
+  const int4 open = mt[0], seq = mt[1];
+  const int last = open.x, h = open.y, qt = open.z;
   if (last < 0) return;
-  const int h = mt[2], qt = mt[3];
-  const Seq s = wave_seq(a, mt[1]);
+  const Seq s{seq.x, seq.y, 0};
   const int left = s.n * a.r - qt * TQ, rows = left < TQ ? left : TQ;
   const int tid = threadIdx.x;
   const int rw = tid / (QD * PG), pg = tid / QD % PG, qd = tid % QD;

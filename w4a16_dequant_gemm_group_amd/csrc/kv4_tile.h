@@ -309,6 +309,8 @@ struct Tile {
     constexpr int kAhead = 4;
     f16x8 ring[kAhead];
     f32x16 x[2];
+    // products go first where the SIMD's other wave has vector work (2 %)
+    __builtin_amdgcn_s_setprio(1);
     if constexpr (SPLIT) {
       // both halves of the keys, their lower parts, then the next channels
       constexpr int kAll = D / 4;
@@ -369,6 +371,7 @@ struct Tile {
       }
       scale(kRuns - 1, 0, 16);
     }
+    __builtin_amdgcn_s_setprio(0);
     const uint8_t* vb = buf + kV;
     auto read_v = [&](int r) {   // 16 keys, part, channels 32 d ..
       const int b = r / (kParts * NS), d = r % (kParts * NS);
@@ -436,6 +439,7 @@ struct Tile {
         }
     };
     weigh(0, 0, 8);
+    __builtin_amdgcn_s_setprio(1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int b = 0; b < 4; ++b)
@@ -447,6 +451,7 @@ struct Tile {
         if (b < 3) weigh(b + 1, 8 * d / (kParts * NS), 8 * (d + 1) / (kParts * NS));
         __builtin_amdgcn_sched_barrier(0);
       }
+    __builtin_amdgcn_s_setprio(0);
   }
 
   __device__ __forceinline__ void finish(const Kv4Attn& a, const Seq& s, int h, int qt, int ri, float* part,
@@ -498,8 +503,9 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
   uint32_t at = sh.at;
   int last = -1;
   Cursor cur = sh.cur;
+  Seq s{0, 0, 0};
   if (at < sh.end) {
-    Seq s = wave_seq(a, cur.b);
+    s = wave_seq(a, cur.b);
     for (;;) {
       const Span sp = get_span<T::TQ>(a, s, cur.qt);
       const int j0 = cur.off, left = (int)(sh.end - at);
@@ -581,7 +587,7 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv4_til
       }
     }
   }
-  if (threadIdx.x == 0) leave_meta(a, sh, last, cur);
+  if (threadIdx.x == 0) leave_meta(a, sh, last, cur, s);
 }
 
 template <int D, int NG, bool SYM, bool SPLIT, bool F16>
