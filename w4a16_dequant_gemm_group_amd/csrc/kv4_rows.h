@@ -411,9 +411,9 @@ __device__ __forceinline__ f16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32
 // the operands' exponent fields: measured errors of 2^-14 of a code.)
 // What bounds it: vector instructions, most of them the expansion of the codes.
 // Of a unit of 32 keys at 128 channels 176 of some 300 make the operands of its 16
-// products; counters show the vector unit 62 % busy, the matrix unit 10 %, and
-// no byte fetched twice.  151 MB of one sequence of 128 K keys pass in 40 us
-// (3.8 TB/s; a copy reaches 5.0), 332 MB of 64 ragged ones in 89 us (3.7).
+// products; counters show the vector unit 60 to 70 % busy, the matrix unit 10 %,
+// and no byte fetched twice.  151 MB of one sequence of 128 K keys pass in 36 us
+// (4.2 TB/s; a copy reaches 5.0), 332 MB of 64 ragged ones in 83 us (4.0).
 // Q becomes fp16 with a power of two per row that puts its largest element
 // near 2^14: exact for fp16 and bf16 elements down to 2^-29 of the largest.
 // So the scores are exact up to fp32 sums: s = sum_g S_g ((codes - z) . q).
@@ -702,7 +702,8 @@ struct Rows {
   // loads that need no registers leave those to more waves.  Load by load into
   // registers, each with half a unit's work to arrive, 64 ragged sequences
   // (groups of 32) took 130 us where this takes 110 (89 with the split evened
-  // out), one token over 128 K keys 45 against 40.
+  // out, 83 with two waves a SIMD), one token over 128 K keys 45 against 39 (36
+  // with the steps of priority).
   __device__ __forceinline__ void keys(const Kv4Attn& a, const Seq& s, const Span& sp, int64_t b, int h,
                                        int qt, int j0, int j1, uint8_t* smem, int wave, int m, int kg) {
     const PageRow row = page_row(a, b);

@@ -12,10 +12,10 @@
 // The expansion costs a wave some 60 to 90 vector instructions per 64 keys, an
 // eighth of what it would be for 32 rows alone; the softmax of its 32 rows
 // costs 170.  Counters for a prompt of 4096 (32 heads of 128, causal): vector
-// unit 51 % busy, matrix unit 35 %; reading the operands from LDS takes as long
-// as the products (one 1 KiB operand each).  Rates: 214 us or 640 TFLOP/s there,
+// unit 55 % busy, matrix unit 38 %; reading the operands from LDS takes as long
+// as the products (one 1 KiB operand each).  Rates: 212 us or 650 TFLOP/s there,
 // where a library product of 8192^3 reaches 1190; ragged chunks with groups of
-// 32 and fp16 results 175 us (twice the products, see below); a window of 4096
+// 32 and fp16 results 171 us (twice the products, see below); a window of 4096
 // keys at 256 channels 93 us.
 #pragma once
 
