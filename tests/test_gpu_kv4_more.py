@@ -83,6 +83,20 @@ def test_long_and_empty_row_tiles_together():
     p.check(*p.run(), fp16_operands=True, what="queries before all keys")
 
 
+@pytest.mark.parametrize("q", [1, 40])
+def test_tables_far_wider_than_the_lengths(q):
+    # 2^30 positions in a row of the table: more tiles than 32 bits count at the
+    # usual grain of the split, so the grain is coarser
+    gen = torch.Generator().manual_seed(5)
+    kv = [int(x) for x in torch.randint(41, 3000, (32,), generator=gen)]
+    kv[3], kv[9], kv[20] = 2900, 41, 512
+    p = Problem(91, 64, 64, False, 1024, "bf16", 8, 1, [q] * 32, kv)
+    announce_case(p, "wide table")
+    table = torch.full((32, 1 << 20), 0x7FFFFFF0, dtype=torch.int32)
+    table[:, :p.table.shape[1]] = p.table
+    p.check(*p.run(table=table), fp16_operands=True, what="wide table")
+
+
 @pytest.mark.parametrize("d,g,sym", [(64, 64, True), (128, 32, False), (256, 256, False)])
 def test_fp16_result_of_few_rows_is_rounded_once(d, g, sym):
     # Up to 8 rows: what rounding the weights leaves is carried along.  Besides the

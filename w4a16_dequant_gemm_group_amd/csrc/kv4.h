@@ -85,13 +85,11 @@ struct Kv4Attn {
   float* part;                       // [2 * workers][rows][D + 2] partial results
 };
 
-// Waves per SIMD of the rows kernel (d channels in ng groups, nq tiles of 16
-// rows): what its registers allow without spilling, and no more than three, as
-// each workgroup has fixed work.  64 ragged sequences with 4 groups: 83 us with
-// two, 88 with three; 128 K keys with 2 groups: 39 with two, 36 with three.
-constexpr int kv4_rows_waves(int d, int ng, int nq) {
-  return d * nq > 256 ? 1 : d > 128 || nq > 1 || ng > 2 ? 2 : 3;
-}
+// Waves per SIMD of the rows kernel (d channels, nq tiles of 16 rows): what its
+// registers allow, and no more than three, as each workgroup has fixed work (128
+// K keys with 2 groups: 39 us with two, 36 with three; 64 ragged sequences with
+// 4 groups: 88 with two, 79 with three).
+constexpr int kv4_rows_waves(int d, int nq) { return d * nq > 256 ? 1 : d > 128 || nq > 1 ? 2 : 3; }
 
 struct Kv4Plan {
   bool tile;           // the kernel for many rows; else the rows kernel

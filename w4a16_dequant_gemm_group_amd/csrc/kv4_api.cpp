@@ -16,6 +16,9 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 constexpr int kOverhead = 2;
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;
+// Tokens of one launch of the storage kernels: 8 rows per workgroup at least,
+// 2^32 threads at most over all heads' grid columns.
+constexpr int64_t kLaunchTokens = (int64_t)1 << 24;
 
 gq_status check_layout(const gq_kv4_layout& y) {
   if (y.kv_heads < 1 || y.kv_heads > 65535 || y.head_dim < 1) return GQ_ERR_INVALID_ARG;
@@ -103,10 +106,12 @@ Kv4Plan kv4_plan(const gq_kv4_attention_args& a) {
   while (p.grain < 30 && row_tiles * ((cap >> p.grain) + 1 + kOverhead) >= INT32_MAX) ++p.grain;
   const int64_t segs = a.batch * a.layout.kv_heads * p.grid_q;
   const int64_t tiles = segs * (kOverhead + ((a.max_kv_len + (1 << p.grain) - 1) >> p.grain));
-  p.split = p.tile || a.max_kv_len > 1024 || segs > INT32_MAX;
+  // up to 1024 keys a workgroup per row tile, without the second kernel, is
+  // faster than the split (a launch takes fewer than 2^32 threads)
+  p.split = p.tile || a.max_kv_len > 1024 || segs >= (int64_t)1 << 24;
   if (p.split) {
     // as many workgroups (a wave on each SIMD) as run at once
-    const int64_t want = (int64_t)num_cus() * (p.tile ? 1 : kv4_rows_waves(d, d / a.layout.group_size, p.nq));
+    const int64_t want = (int64_t)num_cus() * (p.tile ? 1 : kv4_rows_waves(d, p.nq));
     p.workers = (int)std::max<int64_t>(8, std::min(tiles, want) & ~(int64_t)7);
     p.ws_bytes = (size_t)p.workers * 32 + (size_t)p.workers * 2 * tq * (d + 2) * sizeof(float);
   }
@@ -161,8 +166,13 @@ gq_status gq_kv4_write(const void* k, int64_t k_token_stride, int64_t k_head_str
     return GQ_ERR_MISALIGNED;
   hipStream_t s = (hipStream_t)stream;
   if (gq_status st = check_device(s)) return st;
-  return from_hip(launch_kv4_write(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride,
-                                   dtype, tokens, slots, geometry(cache, n_pages, layout), s));
+  const Kv4Geo c = geometry(cache, n_pages, layout);
+  for (int64_t t = 0; t < tokens; t += kLaunchTokens)
+    if (hipError_t e = launch_kv4_write((const uint16_t*)k + t * k_token_stride, k_token_stride, k_head_stride,
+                                        (const uint16_t*)v + t * v_token_stride, v_token_stride, v_head_stride,
+                                        dtype, std::min(tokens - t, kLaunchTokens), slots + t, c, s))
+      return from_hip(e);
+  return GQ_OK;
 }
 
 gq_status gq_kv4_read(const uint8_t* cache, int64_t n_pages, gq_kv4_layout layout,
@@ -177,7 +187,13 @@ gq_status gq_kv4_read(const uint8_t* cache, int64_t n_pages, gq_kv4_layout layou
     return GQ_ERR_MISALIGNED;
   hipStream_t s = (hipStream_t)stream;
   if (gq_status st = check_device(s)) return st;
-  return from_hip(launch_kv4_read(geometry(cache, n_pages, layout), slots, tokens, k, v, out_dtype, s));
+  const Kv4Geo c = geometry(cache, n_pages, layout);
+  const int64_t row = (int64_t)layout.kv_heads * layout.head_dim * (out_dtype == GQ_F32 ? 4 : 2);
+  for (int64_t t = 0; t < tokens; t += kLaunchTokens)
+    if (hipError_t e = launch_kv4_read(c, slots + t, std::min(tokens - t, kLaunchTokens), (uint8_t*)k + t * row,
+                                       (uint8_t*)v + t * row, out_dtype, s))
+      return from_hip(e);
+  return GQ_OK;
 }
 
 gq_status gq_kv4_attention_workspace_size(const gq_kv4_attention_args* args, size_t* bytes) {

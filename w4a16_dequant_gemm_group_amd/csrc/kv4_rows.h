@@ -339,7 +339,10 @@ struct KeyBlock {
 template <int D, int NG, bool SYM>
 struct ValueBlock {
   static constexpr int NS = D / 32;
-  uint32_t c[NS], s[NG][2], z[SYM ? 1 : NG][2];
+  // Three groups and more: a group's zero points are read when it is multiplied;
+  // all of them at once spill (24 rows at 4 groups 56 us, so 44).
+  static constexpr bool kLate = !SYM && NG > 2;
+  uint32_t c[NS], s[NG][2], z[SYM || kLate ? 1 : NG][2];
 
   __device__ __forceinline__ void load(const uint8_t* w, uint32_t m, uint32_t kg) {
     load_dwords<NS>(w + kg * (64 * NS) + m * (4 * NS), c);
@@ -348,6 +351,8 @@ struct ValueBlock {
     for (int g = 0; g < NG; ++g) {
       if constexpr (SYM) {
         load_dwords<2>(pv + g * 32 + kg * 8, s[g]);
+      } else if constexpr (kLate) {
+        load_dwords<2>(pv + g * 64 + kg * 16, s[g]);
       } else {
         uint32_t t[4];
         load_dwords<4>(pv + g * 64 + kg * 16, t);
@@ -411,9 +416,9 @@ __device__ __forceinline__ f16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32
 // the operands' exponent fields: measured errors of 2^-14 of a code.)
 // What bounds it: vector instructions, most of them the expansion of the codes.
 // Of a unit of 32 keys at 128 channels 176 of some 300 make the operands of its 16
-// products; counters show the vector unit 60 to 70 % busy, the matrix unit 10 %,
+// products; counters show the vector unit 70 to 76 % busy, the matrix unit 10 %,
 // and no byte fetched twice.  151 MB of one sequence of 128 K keys pass in 36 us
-// (4.2 TB/s; a copy reaches 5.0), 332 MB of 64 ragged ones in 83 us (4.0).
+// (4.2 TB/s; a copy reaches 5.0), 332 MB of 64 ragged ones in 79 us (4.2).
 // Q becomes fp16 with a power of two per row that puts its largest element
 // near 2^14: exact for fp16 and bf16 elements down to 2^-29 of the largest.
 // So the scores are exact up to fp32 sums: s = sum_g S_g ((codes - z) . q).
@@ -562,7 +567,7 @@ struct Rows {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           vb[t].s[g][i] &= live[i];
-          if constexpr (!SYM) vb[t].z[g][i] &= live[i];
+          if constexpr (!SYM && !ValueBlock<D, NG, SYM>::kLate) vb[t].z[g][i] &= live[i];
         }
     }
   }
@@ -644,10 +649,23 @@ struct Rows {
     }
   }
 
-  // o += V^^T p
-  __device__ __forceinline__ void values(const ValueBlock<D, NG, SYM> (&vb)[2], const float (&p)[NQ][2][4]) {
+  // o += V^^T p.  blk: the unit in LDS; masked: it may hold memory of any content.
+  __device__ __forceinline__ void values(const ValueBlock<D, NG, SYM> (&vb)[2], const float (&p)[NQ][2][4],
+                                         const uint8_t* blk, bool masked, uint32_t kg) {
+    constexpr bool kLate = ValueBlock<D, NG, SYM>::kLate;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
+      uint32_t zl[2][2];
+      if constexpr (kLate) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          load_dwords<2>(blk + kSub / 2 + t * kSub + 8 * D + g * 64 + kg * 16 + 8, zl[t]);
+          if (masked) {   // any finite one will do beside a scale of 0
+#pragma unroll
+            for (int i = 0; i < 2; ++i) zl[t][i] = (zl[t][i] & 0x000F000Fu) | 0xE400E400u;
+          }
+        }
+      }
       f16x8 pw[NQ];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -675,7 +693,8 @@ struct Rows {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         n1[i] = SYM ? f16x2{(_Float16)-1032.0f, (_Float16)-1032.0f}
-                    : __builtin_bit_cast(f16x2, vb[i >> 1].z[SYM ? 0 : g][i & 1]);
+                : kLate ? __builtin_bit_cast(f16x2, zl[i >> 1][i & 1])
+                        : __builtin_bit_cast(f16x2, vb[i >> 1].z[SYM || kLate ? 0 : g][i & 1]);
         n2[i] = n1[i] + (_Float16)960.0f;
       }
 #pragma unroll
@@ -702,7 +721,7 @@ struct Rows {
   // loads that need no registers leave those to more waves.  Load by load into
   // registers, each with half a unit's work to arrive, 64 ragged sequences
   // (groups of 32) took 130 us where this takes 110 (89 with the split evened
-  // out, 83 with two waves a SIMD), one token over 128 K keys 45 against 39 (36
+  // out, 79 with late zero points), one token over 128 K keys 45 against 39 (36
   // with the steps of priority).
   __device__ __forceinline__ void keys(const Kv4Attn& a, const Seq& s, const Span& sp, int64_t b, int h,
                                        int qt, int j0, int j1, uint8_t* smem, int wave, int m, int kg) {
@@ -783,7 +802,7 @@ struct Rows {
       vb[1].load(blk + kSub / 2 + kSub, m, kg);
       if (!full) clear_unseen(sp, u, ok & 1, ok & 2, vb, kg);
       weights(a, s, qt, u, !full, ok & 1, ok & 2, vb, x, kg);
-      values(vb, x);
+      values(vb, x, blk, !full, kg);
       tile_done();
       if (un >= end) break;
       u = un;
@@ -892,7 +911,7 @@ struct Rows {
 };
 
 template <int D, int NG, int NQ, bool SYM>
-__global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NG, NQ)) void kv4_rows_kernel(Kv4Attn a) {
+__global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NQ)) void kv4_rows_kernel(Kv4Attn a) {
   using R = Rows<D, NG, NQ, SYM>;
   __shared__ __attribute__((aligned(16))) uint8_t smem[R::kSmem];
   const int lane = threadIdx.x & 63;
