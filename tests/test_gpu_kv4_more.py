@@ -57,6 +57,16 @@ def test_one_prompt(q, kv, h, r, d, g):
     p.check(*p.run(), fp16_operands=True, what="one prompt")
 
 
+def test_long_prompt_beside_a_short_one():
+    # more row tiles than 8 per sequence: the lengths are scanned sequence by sequence
+    p = Problem(57, 64, 64, False, 32, "bf16", 2, 4, [1200, 30, 0], [1300, 30, 7])
+    announce_case(p, "long prompt beside a short one")
+    p.check(*p.run(), fp16_operands=True, what="long prompt beside a short one")
+    p = Problem(58, 64, 32, True, 16, "f16", 1, 8, [2, 1100], [90, 1100])
+    announce_case(p, "short prompt before a long one")
+    p.check(*p.run(window=300), window=300, fp16_operands=True, what="short prompt before a long one")
+
+
 @pytest.mark.parametrize("max_q", [1, 40])
 def test_more_sequences_than_lanes(max_q):
     gen = torch.Generator().manual_seed(3)
