@@ -104,7 +104,8 @@ gq_status gq_kv4_read(const uint8_t* cache, int64_t n_pages, gq_kv4_layout layou
  * take keys exactly (integers, or two fp16 parts); weights, and for more than 32
  * rows per key/value head values too, are rounded to fp16 once (2^-11), for
  * fp16 results of at most 8 rows the weights and of more than 32 rows the
- * values not at all. */
+ * values not at all.  Weights below 2^-22 of a row's largest have fewer bits
+ * (2^-25 for up to 32 rows, of weight times value scale), below 2^-33 (2^-36) none. */
 typedef struct {
   const void* q;
   int64_t q_token_stride, q_head_stride;

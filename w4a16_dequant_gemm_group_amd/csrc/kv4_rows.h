@@ -25,9 +25,12 @@ constexpr int kUnit = 32;            // tokens a wave takes at once (two sub-blo
 constexpr int kTile = kWaves * kUnit;  // tokens of a key tile, the grain of the split
 constexpr int kMetaInts = 8;
 constexpr float kNegInf = -__builtin_inff();
-// The running reference of the softmax is raised only when a score exceeds it
-// by this many powers of two: P stays below 2^9, well inside fp16.
-constexpr float kSlack = 8.0f;
+// The running reference of the softmax lies kRoom powers of two below the largest
+// score and is raised only when a score exceeds that by kSlack more: the largest
+// weight is 2^11 to 2^15 as fp16, so weights keep all their bits down to 2^-25 of
+// it and vanish below 2^-36.  With the largest at 1 and less room, what many light
+// keys add up to beside a heavy one was lost (4096 keys 18 nats behind: all of it).
+constexpr float kRoom = 11.0f, kSlack = 4.0f;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -425,7 +428,8 @@ __device__ __forceinline__ f16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32
 // P' = p S_V goes to the matrix cores as fp16, one operand per group; it is
 // rounded once (2^-11; `rest` below keeps what that leaves where it would show).  The reference that the exponentials subtract is the
 // running maximum of score + log2 S_V, so that P' itself, not p, is what lies
-// in fp16's range, whatever the scales are.
+// in fp16's range; a weight whose scale in one group is far below the largest of
+// its groups has that much less of the room above.
 template <int D, int NG, int NQ, bool SYM>
 struct Rows {
   static constexpr int NS = D / 32, SPG = NS / NG, TQ = 16 * NQ;
@@ -591,8 +595,8 @@ struct Rows {
         const uint32_t w = __builtin_bit_cast(uint32_t, b);
         const float f0 = __uint_as_float(__builtin_amdgcn_perm(0x4B000000u, w, 0x07060100u));
         const float f1 = __uint_as_float(__builtin_amdgcn_perm(0x4B000000u, w, 0x07060302u));
-        lv[t][2 * i] = __builtin_fmaf(f0, 1.0f / 1024.0f, -8207.0f);
-        lv[t][2 * i + 1] = __builtin_fmaf(f1, 1.0f / 1024.0f, -8207.0f);
+        lv[t][2 * i] = __builtin_fmaf(f0, 1.0f / 1024.0f, -8207.0f - kRoom);
+        lv[t][2 * i + 1] = __builtin_fmaf(f1, 1.0f / 1024.0f, -8207.0f - kRoom);
       }
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) {
@@ -898,7 +902,8 @@ struct Rows {
   }
 
   static __device__ __forceinline__ float lse_of(float M, float L) {
-    return L == 0.0f ? kNegInf : (M + __log2f(L)) * 0.69314718055994531f;
+    // kRoom moved from one term to the other, exactly: both are smaller so
+    return L == 0.0f ? kNegInf : (M + kRoom + __log2f(L * (1.0f / (1 << (int)kRoom)))) * 0.69314718055994531f;
   }
   static __device__ __forceinline__ uint32_t pack_out(int bf16, float a, float b) {
     if (bf16) return bf16_bits(a) | (uint32_t)bf16_bits(b) << 16;
