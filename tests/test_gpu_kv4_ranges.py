@@ -52,6 +52,20 @@ def check(what, out, lse, o, l, tol, ltol):
 FORMS = [(128, 128, False), (128, 32, False), (256, 64, False), (64, 32, True)]
 
 
+@pytest.mark.parametrize("n", [2, 70])
+@pytest.mark.parametrize("d,g,sym", FORMS)
+def test_large_queries(d, g, sym, n):
+    # queries up to bf16's largest, keys so small that the scores are ordinary
+    gen = torch.Generator().manual_seed(d + g)
+    for e in (90, 101, 102, 115, 127):
+        q = torch.randn(n, 2, d, generator=gen)
+        q[0, 0, 3], q[n - 1, 1, 5] = 1.9, -1.8
+        q = (q.clamp(-1.9, 1.9) * 2.0 ** e).to(torch.bfloat16)
+        k = (rows(gen, 200, 1, d, torch.bfloat16).double() * 2.0 ** -12).to(torch.bfloat16)
+        v = rows(gen, 200, 1, d, torch.bfloat16)
+        check(f"queries to 2^{e}", *attend(q, k, v, g, sym, scale=d ** -0.5 * 2.0 ** (11 - e)))
+
+
 def with_sink(gen, kv, d, dtype, ahead, spread=0.3):
     """Queries and keys such that key 0's score is `ahead` nats above the others'."""
     u = torch.randn(d, generator=gen)
