@@ -66,6 +66,18 @@ def test_large_queries(d, g, sym, n):
         check(f"queries to 2^{e}", *attend(q, k, v, g, sym, scale=d ** -0.5 * 2.0 ** (11 - e)))
 
 
+@pytest.mark.parametrize("n", [2, 70])
+@pytest.mark.parametrize("d,g,sym", FORMS)
+def test_tiny_scale(d, g, sym, n):
+    # scores that vanish in fp32: the mean of the keys that a row sees, no more of them
+    gen = torch.Generator().manual_seed(9 * d + g)
+    q = 1e-3 * torch.randn(n, 2, d, generator=gen)
+    k, v = rows(gen, 200, 1, d, torch.bfloat16), rows(gen, 200, 1, d, torch.bfloat16)
+    for scale in (1e-12, 1e-30, 1e-38):
+        check(f"scale {scale}", *attend(q.to(torch.bfloat16), k, v, g, sym, scale=scale))
+        check(f"scale {scale}, no query", *attend(torch.zeros_like(q).to(torch.bfloat16), k, v, g, sym, scale=scale))
+
+
 def with_sink(gen, kv, d, dtype, ahead, spread=0.3):
     """Queries and keys such that key 0's score is `ahead` nats above the others'."""
     u = torch.randn(d, generator=gen)

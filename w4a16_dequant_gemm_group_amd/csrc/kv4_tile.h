@@ -277,6 +277,8 @@ struct Tile {
     e = e < -60 ? -60 : (e > 127 ? 127 : e);   // 128: infinite or NaN
     const float f = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
     A = a.scale_log2 * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+    // never 0, which would make NaN of a hidden key's -inf; scores times 2^-100 vanish too
+    A = fmaxf(A, 0x1p-100f);
 #pragma unroll
     for (int st = 0; st < D / 16; ++st) {
       float x[8];
