@@ -68,6 +68,17 @@ def test_large_queries(d, g, sym, n):
 
 @pytest.mark.parametrize("n", [2, 70])
 @pytest.mark.parametrize("d,g,sym", FORMS)
+def test_small_queries(d, g, sym, n):
+    # queries down to bf16's smallest normal ones, a scale that makes up for it
+    gen = torch.Generator().manual_seed(11 * d + g)
+    for e in (-59, -64, -100, -124):
+        q = (torch.randn(n, 2, d, generator=gen) * 2.0 ** e).to(torch.bfloat16)
+        k, v = rows(gen, 200, 1, d, torch.bfloat16), rows(gen, 200, 1, d, torch.bfloat16)
+        check(f"queries of 2^{e}", *attend(q, k, v, g, sym, scale=d ** -0.5 * 2.0 ** -e))
+
+
+@pytest.mark.parametrize("n", [2, 70])
+@pytest.mark.parametrize("d,g,sym", FORMS)
 def test_tiny_scale(d, g, sym, n):
     # scores that vanish in fp32: the mean of the keys that a row sees, no more of them
     gen = torch.Generator().manual_seed(9 * d + g)

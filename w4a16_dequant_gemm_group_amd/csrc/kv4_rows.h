@@ -499,7 +499,7 @@ struct Rows {
       mx = fmaxf(mx, __shfl_xor(mx, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
       int e = (int)(__float_as_uint(mx) >> 23) - 127;   // exponent of the largest
-      e = e < -60 ? -60 : (e > 127 ? 127 : e);   // 128: infinite or NaN
+      e = e < -112 ? -112 : (e > 127 ? 127 : e);   // 128: infinite or NaN
       const float f = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
       A[nq] = a.scale_log2 * __uint_as_float((uint32_t)(127 - 14 + e) << 23);   // / f
 #pragma unroll

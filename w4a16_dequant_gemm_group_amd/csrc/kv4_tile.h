@@ -274,7 +274,7 @@ struct Tile {
     }
     mx = fmaxf(mx, __shfl_xor(mx, 32));
     int e = (int)(__float_as_uint(mx) >> 23) - 127;
-    e = e < -60 ? -60 : (e > 127 ? 127 : e);   // 128: infinite or NaN
+    e = e < -112 ? -112 : (e > 127 ? 127 : e);   // 128: infinite or NaN
     const float f = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
     A = a.scale_log2 * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
     // never 0, which would make NaN of a hidden key's -inf; scores times 2^-100 vanish too
