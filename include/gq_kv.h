@@ -61,7 +61,8 @@ gq_status gq_kv4_cache_bytes(int64_t n_pages, gq_kv4_layout layout, size_t* byte
  *          page_size - 1 (-1 by custom) is skipped.  Two tokens of one call on
  *          the same slot leave one of them, or a mix of both.
  * The codes, scales and zero points are those of gq_quantize_groups bit for
- * bit.  An infinite input saturates its group's scale; NaN leaves its group
+ * bit, but for the scale of a group of zeros, which is kept as 0 and not 1 (it
+ * stands for zeros either way).  An infinite input saturates its group's scale; NaN leaves its group
  * with unspecified but finite values.  Errors: INVALID_ARG (layout, shapes,
  * NULL), UNSUPPORTED (dtype, head_dim, device), MISALIGNED. */
 gq_status gq_kv4_write(const void* k, int64_t k_token_stride, int64_t k_head_stride,

@@ -113,3 +113,16 @@ def test_a_key_that_takes_nearly_all_the_weight(d, g, sym, n, dtype):
         if g < d:
             v[0, 0, :g] = torch.rand(g, generator=gen) * 4.0
         check(f"sink {ahead} ahead of {kv} keys", *attend(make_q(n, 2), k, v, g, sym, copies=300))
+
+
+@pytest.mark.parametrize("n,dtype", [(1, "f16"), (2, "bf16"), (9, "bf16"), (70, "bf16"), (70, "f16")])
+@pytest.mark.parametrize("d,g,sym", FORMS)
+def test_rows_of_zeros_beside_small_values(d, g, sym, n, dtype):
+    # a zero row stands for zeros whatever its scale is: it must not set the range
+    gen = torch.Generator().manual_seed(5 * d + g)
+    for ahead, small in ((12.0, 1e-3), (14.0, 0.02), (18.0, 1e-4)):
+        make_q, k = with_sink(gen, 3000, d, DT[dtype], ahead)
+        v = (rows(gen, 3000, 1, d, torch.float32).abs() * small).to(DT[dtype])
+        v[0] = 0.0
+        v[700:720] = 0.0
+        check(f"zero row {ahead} ahead of values of {small}", *attend(make_q(n, 2), k, v, g, sym, copies=300))

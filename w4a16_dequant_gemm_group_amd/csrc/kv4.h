@@ -8,8 +8,8 @@
 //   value codes  [4 token quads][16 m][4 tokens][NS] bytes
 //   value params S fp16 [NG][16 tokens] (symmetric), or [NG][4 token quads] of
 //                {S of 4 tokens, z of 4 tokens} fp16
-// A zero point z (an integer 0 .. 15) is kept as -(1024 + z), what a code takes
-// on as fp16 bits 0x6400 | c is short of c - z by.
+// A group of zeros has S = 0.  A zero point z (an integer 0 .. 15) is kept as
+// -(1024 + z), what a code takes on as fp16 bits 0x6400 | c is short of c - z by.
 // Both code orders are those in which the 16x16x32 matrix product takes its first
 // operand, whose lane (m = lane % 16, kg = lane / 16) holds row m and 8
 // consecutive k:

@@ -129,6 +129,9 @@ __device__ __forceinline__ Quant quantise(float (&x)[8], int g, uint32_t at) {
     extra += 0x4B400000u << (4 * sh);
   }
   r.codes = sum - extra;
+  // a group of zeros stands for them whatever its scale is; kept as 0, it does
+  // not pass for a group of large values where attention looks at the scales
+  if (hi + lo == 0.0f) r.S = 0;
   return r;
 }
 

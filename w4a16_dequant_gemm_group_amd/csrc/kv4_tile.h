@@ -119,12 +119,14 @@ struct Tile {
     return x > y ? x : y;
   }
 
-  // Exponent field of the largest of the wave's fp16 scales, and 2^-E for it; E
-  // = 0 where all are subnormal: they stay as they are.
-  static __device__ __forceinline__ uint32_t top_exponent(uint32_t top) { return wave_max(top) >> 10; }
-  static __device__ __forceinline__ float pow2_neg(uint32_t e) {
-    return __uint_as_float((e ? 142 - e : 127) << 23);
+  // Exponent field of the largest of the wave's fp16 scales, and 2^-E for it.
+  // Subnormal ones, and zeros (rows of zeros), count as the smallest normal one:
+  // with E = 0 for them a block of zeros would set the reference of the softmax.
+  static __device__ __forceinline__ uint32_t top_exponent(uint32_t top) {
+    const uint32_t e = wave_max(top) >> 10;
+    return e ? e : 1;
   }
+  static __device__ __forceinline__ float pow2_neg(uint32_t e) { return __uint_as_float((142 - e) << 23); }
 
   // Keys.  Parts: x^ / 2^E as fp16, E the exponent of the largest scale of the
   // 16, and what its rounding left, as fp16 too: together x^ to 2^-22.  2^E
@@ -149,7 +151,7 @@ struct Tile {
     if constexpr (SPLIT) {
       const uint32_t e = top_exponent(top);
       inv = pow2_neg(e);
-      if (m == 0 && kg == 0) ((float*)(buf + kEx))[8 + blk] = __uint_as_float((e ? 112 + e : 127) << 23);
+      if (m == 0 && kg == 0) ((float*)(buf + kEx))[8 + blk] = __uint_as_float((112 + e) << 23);
     } else if (kg == 0) {
       // scale of token m: the lanes of one result half take 16 tokens of 32 in
       // the order 8 (i / 4) + 4 half + i % 4
@@ -217,7 +219,7 @@ struct Tile {
     if (m == 0 && kg == 0) {
       float* ex = (float*)(buf + kEx);
       // -inf takes keys that do not exist out of the softmax
-      ex[blk] = c.ok ? (e ? (float)((int)e - 15) : 0.0f) : kNegInf;
+      ex[blk] = c.ok ? (float)((int)e - 15) : kNegInf;
       ex[4 + blk] = inv;
     }
     uint8_t* vb = buf + kV + blk * 32 + (kg & 1) * 16 + (kg >> 1) * 8;
