@@ -126,3 +126,20 @@ def test_rows_of_zeros_beside_small_values(d, g, sym, n, dtype):
         v[0] = 0.0
         v[700:720] = 0.0
         check(f"zero row {ahead} ahead of values of {small}", *attend(make_q(n, 2), k, v, g, sym, copies=300))
+
+
+@pytest.mark.parametrize("n,dtype", [(2, "bf16"), (70, "bf16"), (70, "f16")])
+@pytest.mark.parametrize("d,g,sym", FORMS)
+def test_neighbours_of_very_different_size(d, g, sym, n, dtype):
+    # key 21 and its value are 2^19 times those of the tokens around them, but no
+    # query gives it weight: the others lose nothing by standing next to it
+    gen = torch.Generator().manual_seed(7 * d + g)
+    kv = 96
+    q = 1.5 * torch.randn(n, 2, d, generator=gen)
+    q[..., 0] = -1.0
+    k, v = 2.0 ** -6 * rows(gen, kv, 1, d, torch.float32), 2.0 ** -8 * rows(gen, kv, 1, d, torch.float32)
+    k[..., 0] = 0.0
+    k[21] = 0.0
+    k[21, 0, 0], k[21, 0, 1] = 2.0 ** 15, 2.0 ** -12
+    v[21] = 2.0 ** 14 * torch.rand(1, d, generator=gen)
+    check("neighbours of different size", *attend(q.to(DT[dtype]), k.to(DT[dtype]), v.to(DT[dtype]), g, sym))

@@ -119,19 +119,21 @@ struct Tile {
     return x > y ? x : y;
   }
 
-  // Exponent field of the largest of the wave's fp16 scales, and 2^-E for it.
-  // Subnormal ones, and zeros (rows of zeros), count as the smallest normal one:
-  // with E = 0 for them a block of zeros would set the reference of the softmax.
+  // Exponent field of the largest of the wave's fp16 scales, and 2^-E for it: E is
+  // ten less than its exponent, so that codes times scales reach 2^15, the end of
+  // fp16's range, and scales down to 2^-24 of the largest keep their bits beside it
+  // (2^-14 with E its exponent).  Subnormal ones, and zeros (rows of zeros), count as
+  // the smallest normal one: as 2^0 a block of zeros would set the softmax's reference.
   static __device__ __forceinline__ uint32_t top_exponent(uint32_t top) {
     const uint32_t e = wave_max(top) >> 10;
     return e ? e : 1;
   }
-  static __device__ __forceinline__ float pow2_neg(uint32_t e) { return __uint_as_float((142 - e) << 23); }
+  static __device__ __forceinline__ float pow2_neg(uint32_t e) { return __uint_as_float((152 - e) << 23); }
 
-  // Keys.  Parts: x^ / 2^E as fp16, E the exponent of the largest scale of the
-  // 16, and what its rounding left, as fp16 too: together x^ to 2^-22.  2^E
-  // comes back in the factor of the scores.  Keys that no row sees count as
-  // zeros, whatever their memory holds.
+  // Keys.  Parts: x^ / 2^E as fp16, E from the largest scale of the 16, and what
+  // its rounding left, as fp16 too: together x^ to 2^-22 of it, or 2^-34 of the
+  // largest of the 16.  2^E comes back in the factor of the scores.  Keys that no
+  // row sees count as zeros, whatever their memory holds.
   static __device__ __forceinline__ void expand_k(const Nibbles& nib, Codes& c, const Span& sp, uint8_t* buf,
                                                   int blk, int m, int kg) {
     if (!(c.ok && c.pos >= sp.lo && c.pos + 16 <= sp.hi)) {
@@ -151,7 +153,7 @@ struct Tile {
     if constexpr (SPLIT) {
       const uint32_t e = top_exponent(top);
       inv = pow2_neg(e);
-      if (m == 0 && kg == 0) ((float*)(buf + kEx))[8 + blk] = __uint_as_float((112 + e) << 23);
+      if (m == 0 && kg == 0) ((float*)(buf + kEx))[8 + blk] = __uint_as_float((102 + e) << 23);
     } else if (kg == 0) {
       // scale of token m: the lanes of one result half take 16 tokens of 32 in
       // the order 8 (i / 4) + 4 half + i % 4
@@ -190,9 +192,9 @@ struct Tile {
     }
   }
 
-  // Values: x^ / 2^E as fp16 (F16: and what the rounding left); E is the exponent of the
-  // largest scale of the 16, so that they lie in fp16's normal range whatever
-  // the scales are.  2^E comes back in the exponent of P.
+  // Values: x^ / 2^E as fp16 (F16: and what the rounding left), E from the largest
+  // scale of the 16: values down to 2^-28 of the largest of them are normal numbers.
+  // 2^E comes back in the exponent of P.
   static __device__ __forceinline__ void expand_v(const Nibbles& nib, Codes& c, const Span& sp, uint8_t* buf, int blk, int m,
                                                   int kg) {
     if (!(c.ok && c.pos >= sp.lo && c.pos + 16 <= sp.hi)) {
@@ -219,7 +221,7 @@ struct Tile {
     if (m == 0 && kg == 0) {
       float* ex = (float*)(buf + kEx);
       // -inf takes keys that do not exist out of the softmax
-      ex[blk] = c.ok ? (float)((int)e - 15) : kNegInf;
+      ex[blk] = c.ok ? (float)((int)e - 25) : kNegInf;
       ex[4 + blk] = inv;
     }
     uint8_t* vb = buf + kV + blk * 32 + (kg & 1) * 16 + (kg >> 1) * 8;
