@@ -106,10 +106,9 @@ gq_status gq_kv4_read(const uint8_t* cache, int64_t n_pages, gq_kv4_layout layou
  * rows per key/value head values too, are rounded to fp16 once (2^-11), for
  * fp16 results of at most 8 rows the weights and of more than 32 rows the
  * values not at all.  Weights below 2^-22 of a row's largest have fewer bits
- * (2^-25 for up to 32 rows, of weight times value scale), below 2^-33 (2^-36) none;
- * so have, for more than 32 rows, values below 2^-28 and keys below 2^-34 of the
- * largest element among the 16 tokens of a sub-block.  Scores have to lie in
- * fp32's range. */
+ * (2^-25 for up to 32 rows, of weight times value scale), below 2^-33 (2^-36) none.
+ * For more than 32 rows keys and values are also off by up to 2^-33 of the largest
+ * element among the 16 tokens of a sub-block.  Scores have to lie in fp32's range. */
 typedef struct {
   const void* q;
   int64_t q_token_stride, q_head_stride;

@@ -131,7 +131,7 @@ struct Tile {
   static __device__ __forceinline__ float pow2_neg(uint32_t e) { return __uint_as_float((152 - e) << 23); }
 
   // Keys.  Parts: x^ / 2^E as fp16, E from the largest scale of the 16, and what
-  // its rounding left, as fp16 too: together x^ to 2^-22 of it, or 2^-34 of the
+  // its rounding left, as fp16 too: together x^ to 2^-22 of it and 2^-33 of the
   // largest of the 16.  2^E comes back in the factor of the scores.  Keys that no
   // row sees count as zeros, whatever their memory holds.
   static __device__ __forceinline__ void expand_k(const Nibbles& nib, Codes& c, const Span& sp, uint8_t* buf,
@@ -193,7 +193,7 @@ struct Tile {
   }
 
   // Values: x^ / 2^E as fp16 (F16: and what the rounding left), E from the largest
-  // scale of the 16: values down to 2^-28 of the largest of them are normal numbers.
+  // scale of the 16: x^ to 2^-11 of it (2^-22) and 2^-33 of the largest of them.
   // 2^E comes back in the exponent of P.
   static __device__ __forceinline__ void expand_v(const Nibbles& nib, Codes& c, const Span& sp, uint8_t* buf, int blk, int m,
                                                   int kg) {
