@@ -48,8 +48,8 @@ typedef struct {
 
 /* Bytes of a cache of n_pages pages: per token and head, for keys and for
  * values, head_dim / 2 bytes of codes and 2 (symmetric) or 4 bytes per group.
- * Host only.  Errors: INVALID_ARG (n_pages < 1 or >= 2^31, the layout's limits,
- * a NULL `bytes`), UNSUPPORTED (head_dim). */
+ * Host only.  Errors: INVALID_ARG (n_pages < 1 or >= 2^31, 2^63 bytes or more
+ * (so in every call), the layout's limits, a NULL `bytes`), UNSUPPORTED (head_dim). */
 gq_status gq_kv4_cache_bytes(int64_t n_pages, gq_kv4_layout layout, size_t* bytes);
 
 /* Quantize keys and values into the cache.

@@ -32,9 +32,18 @@ gq_status check_layout(const gq_kv4_layout& y) {
   return GQ_OK;
 }
 
+// Bytes of 16 tokens of one head.
+uint32_t params_bytes(const gq_kv4_layout& y) {
+  return 16u * (uint32_t)(y.head_dim / y.group_size) * (y.symmetric ? 2u : 4u);
+}
+uint32_t block_bytes(const gq_kv4_layout& y) { return 2u * (8u * (uint32_t)y.head_dim + params_bytes(y)); }
+
+// Also that every offset into the cache fits 63 bits.
 gq_status check_cache(int64_t n_pages, const gq_kv4_layout& y) {
   if (gq_status s = check_layout(y)) return s;
   if (n_pages < 1 || n_pages > INT32_MAX) return GQ_ERR_INVALID_ARG;
+  const int64_t page = (int64_t)y.kv_heads * (y.page_size / 16) * block_bytes(y);
+  if (n_pages > INT64_MAX / page) return GQ_ERR_INVALID_ARG;
   return GQ_OK;
 }
 
@@ -48,8 +57,8 @@ Kv4Geo geometry(const uint8_t* cache, int64_t n_pages, const gq_kv4_layout& y) {
   c.ng = y.head_dim / y.group_size;
   c.sym = y.symmetric;
   c.page_shift = __builtin_ctz((unsigned)y.page_size);
-  c.meta = 16u * c.ng * (c.sym ? 2u : 4u);
-  c.sb = 2u * (8u * c.d + c.meta);
+  c.meta = params_bytes(y);
+  c.sb = block_bytes(y);
   return c;
 }
 
