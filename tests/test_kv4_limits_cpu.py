@@ -29,3 +29,19 @@ def test_the_largest_cache_that_fits_is_accepted():
     pages = ((1 << 63) - 1) // PAGE
     assert B.lib().gq_kv4_cache_bytes(pages, layout(**WIDE), ctypes.byref(n)) == B.GQ_OK
     assert n.value == pages * PAGE
+
+
+def workspace(**kw):
+    n = ctypes.c_size_t()
+    assert B.lib().gq_kv4_attention_workspace_size(ctypes.byref(attn_args(**kw)), ctypes.byref(n)) == B.GQ_OK
+    return n.value
+
+
+def test_workgroups_do_not_run_out_at_the_largest_sizes():
+    # tiles of the split were counted past 63 bits: 8 workgroups for the whole call
+    plain = workspace(layout=layout(kv_heads=1), q_heads=1, batch=64, q_tokens=64 * 4096, q_starts=FAKE,
+                      max_q_len=4096, max_kv_len=4096)
+    for max_kv in (0, 1, 1 << 20, 1 << 30):
+        huge = workspace(layout=layout(kv_heads=65535), q_heads=65535, batch=1 << 24, q_tokens=1, q_starts=FAKE,
+                         max_q_len=1 << 30, max_kv_len=max_kv)
+        assert huge == plain

@@ -113,11 +113,13 @@ Kv4Plan kv4_plan(const gq_kv4_attention_args& a) {
   const int64_t row_tiles = (a.q_tokens * r / tq + std::min(a.batch, a.q_tokens)) * a.layout.kv_heads;
   p.grain = p.tile ? 6 : 7;
   while (p.grain < 30 && row_tiles * ((cap >> p.grain) + 1 + kOverhead) >= INT32_MAX) ++p.grain;
-  const int64_t segs = a.batch * a.layout.kv_heads * p.grid_q;
+  // counted up to 2^24: so many row tiles are split and take all workgroups in any case
+  constexpr int64_t kMany = (int64_t)1 << 24;
+  const int64_t segs = std::min(kMany, std::min(kMany, a.batch * a.layout.kv_heads) * p.grid_q);
   const int64_t tiles = segs * (kOverhead + ((a.max_kv_len + (1 << p.grain) - 1) >> p.grain));
   // up to 1024 keys a workgroup per row tile, without the second kernel, is
   // faster than the split (a launch takes fewer than 2^32 threads)
-  p.split = p.tile || a.max_kv_len > 1024 || segs >= (int64_t)1 << 24;
+  p.split = p.tile || a.max_kv_len > 1024 || segs >= kMany;
   if (p.split) {
     // as many workgroups (a wave on each SIMD) as run at once
     const int64_t want = (int64_t)num_cus() * (p.tile ? 1 : kv4_rows_waves(d, p.nq));
