@@ -280,7 +280,7 @@ __device__ __forceinline__ void dma16(const uint8_t* p, uint32_t voff, uint32_t 
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
                : "s"(lds), "v"(voff), "s"(p)
-               : "memory");
+               : "memory", "m0");
 }
 // Until at most N of the wave's loads are under way.
 template <int N>
