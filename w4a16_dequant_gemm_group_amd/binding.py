@@ -133,11 +133,18 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it, a third of a small
+# call's host time.  Not part of torch's public interface: where a torch lacks it, the
+# public way is taken.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
-    """Handle of a stream (default: the current device's current one, taken without
-    building a Stream object around it, a third of a small call's host time)."""
+    """Handle of a stream (default: the current device's current one)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
