@@ -16,8 +16,8 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 constexpr int kOverhead = 2;
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;
-// Tokens of one launch of the storage kernels: 8 rows per workgroup at least,
-// 2^32 threads at most over all heads' grid columns.
+// Tokens of one launch of the storage kernels: at 8 rows per workgroup of 256
+// threads at least, 2^29 threads along the grid's first dimension (2^32 is the end).
 constexpr int64_t kLaunchTokens = (int64_t)1 << 24;
 
 gq_status check_layout(const gq_kv4_layout& y) {
