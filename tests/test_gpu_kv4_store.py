@@ -65,3 +65,24 @@ def test_storage_calls_of_more_than_one_launch():
         for a in range(0, t, 1 << 22):
             b = min(t, a + (1 << 22))
             assert torch.equal(got[a:b], ref[slots[a:b].clamp(0, n_pages * page - 1)] * ok[a:b, None, None])
+
+
+@pytest.mark.parametrize("d,g,sym,h", [(64, 32, True, 8), (96, 96, False, 8), (128, 64, False, 8), (256, 32, False, 4)])
+def test_results_past_the_last_cache(d, g, sym, h):
+    # from 2^28 bytes on a lane reads four rows of 16-bit results: as in pieces, where it reads one
+    row = d // 2 + (2 if sym else 4) * (d // g)
+    t = (1 << 28) // (h * (4 * d + 2 * row)) + 77
+    announce(f"kv4 read of {t} tokens d={d} g={g} h={h}")
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    n_pages = 40
+    k = torch.randn(n_pages * 64, h, d, generator=gen, device="cuda").to(torch.bfloat16)
+    v = torch.randn(n_pages * 64, h, d, generator=gen, device="cuda").to(torch.bfloat16)
+    cache = B.gq_kv4_empty(n_pages, h, d, 64, g, sym)
+    B.gq_kv4_write(k, v, cache, torch.arange(n_pages * 64, device="cuda"), g, sym)
+    slots = torch.randint(0, n_pages * 64, (t,), generator=gen, device="cuda")
+    slots[9], slots[t - 2] = -1, n_pages * 64
+    for odt in (torch.bfloat16, torch.float16):
+        ko, vo = B.gq_kv4_read(cache, slots, d, g, sym, odt)
+        for a in range(0, t, 4000):
+            kw, vw = B.gq_kv4_read(cache, slots[a:a + 4000], d, g, sym, odt)
+            assert torch.equal(ko[a:a + 4000], kw) and torch.equal(vo[a:a + 4000], vw)

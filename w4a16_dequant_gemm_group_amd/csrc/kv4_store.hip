@@ -342,8 +342,12 @@ hipError_t launch_kv4_write(const void* k, int64_t k_ts, int64_t k_hs, const voi
 
 hipError_t launch_kv4_read(const Kv4Geo& c, const int64_t* slots, int64_t tokens, void* k, void* v,
                            gq_dtype odt, hipStream_t s) {
-  // few rows: one per lane, spread over the most workgroups
-  const bool many = tokens * c.hkv >= 65536;
+  // Four rows per lane where 16-bit results and what they are made of pass the 256 MB
+  // that the card's last cache holds (8 heads of 128, 57 K tokens 77 -> 70 us, 131 K 179
+  // -> 155; 4 heads of 256 197 -> 153); up to there one row is as fast or faster (8 heads
+  // of 64, 33 K tokens 17.0 against 18.5), for fp32 results beyond it too (156 against 167).
+  const int64_t bytes = tokens * c.hkv * (4 * c.d + c.sb / 16);
+  const bool many = odt != GQ_F32 && bytes >= (int64_t)1 << 28;
 #define GQ_KV4_READ(D)                                                                                \
   if (many)                                                                                           \
     hipLaunchKernelGGL((kv4_read_kernel<D, 4>), grid_of<D>(tokens, c.hkv, 4), dim3(kThreads), 0, s, c, \
