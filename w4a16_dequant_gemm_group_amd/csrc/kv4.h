@@ -85,11 +85,15 @@ struct Kv4Attn {
   float* part;                       // [2 * workers][rows][D + 2] partial results
 };
 
-// Waves per SIMD of the rows kernel (d channels, nq tiles of 16 rows): what its
-// registers allow, and no more than three, as each workgroup has fixed work (128
-// K keys with 2 groups: 39 us with two, 36 with three; 64 ragged sequences with
-// 4 groups: 88 with two, 79 with three).
-constexpr int kv4_rows_waves(int d, int nq) { return d * nq > 256 ? 1 : d > 128 || nq > 1 ? 2 : 3; }
+// Waves per SIMD of the rows kernel (d channels in ng groups, nq tiles of 16 rows),
+// which limits their registers.  16 sequences of 8192 keys, 8 key/value heads, with
+// as many as here / one fewer: 128 channels 35 / 39 us, in 4 groups 43 / 48 (though
+// with two row tiles 30 registers spill: 69 / 88); 256 channels 60 / 69, in 4 groups
+// 70 / 86, in 8 groups one wave: 106, two spill 50 registers in the loop, 117.
+constexpr int kv4_rows_waves(int d, int ng, int nq) {
+  if (d * nq > 256 || ng > 4) return 1;
+  return d > 128 || nq > 1 ? 2 : 3;
+}
 
 struct Kv4Plan {
   bool tile;           // the kernel for many rows; else the rows kernel

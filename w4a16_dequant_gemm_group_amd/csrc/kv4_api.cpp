@@ -122,7 +122,7 @@ Kv4Plan kv4_plan(const gq_kv4_attention_args& a) {
   p.split = p.tile || a.max_kv_len > 1024 || segs >= kMany;
   if (p.split) {
     // as many workgroups (a wave on each SIMD) as run at once
-    const int64_t want = (int64_t)num_cus() * (p.tile ? 1 : kv4_rows_waves(d, p.nq));
+    const int64_t want = (int64_t)num_cus() * (p.tile ? 1 : kv4_rows_waves(d, d / a.layout.group_size, p.nq));
     p.workers = (int)std::max<int64_t>(8, std::min(tiles, want) & ~(int64_t)7);
     p.ws_bytes = (size_t)p.workers * 32 + (size_t)p.workers * 2 * tq * (d + 2) * sizeof(float);
   }

@@ -916,7 +916,7 @@ struct Rows {
 };
 
 template <int D, int NG, int NQ, bool SYM>
-__global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NQ)) void kv4_rows_kernel(Kv4Attn a) {
+__global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NG, NQ)) void kv4_rows_kernel(Kv4Attn a) {
   using R = Rows<D, NG, NQ, SYM>;
   __shared__ __attribute__((aligned(16))) uint8_t smem[R::kSmem];
   const int lane = threadIdx.x & 63;
