@@ -45,3 +45,10 @@ def test_workgroups_do_not_run_out_at_the_largest_sizes():
         huge = workspace(layout=layout(kv_heads=65535), q_heads=65535, batch=1 << 24, q_tokens=1, q_starts=FAKE,
                          max_q_len=1 << 30, max_kv_len=max_kv)
         assert huge == plain
+
+
+def test_few_row_tiles_are_split_from_fewer_keys_on():
+    # 512 keys and 8 more per row tile, 1024 at most, go to one workgroup without scratch
+    for batch, limit in ((1, 576), (4, 768), (8, 1024), (100, 1024)):
+        a = dict(batch=batch, q_tokens=batch, max_q_len=1)
+        assert workspace(max_kv_len=limit, **a) == 0 and workspace(max_kv_len=limit + 1, **a) > 0

@@ -117,9 +117,14 @@ Kv4Plan kv4_plan(const gq_kv4_attention_args& a) {
   constexpr int64_t kMany = (int64_t)1 << 24;
   const int64_t segs = std::min(kMany, std::min(kMany, a.batch * a.layout.kv_heads) * p.grid_q);
   const int64_t tiles = segs * (kOverhead + ((a.max_kv_len + (1 << p.grain) - 1) >> p.grain));
-  // up to 1024 keys a workgroup per row tile, without the second kernel, is
-  // faster than the split (a launch takes fewer than 2^32 threads)
-  p.split = p.tile || a.max_kv_len > 1024 || segs >= kMany;
+  // One workgroup per row tile, without the second kernel, as long as that is faster
+  // than the split, which spreads few row tiles over the card.  Equal lengths of 512 /
+  // 1024 keys, one against split: 8 row tiles of 128 channels 9.9 : 11.0 / 14.0 : 11.3
+  // us, 64 of 256 channels 14.6 : 17.6 / 21.2 : 21.3, 128 of 128 channels 10.2 : 13.8 /
+  // 14.4 : 16.5, 512 14.6 : 21.7 / 22 : 31.  Of more row tiles it would be faster for
+  // longer (512: 4096 keys), but one long sequence among short ones runs alone then.
+  // (A launch takes fewer than 2^32 threads.)
+  p.split = p.tile || a.max_kv_len > std::min<int64_t>(1024, 512 + 8 * segs) || segs >= kMany;
   if (p.split) {
     // as many workgroups (a wave on each SIMD) as run at once
     const int64_t want = (int64_t)num_cus() * (p.tile ? 1 : kv4_rows_waves(d, d / a.layout.group_size, p.nq));
