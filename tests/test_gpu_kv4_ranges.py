@@ -143,3 +143,22 @@ def test_neighbours_of_very_different_size(d, g, sym, n, dtype):
     k[21, 0, 0], k[21, 0, 1] = 2.0 ** 15, 2.0 ** -12
     v[21] = 2.0 ** 14 * torch.rand(1, d, generator=gen)
     check("neighbours of different size", *attend(q.to(DT[dtype]), k.to(DT[dtype]), v.to(DT[dtype]), g, sym))
+
+
+@pytest.mark.parametrize("n", [2, 70])
+@pytest.mark.parametrize("d,g,sym", FORMS)
+def test_nonfinite_queries_that_see_no_key(d, g, sym, n):
+    # pages that do not exist, whole or from some page on; keys after a query's position
+    announce(f"kv4 non-finite queries without keys d={d} g={g} n={n}")
+    gen = torch.Generator().manual_seed(d)
+    cache = B.gq_kv4_empty(8, 1, d, 16, g, sym)
+    k = rows(gen, 128, 1, d, torch.bfloat16).cuda()
+    B.gq_kv4_write(k, k, cache, torch.arange(128, device="cuda"), g, sym)
+    q = torch.randn(3 * n, 2, d, generator=gen).to(torch.bfloat16)
+    q[:, 0, 3], q[:, 1, 5] = math.nan, -math.inf
+    table = torch.tensor([[-1] * 8, [8, -5, 1 << 30, 9, -1, -1, -1, -1], list(range(8))], dtype=torch.int32)
+    lens = torch.tensor([128, 77, 0], dtype=torch.int32)
+    out, lse = B.gq_kv4_attention(q.cuda(), cache, table.cuda(), lens.cuda(), g, sym,
+                                  q_starts=torch.tensor([0, n, 2 * n, 3 * n], dtype=torch.int32).cuda(), max_q_len=n,
+                                  max_kv_len=128, causal=False, return_lse=True)
+    assert not out.any() and (lse == -math.inf).all()

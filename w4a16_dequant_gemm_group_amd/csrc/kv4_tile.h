@@ -390,12 +390,18 @@ struct Tile {
     };
 #pragma unroll
     for (int r = 0; r < kAhead; ++r) ring[r] = read_v(r);
+    // per 16 keys, the scores have the factor 2^E of the keys and P that of the values
+    const float4 ev = *(const float4*)(buf + kEx), ei = *(const float4*)(buf + kEx + 16);
+    const float evv[4] = {ev.x, ev.y, ev.z, ev.w}, eiv[4] = {ei.x, ei.y, ei.z, ei.w};
+    const float least = fminf(fminf(ev.x, ev.y), fminf(ev.z, ev.w));
     // whether every row of the wave sees all 64 keys
     const int rows = s.n * a.r;
     const int lastrow = row0 + 32 < rows ? row0 + 31 : rows - 1;
     bool full = u + kTK <= s.kv;
     if (a.causal) full = full && u + kTK - 1 <= s.kv - s.n + div_r(a, row0);
     if (a.window > 0) full = full && u > s.kv - s.n + div_r(a, lastrow) - a.window;
+    // and all of them exist: a query that is not finite makes NaN of the zeros that stand there
+    full = full && __builtin_amdgcn_readfirstlane(__float_as_uint(least)) != __float_as_uint(kNegInf);
     if (!full) {
       const int pos = s.kv - s.n + div_r(a, row0 + n);
       const int last = a.causal && pos < s.kv - 1 ? pos : s.kv - 1;
@@ -405,12 +411,9 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int j = u + 32 * tt + 8 * (i / 4) + 4 * hf + (i & 3);
-          x[tt][i] = j <= last && j >= first ? x[tt][i] : kNegInf;
+          x[tt][i] = j <= last && j >= first && evv[2 * tt + i / 8] != kNegInf ? x[tt][i] : kNegInf;
         }
     }
-    // per 16 keys, the scores have the factor 2^E of the keys and P that of the values
-    const float4 ev = *(const float4*)(buf + kEx), ei = *(const float4*)(buf + kEx + 16);
-    const float evv[4] = {ev.x, ev.y, ev.z, ev.w}, eiv[4] = {ei.x, ei.y, ei.z, ei.w};
     float Ab[4] = {A, A, A, A};
     if constexpr (SPLIT) {
       const float4 ek = *(const float4*)(buf + kEx + 32);
