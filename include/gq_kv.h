@@ -102,10 +102,11 @@ gq_status gq_kv4_read(const uint8_t* cache, int64_t n_pages, gq_kv4_layout layou
  *   out        [q_tokens, q_heads, head_dim] of dtype, contiguous, 16-byte aligned
  *   lse        [q_tokens, q_heads] float, or NULL
  * Scores, softmax statistics and outputs are kept in fp32.  The matrix cores
- * take keys exactly (integers, or two fp16 parts); weights, and for more than 32
- * rows per key/value head values too, are rounded to fp16 once (2^-11), for
- * fp16 results of at most 8 rows the weights and of more than 32 rows the
- * values not at all.  Weights below 2^-22 of a row's largest have fewer bits
+ * take keys exactly (integers, or two fp16 parts) and queries as fp16 times a power
+ * of two per row (elements below 2^-29 of a row's largest have fewer bits); weights,
+ * and for more than 32 rows per key/value head values too, are rounded to fp16 once
+ * (2^-11), for fp16 results of at most 8 rows the weights and of more than 32 rows
+ * the values not at all.  Weights below 2^-22 of a row's largest have fewer bits
  * (2^-25 for up to 32 rows, of weight times value scale), below 2^-33 (2^-36) none.
  * For more than 32 rows keys and values are also off by up to 2^-33 of the largest
  * element among the 16 tokens of a sub-block.  Scores have to lie in fp32's range. */

@@ -420,16 +420,20 @@ __device__ __forceinline__ f16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32
 // What bounds it: vector instructions, most of them the expansion of the codes.
 // Of a unit of 32 keys at 128 channels 176 of some 300 make the operands of its 16
 // products; counters show the vector unit 70 to 76 % busy, the matrix unit 10 %,
-// and no byte fetched twice.  151 MB of one sequence of 128 K keys pass in 36 us
-// (4.2 TB/s; a copy reaches 5.0), 332 MB of 64 ragged ones in 79 us (4.2).
+// and no byte fetched twice.  151 MB of one sequence of 128 K keys pass in 35.5 us
+// (4.2 TB/s; a copy reaches 5.0), 332 MB of 64 ragged ones in 79 us (4.2; 94 to 99
+// where passes follow each other for milliseconds).
 // Q becomes fp16 with a power of two per row that puts its largest element
 // near 2^14: exact for fp16 and bf16 elements down to 2^-29 of the largest.
 // So the scores are exact up to fp32 sums: s = sum_g S_g ((codes - z) . q).
 // P' = p S_V goes to the matrix cores as fp16, one operand per group; it is
-// rounded once (2^-11; `rest` below keeps what that leaves where it would show).  The reference that the exponentials subtract is the
-// running maximum of score + log2 S_V, so that P' itself, not p, is what lies
-// in fp16's range; a weight whose scale in one group is far below the largest of
-// its groups has that much less of the room above.
+// rounded once (2^-11; `rest` below keeps what that leaves where it would show most,
+// in fp16 results of the fewest rows: elsewhere a second part would double the second
+// products, and in bf16 results it is an eighth of their own rounding).
+// The reference that the exponentials subtract is the running maximum of score +
+// log2 S_V, so that P' itself, not p, is what lies in fp16's range; a weight whose
+// scale in one group is far below the largest of its groups has that much less of
+// the room above.
 template <int D, int NG, int NQ, bool SYM>
 struct Rows {
   static constexpr int NS = D / 32, SPG = NS / NG, TQ = 16 * NQ;
@@ -976,8 +980,8 @@ __global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NG, NQ)) void kv4_ro
 }
 
 // Joins the partial results of the row tiles that were split: 4 to 6 us for
-// single tokens (latency: two dependent loads, then the partials), 13 us for a
-// prompt of 4096 (the partials of all its rows, 30 MB).  Worker w left
+// single tokens (latency: two dependent loads, then the partials), 12.5 us for a
+// prompt of 4096 (464 partials of 232 of its 512 row tiles, 62 MB).  Worker w left
 // its last row tile open: the workers after it, up to `last`, hold the rest.
 // One workgroup per worker and RW rows at a time: D / 4 threads hold a row, PG
 // such sets take every PG-th partial of it (many partials of few rows for

@@ -9,8 +9,8 @@
 // the same workgroup, in the L2 cache, for consecutive slots.
 //
 // 16 K tokens of 8 heads of 128: written in 21 us (86 MB, 4.1 TB/s; bound by
-// vector instructions, 21 per pair of values), read back in 17 us; 64 K tokens
-// read back in 81 us (340 MB, 4.2 TB/s; a copy reaches 5.0).  All tokens of one
+// vector instructions, 22 per pair of values), read back in 17 us; 64 K tokens
+// read back in 80 to 86 us (340 MB, 4.2 TB/s; a copy reaches 5.0).  All tokens of one
 // head before the next, or all heads of a token first, measured level.
 #include "kv4.h"
 #include "stream_util.h"

@@ -15,8 +15,9 @@
 // unit 55 % busy, matrix unit 38 %; reading the operands from LDS takes as long
 // as the products (one 1 KiB operand each).  Rates: 212 us or 650 TFLOP/s there,
 // where a library product of 8192^3 reaches 1190; ragged chunks with groups of
-// 32 and fp16 results 171 us (twice the products, see below); a window of 4096
-// keys at 256 channels 93 us.
+// 32 and fp16 results 170 us (twice the products, see below); a window of 4096
+// keys at 256 channels 91.5 us (one wave a SIMD, and a quarter to a third of its
+// vector instructions only move accumulation registers).
 #pragma once
 
 #include "kv4_rows.h"
@@ -442,7 +443,9 @@ struct Tile {
     const float base = mref == kNegInf ? 0.0f : mref;
     f16x8 pw[2];
     float sum[2];
-    // weights from .. to - 1 of 16 keys' 8 in this lane
+    // weights from .. to - 1 of 16 keys' 8 in this lane.  They are rounded to fp16
+    // (2^-11, their sum is not): fp16 results are off by 2.6e-4 where their own
+    // rounding alone makes 2.1e-4; a second part would double the second products.
     auto weigh = [&](int b, int from, int to) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
