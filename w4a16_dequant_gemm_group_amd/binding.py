@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libgq (``include/gq.h``, ``include/gq_kv.h``), same names as the C ABI.
+"""Thin ctypes binding of libgq (``include/gq.h``, ``gq_kv.h``, ``gq_kv8.h``, ``gq_rope.h``),
+same names as the C ABI.
 
 The functions here only marshal arguments: they check the dtype, shape,
 contiguity and device of every torch tensor they pass (inputs and
@@ -33,6 +34,11 @@ EXPORTS = (
 # the 4-bit key/value cache and its attention (include/gq_kv.h)
 KV_EXPORTS = ("gq_kv4_cache_bytes", "gq_kv4_write", "gq_kv4_read",
               "gq_kv4_attention_workspace_size", "gq_kv4_attention")
+# rotary positions (include/gq_rope.h)
+ROPE_EXPORTS = ("gq_rope_frequencies", "gq_rope")
+# the 8-bit key/value cache, its attention and the choice of pages (include/gq_kv8.h)
+KV8_EXPORTS = ("gq_kv8_cache_bytes", "gq_kv8_append", "gq_kv8_read", "gq_kv8_attention_workspace_size",
+               "gq_kv8_attention", "gq_kv8_select_workspace_size", "gq_kv8_select")
 # comparators and probes (include/gq_bench.h)
 BENCH_EXPORTS = ("gq_bf16_gemv", "gq_stream_read", "gq_probe_mfma_valu", "gq_probe_lds_read")
 
@@ -59,6 +65,57 @@ class GqKv4AttentionArgs(ctypes.Structure):
                 ("max_kv_len", ctypes.c_int64), ("causal", ctypes.c_int32),
                 ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("out", ctypes.c_void_p),
                 ("lse", ctypes.c_void_p)]
+
+
+class GqRopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("original_length", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class GqRopeArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_token_stride", ctypes.c_int64),
+                ("out_head_stride", ctypes.c_int64), ("dtype", ctypes.c_int), ("tokens", ctypes.c_int64),
+                ("heads", ctypes.c_int64), ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("positions", ctypes.c_void_p), ("freqs", ctypes.c_void_p), ("amplitude", ctypes.c_float),
+                ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32)]
+
+
+class GqKv8Layout(ctypes.Structure):
+    _fields_ = [("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class GqKv8AppendArgs(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v", ctypes.c_void_p), ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("tokens", ctypes.c_int64), ("cache", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("layout", GqKv8Layout), ("page_table", ctypes.c_void_p),
+                ("batch", ctypes.c_int64), ("table_pages", ctypes.c_int64), ("kv_lens", ctypes.c_void_p),
+                ("starts", ctypes.c_void_p), ("bounds", ctypes.c_void_p)]
+
+
+class GqKv8AttentionArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("q_tokens", ctypes.c_int64),
+                ("q_heads", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("cache", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("layout", GqKv8Layout),
+                ("page_table", ctypes.c_void_p), ("batch", ctypes.c_int64),
+                ("table_pages", ctypes.c_int64), ("head_tables", ctypes.c_int32), ("kv_lens", ctypes.c_void_p),
+                ("q_starts", ctypes.c_void_p), ("max_q_len", ctypes.c_int64),
+                ("max_kv_len", ctypes.c_int64), ("causal", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p)]
+
+
+class GqKv8SelectArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("q_tokens", ctypes.c_int64),
+                ("q_heads", ctypes.c_int32), ("dtype", ctypes.c_int), ("bounds", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("layout", GqKv8Layout), ("page_table", ctypes.c_void_p),
+                ("batch", ctypes.c_int64), ("table_pages", ctypes.c_int64), ("kv_lens", ctypes.c_void_p),
+                ("q_starts", ctypes.c_void_p), ("max_kv_len", ctypes.c_int64), ("keep", ctypes.c_int32),
+                ("first", ctypes.c_int32), ("last", ctypes.c_int32), ("pages", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p)]
 
 
 class GqError(RuntimeError):
@@ -112,6 +169,16 @@ def lib() -> ctypes.CDLL:
         "gq_kv4_read": [p, i64, GqKv4Layout, p, i64, p, p, c, p],
         "gq_kv4_attention_workspace_size": [ctypes.POINTER(GqKv4AttentionArgs), ctypes.POINTER(sz)],
         "gq_kv4_attention": [ctypes.POINTER(GqKv4AttentionArgs), p, sz, p],
+        "gq_rope_frequencies": [i64, ctypes.c_double, GqRopeScaling, ctypes.POINTER(ctypes.c_double),
+                                ctypes.POINTER(ctypes.c_double)],
+        "gq_rope": [ctypes.POINTER(GqRopeArgs), p],
+        "gq_kv8_cache_bytes": [i64, GqKv8Layout, ctypes.POINTER(sz)],
+        "gq_kv8_append": [ctypes.POINTER(GqKv8AppendArgs), p],
+        "gq_kv8_read": [p, i64, GqKv8Layout, p, i64, p, p, c, p],
+        "gq_kv8_attention_workspace_size": [ctypes.POINTER(GqKv8AttentionArgs), ctypes.POINTER(sz)],
+        "gq_kv8_attention": [ctypes.POINTER(GqKv8AttentionArgs), p, sz, p],
+        "gq_kv8_select_workspace_size": [ctypes.POINTER(GqKv8SelectArgs), ctypes.POINTER(sz)],
+        "gq_kv8_select": [ctypes.POINTER(GqKv8SelectArgs), p, sz, p],
         "gq_stream_read": [p, i64, p, p],
         "gq_probe_mfma_valu": [i32, i32, i32, p, p, p],
         "gq_probe_lds_read": [i32, i32, i32, p, p, p],
@@ -751,3 +818,346 @@ def gq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
     _ok(L.gq_kv4_attention(ref, _ptr(workspace), 0 if workspace is None else workspace.numel(),
                            _stream(stream)), "gq_kv4_attention")
     return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions (include/gq_rope.h) and the 8-bit key/value cache (gq_kv8.h)
+# ---------------------------------------------------------------------------
+
+# Calls whose tensors lie on another device than the current one run there; a stream
+# has to be one of that device.
+
+def _enter(dev, stream):
+    """The device to switch to for a call on `dev`, or None where it is the current one."""
+    sdev = getattr(stream, "device_index", None)
+    if sdev is not None and sdev != dev.index:
+        raise ValueError(f"the stream is on cuda:{sdev}, the tensors on {dev}")
+    return None if dev.index == torch.cuda.current_device() else dev
+
+
+def _on_stream(stream, dev, make):
+    """Memory made by `make` for work on `stream` (default: dev's current one)."""
+    if stream is None or not hasattr(stream, "cuda_stream"):
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _scratch(need: int, workspace, dev, stream):
+    """The caller's workspace, or one allocated on the call's stream."""
+    if workspace is not None:
+        if workspace.numel() < need:
+            raise ValueError(f"workspace has {workspace.numel()} bytes, the call needs {need}")
+        return workspace
+    if need == 0:
+        return None
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        raise ValueError("with a raw stream handle the caller passes the workspace "
+                         f"({need} bytes) that the call needs")
+    return _on_stream(stream, dev, lambda: torch.empty(need, dtype=torch.uint8, device=dev))
+
+
+_ROPE_KINDS = {"none": 0, "linear": 1, "wavelength": 2, "yarn": 3}
+
+
+def gq_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                        original_length: float = 0.0, low: float = 1.0, high: float = 4.0, device="cuda"):
+    """(freqs float64 [rot_dim / 2] on `device`, amplitude): the angles per position of the
+    pairs and the factor of the result.  scaling "none", "linear" (by factor), "wavelength" or
+    "yarn" (by factor, mixed between `low` and `high` turns over original_length)."""
+    if scaling not in _ROPE_KINDS:
+        raise ValueError(f"scaling {scaling!r} not in {tuple(_ROPE_KINDS)}")
+    if rot_dim < 2 or rot_dim > 1024 or rot_dim % 2:
+        raise ValueError(f"rot_dim {rot_dim} must be even, 2..1024")
+    f, m = (ctypes.c_double * (rot_dim // 2))(), ctypes.c_double()
+    s = GqRopeScaling(_ROPE_KINDS[scaling], float(factor), float(original_length), float(low), float(high))
+    _ok(lib().gq_rope_frequencies(rot_dim, float(base), s, f, ctypes.byref(m)), "gq_rope_frequencies")
+    return torch.tensor(list(f), dtype=torch.float64, device=device), m.value
+
+
+def _heads3(t, name: str, dtypes, shape=None):
+    """A [tokens, heads, dim] tensor with contiguous dim; its two strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"{'(tokens, heads, head_dim)' if shape is None else tuple(shape)}")
+    ts, hs, ds = t.stride()
+    if t.shape[2] > 1 and ds != 1:
+        raise ValueError(f"{name}: strides {t.stride()}; the last must be 1")
+    return (ts if t.shape[0] > 1 else 0), (hs if t.shape[1] > 1 else 0)
+
+
+def gq_rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, interleaved: bool = False,
+            amplitude: float = 1.0, inverse: bool = False, out=None, stream=None):
+    """x [tokens, heads, head_dim] (bf16, fp16 or fp32; a view with contiguous rows is taken
+    as it is) turned by its positions (int64 [tokens]) with freqs (float64 [rot_dim / 2]): pairs
+    (i, i + rot_dim / 2), interleaved (2 i, 2 i + 1).  inverse: by the negative angles, which
+    makes the gradient of x from that of the result.  out may be x."""
+    xts, xhs = _heads3(x, "x", tuple(_DT))
+    T, H, D = x.shape
+    _need(positions, "positions", (torch.int64,), (T,))
+    _need(freqs, "freqs", (torch.float64,))
+    if freqs.dim() != 1:
+        raise ValueError(f"freqs must be [rot_dim / 2], got {tuple(freqs.shape)}")
+    rot = 2 * freqs.shape[0]
+    if rot < 2 or rot > D or D % 2 or D > 1024:
+        raise ValueError(f"rot_dim {rot} must be in 2..head_dim={D}, and head_dim even and at most 1024")
+    if out is not None:
+        ots, ohs = _heads3(out, "out", (x.dtype,), x.shape)
+    _on_device(None, x=x)
+    dev = x.device
+    _on_device(dev, positions=positions, freqs=freqs, out=out)
+    away = _enter(dev, stream)
+    if away is not None:
+        with torch.cuda.device(away):
+            return gq_rope(x, positions, freqs, interleaved, amplitude, inverse, out, stream)
+    if out is None:
+        out = _on_stream(stream, dev, lambda: x.new_empty((T, H, D)))
+        ots, ohs = H * D, D
+    a = GqRopeArgs(x.data_ptr(), xts, xhs, out.data_ptr(), ots, ohs, _DT[x.dtype], T, H, D, rot,
+                   positions.data_ptr(), freqs.data_ptr(), float(amplitude), int(bool(interleaved)),
+                   int(bool(inverse)))
+    _ok(lib().gq_rope(ctypes.byref(a), _stream(stream)), "gq_rope")
+    return out
+
+
+def _kv8_check(head_dim: int, page_size: int) -> None:
+    if head_dim not in _KV_DIMS:
+        raise ValueError(f"head_dim {head_dim} not in {_KV_DIMS}")
+    if page_size < 16 or page_size > 1024 or page_size & (page_size - 1):
+        raise ValueError(f"page_size {page_size} must be a power of two in 16..1024")
+
+
+def gq_kv8_empty(n_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, device="cuda") -> torch.Tensor:
+    """A cache of n_pages pages of page_size tokens in 8 bits: uint8 [n_pages, kv_heads,
+    page_size / 16, bytes of 16 tokens], uninitialised.  The shape carries what the other
+    calls need; the bytes are the library's own (gq_kv8_append and gq_kv8_read are the way
+    in and out)."""
+    _kv8_check(head_dim, page_size)
+    if n_pages < 1 or kv_heads < 1:
+        raise ValueError("n_pages and kv_heads must be positive")
+    return torch.empty((n_pages, kv_heads, page_size // 16, 32 * head_dim + 8), dtype=torch.uint8, device=device)
+
+
+def gq_kv8_bounds_empty(n_pages: int, kv_heads: int, head_dim: int, dtype=torch.bfloat16,
+                        device="cuda") -> torch.Tensor:
+    """Bounds of the keys of n_pages pages, [n_pages, kv_heads, 2 (smallest, largest),
+    head_dim] in the keys' type, uninitialised: gq_kv8_append fills and widens them."""
+    _kv8_check(head_dim, 16)
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"dtype {dtype} not in (torch.bfloat16, torch.float16)")
+    if n_pages < 1 or kv_heads < 1:
+        raise ValueError("n_pages and kv_heads must be positive")
+    return torch.empty((n_pages, kv_heads, 2, head_dim), dtype=dtype, device=device)
+
+
+# layouts of the cache shapes seen so far (checked once each)
+_kv8_layouts = {}
+
+
+def _kv8_cache(cache, head_dim: int) -> GqKv8Layout:
+    """Check a cache against head_dim; its layout."""
+    _need(cache, "cache", (torch.uint8,))
+    key = (cache.shape, head_dim)
+    lay = _kv8_layouts.get(key)
+    if lay is None:
+        _kv8_check(head_dim, 16)
+        if cache.dim() != 4 or cache.shape[3] != 32 * head_dim + 8:
+            raise ValueError(f"cache has shape {tuple(cache.shape)}, expected (n_pages, kv_heads, "
+                             f"page_size / 16, {32 * head_dim + 8}) for head_dim {head_dim}")
+        lay = _kv8_layouts[key] = GqKv8Layout(cache.shape[1], head_dim, cache.shape[2] * 16)
+    return lay
+
+
+def _kv8_bounds(bounds, dtype, n_pages=None, heads=None, dim=None) -> None:
+    _need(bounds, "bounds", (dtype,))
+    want = (n_pages, heads, 2, dim)
+    if bounds.dim() != 4 or any(w is not None and w != g for w, g in zip(want, bounds.shape)):
+        raise ValueError(f"bounds has shape {tuple(bounds.shape)}, expected {want}")
+
+
+def _lengths(page_table, kv_lens, starts, name: str, dims):
+    """Check a page table, lengths and row starts; the batch."""
+    _need(page_table, "page_table", (torch.int32,))
+    if page_table.dim() not in dims:
+        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [batch, pages]"
+                         + (" or [batch, kv_heads, pages]" if 3 in dims else ""))
+    nb = page_table.shape[0]
+    _need(kv_lens, "kv_lens", (torch.int32,), (nb,))
+    if starts is not None:
+        _need(starts, name, (torch.int32,), (nb + 1,))
+    return nb
+
+
+def gq_kv8_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
+                  kv_lens: torch.Tensor, starts: Optional[torch.Tensor] = None,
+                  bounds: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantise the next tokens of sequences, k and v [tokens, kv_heads, head_dim] (bf16 or
+    fp16; views with contiguous rows are taken as they are), into the cache.  Sequence b brings
+    the rows starts[b] .. starts[b + 1] - 1 (row b alone where starts is None); kv_lens[b] is its
+    length with them, its row of page_table [batch, pages] says where they go (all int32, on
+    the GPU).  bounds (gq_kv8_bounds_empty), where given, are kept up to date."""
+    kts, khs = _rows16(k, "k", (torch.bfloat16, torch.float16))
+    T, H, D = k.shape
+    vts, vhs = _rows16(v, "v", (k.dtype,), H, D)
+    if v.shape[0] != T:
+        raise ValueError(f"v has {v.shape[0]} tokens, k has {T}")
+    lay = _kv8_cache(cache, D)
+    if lay.kv_heads != H:
+        raise ValueError(f"cache has {lay.kv_heads} heads, k has {H}")
+    nb = _lengths(page_table, kv_lens, starts, "starts", (2,))
+    if starts is None and T != nb:
+        raise ValueError(f"k has {T} tokens for {nb} sequences; other than one each needs starts")
+    if bounds is not None:
+        _kv8_bounds(bounds, k.dtype, cache.shape[0], H, D)
+    _on_device(None, k=k)
+    dev = k.device
+    _on_device(dev, v=v, cache=cache, page_table=page_table, kv_lens=kv_lens, starts=starts, bounds=bounds)
+    away = _enter(dev, stream)
+    if away is not None:
+        with torch.cuda.device(away):
+            return gq_kv8_append(k, v, cache, page_table, kv_lens, starts, bounds, stream)
+    a = GqKv8AppendArgs(k.data_ptr(), kts, khs, v.data_ptr(), vts, vhs, _DT[k.dtype], T, cache.data_ptr(),
+                        cache.shape[0], lay, page_table.data_ptr(), nb, page_table.shape[1], kv_lens.data_ptr(),
+                        _ptr(starts), _ptr(bounds))
+    _ok(lib().gq_kv8_append(ctypes.byref(a), _stream(stream)), "gq_kv8_append")
+
+
+def gq_kv8_read(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, out_dtype=torch.bfloat16, k=None, v=None,
+                stream=None):
+    """(k, v) [tokens, kv_heads, head_dim] in out_dtype: the values that the cache stands for
+    at the given slots (int64; page * page_size + place, out of range: zeros)."""
+    lay = _kv8_cache(cache, head_dim)
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be a 1-D tensor")
+    _slots(slots, slots.shape[0])
+    shape = (slots.shape[0], lay.kv_heads, head_dim)
+    if out_dtype not in _DT:
+        raise TypeError(f"out_dtype {out_dtype} not in {tuple(_DT)}")
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _need(t, name, (out_dtype,), shape)
+    _on_device(None, cache=cache)
+    dev = cache.device
+    _on_device(dev, slots=slots, k=k, v=v)
+    away = _enter(dev, stream)
+    if away is not None:
+        with torch.cuda.device(away):
+            return gq_kv8_read(cache, slots, head_dim, out_dtype, k, v, stream)
+    make = lambda: torch.empty(shape, dtype=out_dtype, device=dev)
+    k = _on_stream(stream, dev, make) if k is None else k
+    v = _on_stream(stream, dev, make) if v is None else v
+    _ok(lib().gq_kv8_read(cache.data_ptr(), cache.shape[0], lay, slots.data_ptr(), slots.shape[0], k.data_ptr(),
+                          v.data_ptr(), _DT[out_dtype], _stream(stream)), "gq_kv8_read")
+    return k, v
+
+
+def gq_kv8_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                     q_starts: Optional[torch.Tensor] = None, max_q_len: Optional[int] = None,
+                     max_kv_len: Optional[int] = None, causal: bool = True, window: int = 0,
+                     scale: Optional[float] = None, return_lse: bool = False, out=None, lse=None,
+                     stream=None, workspace=None):
+    """Attention of q [tokens, q_heads, head_dim] (bf16 or fp16) over the 8-bit cache, as
+    gq_kv4_attention over the 4-bit one.  page_table [batch, pages], or [batch, kv_heads,
+    pages] with pages of each key/value head's own: what gq_kv8_select returns, together
+    with its lengths, makes the attention over the pages it chose."""
+    qts, qhs = _rows16(q, "q", (torch.bfloat16, torch.float16))
+    T, HQ, D = q.shape
+    lay = _kv8_cache(cache, D)
+    if HQ % lay.kv_heads:
+        raise ValueError(f"{HQ} query heads are not a multiple of {lay.kv_heads} key/value heads")
+    nb = _lengths(page_table, kv_lens, q_starts, "q_starts", (2, 3))
+    heads = page_table.dim() == 3
+    if heads and page_table.shape[1] != lay.kv_heads:
+        raise ValueError(f"page_table has {page_table.shape[1]} heads, the cache {lay.kv_heads}")
+    if q_starts is None and T != nb:
+        raise ValueError(f"q has {T} tokens for {nb} sequences; more than one each needs q_starts")
+    if out is not None:
+        _need(out, "out", (q.dtype,), (T, HQ, D))
+    if lse is not None:
+        _need(lse, "lse", (torch.float32,), (T, HQ))
+    if workspace is not None:
+        _need(workspace, "workspace", (torch.uint8,))
+    table_pages = page_table.shape[-1]
+    if max_q_len is None:
+        max_q_len = 1 if q_starts is None else T
+    if max_kv_len is None:
+        max_kv_len = table_pages * lay.page_size
+    _on_device(None, q=q)
+    dev = q.device
+    _on_device(dev, cache=cache, page_table=page_table, kv_lens=kv_lens, q_starts=q_starts, out=out, lse=lse,
+               workspace=workspace)
+    away = _enter(dev, stream)
+    if away is not None:
+        with torch.cuda.device(away):
+            return gq_kv8_attention(q, cache, page_table, kv_lens, q_starts, max_q_len, max_kv_len, causal, window,
+                                    scale, return_lse, out, lse, stream, workspace)
+    if out is None:
+        out = _on_stream(stream, dev, lambda: q.new_empty((T, HQ, D)))
+    if lse is None and return_lse:
+        lse = _on_stream(stream, dev, lambda: torch.empty((T, HQ), dtype=torch.float32, device=dev))
+    a = GqKv8AttentionArgs(
+        q.data_ptr(), qts, qhs, T, HQ, _DT[q.dtype], cache.data_ptr(), cache.shape[0], lay,
+        page_table.data_ptr(), nb, table_pages, int(heads), kv_lens.data_ptr(), _ptr(q_starts), int(max_q_len),
+        int(max_kv_len), int(bool(causal)), int(window), D ** -0.5 if scale is None else float(scale),
+        out.data_ptr(), _ptr(lse))
+    ref, size, L = ctypes.byref(a), ctypes.c_size_t(), lib()
+    _ok(L.gq_kv8_attention_workspace_size(ref, ctypes.byref(size)), "gq_kv8_attention_workspace_size")
+    ws = _scratch(size.value, workspace, dev, stream)
+    _ok(L.gq_kv8_attention(ref, _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)), "gq_kv8_attention")
+    return (out, lse) if return_lse else out
+
+
+def gq_kv8_select(q: torch.Tensor, bounds: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor, keep: int,
+                  page_size: int = 64, q_starts: Optional[torch.Tensor] = None, max_kv_len: Optional[int] = None,
+                  first: int = 1, last: int = 1, pages=None, lens=None, stream=None, workspace=None):
+    """The `keep` pages that each query of q [tokens, q_heads, head_dim] reads, per
+    key/value head: its first `first` and last `last` ones, and of the others those whose
+    bounds allow the largest score.  Queries stand as in gq_kv8_attention (causal).  Returns
+    (pages int32 [tokens, kv_heads, keep], in the order of their positions and then -1, lens
+    int32 [tokens]): the page_table and kv_lens of a gq_kv8_attention call without q_starts."""
+    qts, qhs = _rows16(q, "q", (torch.bfloat16, torch.float16))
+    T, HQ, D = q.shape
+    _kv8_bounds(bounds, q.dtype, dim=D)
+    _kv8_check(D, page_size)
+    H = bounds.shape[1]
+    if H < 1 or HQ % H:
+        raise ValueError(f"{HQ} query heads are not a multiple of {H} key/value heads")
+    nb = _lengths(page_table, kv_lens, q_starts, "q_starts", (2,))
+    if q_starts is None and T != nb:
+        raise ValueError(f"q has {T} tokens for {nb} sequences; more than one each needs q_starts")
+    if first < 0 or last < 1 or first + last > keep:
+        raise ValueError(f"keep {keep} must be at least first {first} + last {last}, and last at least 1")
+    if pages is not None:
+        _need(pages, "pages", (torch.int32,), (T, H, keep))
+    if lens is not None:
+        _need(lens, "lens", (torch.int32,), (T,))
+    if workspace is not None:
+        _need(workspace, "workspace", (torch.uint8,))
+    if max_kv_len is None:
+        max_kv_len = page_table.shape[1] * page_size
+    _on_device(None, q=q)
+    dev = q.device
+    _on_device(dev, bounds=bounds, page_table=page_table, kv_lens=kv_lens, q_starts=q_starts, pages=pages, lens=lens,
+               workspace=workspace)
+    away = _enter(dev, stream)
+    if away is not None:
+        with torch.cuda.device(away):
+            return gq_kv8_select(q, bounds, page_table, kv_lens, keep, page_size, q_starts, max_kv_len, first, last,
+                                 pages, lens, stream, workspace)
+    if pages is None:
+        pages = _on_stream(stream, dev, lambda: torch.empty((T, H, keep), dtype=torch.int32, device=dev))
+    if lens is None:
+        lens = _on_stream(stream, dev, lambda: torch.empty((T,), dtype=torch.int32, device=dev))
+    a = GqKv8SelectArgs(q.data_ptr(), qts, qhs, T, HQ, _DT[q.dtype], bounds.data_ptr(), bounds.shape[0],
+                        GqKv8Layout(H, D, page_size), page_table.data_ptr(), nb, page_table.shape[1],
+                        kv_lens.data_ptr(), _ptr(q_starts), int(max_kv_len), int(keep), int(first), int(last),
+                        pages.data_ptr(), lens.data_ptr())
+    ref, size, L = ctypes.byref(a), ctypes.c_size_t(), lib()
+    _ok(L.gq_kv8_select_workspace_size(ref, ctypes.byref(size)), "gq_kv8_select_workspace_size")
+    ws = _scratch(size.value, workspace, dev, stream)
+    _ok(L.gq_kv8_select(ref, _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)), "gq_kv8_select")
+    return pages, lens

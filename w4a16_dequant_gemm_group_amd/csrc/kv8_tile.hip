@@ -1,0 +1,307 @@
+// Attention over the 8-bit cache for many query rows (prompts, long chunks): the 4-bit
+// cache's scheme (kv4_tile.h) with its query side, split and join.  A workgroup takes 32
+// rows for each of its waves and walks over the keys 64 at a time; the waves expand the
+// codes of 64 keys and values to fp16 integers into LDS once, then every wave multiplies
+// all 64 with its own rows.  Codes are exact as fp16 and a block's scales are the same for
+// 16 keys, so both products take one part each: the keys' scale is a factor of 16 scores
+// at once, the values' goes into the exponent of the weights.
+#include "kv8.h"
+#include "kv4_tile.h"
+
+namespace gq {
+namespace kv8 {
+
+using namespace kv4;
+
+__device__ __forceinline__ f16x2 pair_lo(uint32_t w) {
+  const f16x2 off = {(_Float16)-1152.0f, (_Float16)-1152.0f};
+  return __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, w, 0x04010400u)) + off;
+}
+__device__ __forceinline__ f16x2 pair_hi(uint32_t w) {
+  const f16x2 off = {(_Float16)-1152.0f, (_Float16)-1152.0f};
+  return __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)) + off;
+}
+__device__ __forceinline__ uint32_t bits(f16x2 v) { return __builtin_bit_cast(uint32_t, v); }
+
+template <int D>
+struct Tile8 : Tile<D, 1, true, false, false> {
+  using Base = Tile<D, 1, true, false, false>;
+  using Base::A;
+  using Base::l;
+  using Base::mref;
+  using Base::o;
+  using Base::q;
+  static constexpr int NS = D / 32, NW = Base::NW, TQ = Base::TQ, KP = Base::KP, VP = Base::VP;
+  static constexpr int kV = kTK * KP;                 // the values, behind the keys
+  static constexpr int kEx = kV + D * VP;             // floats {log2 S_V, 1 / S_V, S_K} of the four blocks
+  static constexpr int kBuf = kEx + 48;
+  static constexpr int kBufs = 2 * kBuf <= 160 * 1024 ? 2 : 1;
+
+  // What a wave holds of the next tile: the codes of 16 keys or 16 values.
+  struct Codes {
+    uint32_t d[2 * NS];
+    float S;
+    bool ok;
+
+    __device__ __forceinline__ void load(const Kv8Attn& a, int64_t page, int h, int u, bool values, uint32_t lane) {
+      ok = page >= 0 && page < a.c.n_pages;
+      const int64_t blk = kv8_block(ok ? page : 0, a.c.hkv, h, a.c.page_shift, ok ? u & ((1 << a.c.page_shift) - 1) : 0);
+      const uint8_t* p = a.c.cache + blk * (32 * D) + (values ? 16 * D : 0);
+#pragma unroll
+      for (int s = 0; s + 1 < NS; s += 2) {
+        const u32x4 w = *(const u32x4*)(p + 512 * s + 16 * lane);
+        d[2 * s] = w.x; d[2 * s + 1] = w.y; d[2 * s + 2] = w.z; d[2 * s + 3] = w.w;
+      }
+      if constexpr (NS % 2) {
+        const uint2 w = *(const uint2*)(p + 512 * (NS - 1) + 8 * lane);
+        d[2 * NS - 2] = w.x; d[2 * NS - 1] = w.y;
+      }
+      const float2 sc = a.scales[blk];
+      S = values ? sc.y : sc.x;
+    }
+  };
+
+  // Keys that no row sees are finite integers all the same, and masked later.
+  static __device__ __forceinline__ void expand_k(const Codes& c, uint8_t* buf, int blk, int m, int kg) {
+    if (m == 0 && kg == 0) ((float*)(buf + kEx))[8 + blk] = c.ok ? c.S : 1.0f;
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+      *(u32x4*)(buf + (blk * 16 + m) * KP + s * 64 + kg * 16) =
+          u32x4{bits(pair_lo(c.d[2 * s])), bits(pair_hi(c.d[2 * s])), bits(pair_lo(c.d[2 * s + 1])), bits(pair_hi(c.d[2 * s + 1]))};
+  }
+  static __device__ __forceinline__ void expand_v(const Codes& c, uint8_t* buf, int blk, int m, int kg) {
+    if (m == 0 && kg == 0) {
+      float* ex = (float*)(buf + kEx);
+      // -inf takes keys that do not exist out of the softmax
+      const float e = c.ok ? __log2f(c.S) : kNegInf;
+      ex[blk] = e;
+      ex[4 + blk] = c.ok ? exp2_hw(-e) : 1.0f;
+    }
+    uint8_t* vb = buf + kV + blk * 32 + (kg & 1) * 16 + (kg >> 1) * 8;
+#pragma unroll
+    for (int t = 0; t < 2 * NS; ++t)
+      *(uint2*)(vb + (32 * (t / 2) + 2 * m + t % 2) * VP) = make_uint2(bits(pair_lo(c.d[t])), bits(pair_hi(c.d[t])));
+  }
+
+  // One tile of 64 keys from position u on, in the written order of kv4_tile.h: operands
+  // are read kAhead products before their use, the exponentials of 16 keys stand beside the
+  // products of the 16 before.
+  __device__ __forceinline__ void attend(const Kv4Attn& a, const Seq& s, int row0, int u, const uint8_t* buf, int n, int hf) {
+    constexpr int kAhead = 4;
+    f16x8 ring[kAhead];
+    f32x16 x[2];
+    __builtin_amdgcn_s_setprio(1);
+    constexpr int kAll = D / 8;
+    auto read = [&](int r) { return *(const f16x8*)(buf + (32 * (r & 1) + n) * KP + (r / 2) * 32 + hf * 16); };
+#pragma unroll
+    for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[tt][i] = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) ring[r] = read(r);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int r = 0; r < kAll; ++r) {
+      x[r & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[r % kAhead], q[r / 2], x[r & 1], 0, 0, 0);
+      if (r + kAhead < kAll) ring[r % kAhead] = read(r + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __builtin_amdgcn_s_setprio(0);
+    const uint8_t* vb = buf + kV;
+    auto read_v = [&](int r) { return *(const f16x8*)(vb + (32 * (r % NS) + n) * VP + (r / NS) * 32 + hf * 16); };
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) ring[r] = read_v(r);
+    const float4 ev = *(const float4*)(buf + kEx), ei = *(const float4*)(buf + kEx + 16), ek = *(const float4*)(buf + kEx + 32);
+    const float evv[4] = {ev.x, ev.y, ev.z, ev.w}, eiv[4] = {ei.x, ei.y, ei.z, ei.w}, ekv[4] = {ek.x, ek.y, ek.z, ek.w};
+    const float least = fminf(fminf(ev.x, ev.y), fminf(ev.z, ev.w));
+    // whether every row of the wave sees all 64 keys
+    const int rows = s.n * a.r;
+    const int lastrow = row0 + 32 < rows ? row0 + 31 : rows - 1;
+    bool full = u + kTK <= s.kv;
+    if (a.causal) full = full && u + kTK - 1 <= s.kv - s.n + div_r(a, row0);
+    if (a.window > 0) full = full && u > s.kv - s.n + div_r(a, lastrow) - a.window;
+    // and all of them exist: a query that is not finite makes NaN of what stands there
+    full = full && __builtin_amdgcn_readfirstlane(__float_as_uint(least)) != __float_as_uint(kNegInf);
+    if (!full) {
+      const int pos = s.kv - s.n + div_r(a, row0 + n);
+      const int last = a.causal && pos < s.kv - 1 ? pos : s.kv - 1;
+      const int first = a.window > 0 ? pos - a.window + 1 : 0;
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int j = u + 32 * tt + 8 * (i / 4) + 4 * hf + (i & 3);
+          x[tt][i] = j <= last && j >= first && evv[2 * tt + i / 8] != kNegInf ? x[tt][i] : kNegInf;
+        }
+    }
+    // never 0, which would make NaN of a hidden key's -inf
+    float Ab[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) Ab[b] = fmaxf(A * ekv[b], 0x1p-120f);
+    float top = kNegInf;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      float t = x[b >> 1][8 * (b & 1)];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) t = fmaxf(t, x[b >> 1][8 * (b & 1) + i]);
+      top = fmaxf(top, __builtin_fmaf(t, Ab[b], evv[b]));
+    }
+    top -= kTileRoom;
+    if (__any(top > mref + kTileSlack)) {
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float mn = fmaxf(top, mref);
+      const float f = mn == mref ? 1.0f : exp2_hw(mref - mn);
+      mref = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < NS; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= f;
+    }
+    const float base = mref == kNegInf ? 0.0f : mref;
+    f16x8 pw[2];
+    float sum[2];
+    auto weigh = [&](int b, int from, int to) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i >= from && i < to) {
+          const float e = exp2_hw(__builtin_fmaf(x[b >> 1][8 * (b & 1) + i], Ab[b], evv[b] - base));
+          sum[b & 1] = i == 0 ? e : sum[b & 1] + e;
+          pw[b & 1][i] = (_Float16)e;
+          if (i == 7) l = __builtin_fmaf(sum[b & 1], eiv[b], l);
+        }
+    };
+    weigh(0, 0, 8);
+    __builtin_amdgcn_s_setprio(1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int d = 0; d < NS; ++d) {
+        const int r = b * NS + d;
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[r % kAhead], pw[b & 1], o[d], 0, 0, 0);
+        if (r + kAhead < 4 * NS) ring[r % kAhead] = read_v(r + kAhead);
+        if (b < 3) weigh(b + 1, 8 * d / NS, 8 * (d + 1) / NS);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    __builtin_amdgcn_s_setprio(0);
+  }
+};
+
+template <int D>
+__global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv8_tile_kernel(Kv8Attn a) {
+  using T = Tile8<D>;
+  constexpr bool kBoth = T::NW == 4;   // a wave expands keys and values of its block; else one of them
+  __shared__ __attribute__((aligned(16))) uint8_t smem[T::kBufs * T::kBuf];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = lane & 15, kg = lane >> 4, n = lane & 31, hf = lane >> 5;
+  const int blk = wave & 3;            // the 16 keys of a tile that this wave expands
+  const bool is_k = wave < 4;
+  const int ps = a.c.page_shift;
+  T st;
+  const Share sh = find_share<T::TQ>(a, lane);
+  uint32_t at = sh.at;
+  int last = -1;
+  Cursor cur = sh.cur;
+  Seq s{0, 0, 0};
+  if (at < sh.end) {
+    s = wave_seq(a, cur.b);
+    for (;;) {
+      const Span sp = get_span<T::TQ>(a, s, cur.qt);
+      const int j0 = cur.off, left = (int)(sh.end - at);
+      const int j1 = sp.cnt - j0 < left ? sp.cnt : j0 + left;
+      const bool starts = j0 == 0, ends = j1 == sp.cnt;
+      const int row0 = cur.qt * T::TQ + wave * 32;
+      // the run's keys, 64 at a time
+      const int64_t cut = tile_start(a, sp, j1);
+      const int stop = cut < sp.hi ? (int)cut : sp.hi;
+      int u0 = (int)tile_start(a, sp, j0);
+      if (u0 < sp.lo) u0 = sp.lo & ~(kTK - 1);
+      const PageRow table = (PageRow)(a.table + cur.b * a.table_b + cur.h * a.table_h);
+      // page of this wave's 16 of the 64 keys from u on, -1 where no row sees them
+      auto page_of = [&](int u) -> int64_t {
+        const int pos = u + blk * 16;
+        return pos < stop && pos + 16 > sp.lo ? table[pos >> ps] : -1;
+      };
+      typename T::Codes ck, cv;   // a wave that expands one of them uses ck for it
+      auto fetch = [&](int64_t page, int u) {
+        u += blk * 16;
+        ck.load(a, page, cur.h, u, !kBoth && !is_k, lane);
+        if constexpr (kBoth) cv.load(a, page, cur.h, u, true, lane);
+      };
+      auto expand = [&](uint8_t* buf) {
+        if constexpr (kBoth) {
+          T::expand_k(ck, buf, blk, m, kg);
+          T::expand_v(cv, buf, blk, m, kg);
+        } else if (is_k) {
+          T::expand_k(ck, buf, blk, m, kg);
+        } else {
+          T::expand_v(ck, buf, blk, m, kg);
+        }
+      };
+      fetch(page_of(u0), u0);
+      st.load_q(a, s, cur.h, row0 + n, hf);   // beside the codes
+      expand(smem);
+      fetch(page_of(u0 + kTK), u0 + kTK);
+      int64_t next = page_of(u0 + 2 * kTK);
+      __syncthreads();
+      // Codes are fetched a tile before they are expanded.  The waves of keys
+      // expand before their products and those of values after: of the two
+      // waves of a SIMD one has vector work while the other multiplies.
+      for (int u = u0, b = 0; u < stop; u += kTK, b ^= T::kBufs - 1) {
+        const bool more = u + kTK < stop;
+        auto refill = [&] {
+          if (!more) return;
+          expand(smem + (b ^ (T::kBufs - 1)) * T::kBuf);
+          fetch(next, u + 2 * kTK);
+          next = page_of(u + 3 * kTK);
+        };
+        if (!kBoth && is_k) refill();
+        if (row0 < s.n * a.r) st.attend(a, s, row0, u, smem + b * T::kBuf, n, hf);
+        if (T::kBufs == 1) __syncthreads();
+        if (kBoth || !is_k) refill();
+        __syncthreads();
+      }
+      float* part = nullptr;
+      if (!(starts && ends)) {
+        part = a.part + ((int64_t)2 * sh.w + (starts ? 1 : 0)) * (T::TQ * (D + 2));
+        if (starts) last = sh.worker_with(at + sp.cnt - 1);
+      }
+      st.finish(a, s, cur.h, cur.qt, wave * 32 + n, part, hf);
+      at += j1 - j0;
+      if (at >= sh.end) break;
+      cur.off = 0;
+      const int nqt = row_tiles(a, s, T::TQ);
+      if (++cur.qt == nqt) {
+        cur.qt = 0;
+        if (++cur.h == a.c.hkv) {
+          cur.h = 0;
+          do { ++cur.b; s = wave_seq(a, cur.b); } while (s.n == 0);
+        }
+      }
+    }
+  }
+  if (threadIdx.x == 0) leave_meta(a, sh, last, cur, s);
+}
+
+template <int D>
+hipError_t launch_tile_d(const Kv8Attn& a, const Kv4Plan& p, hipStream_t s) {
+  using T = Tile8<D>;
+  hipLaunchKernelGGL((kv8_tile_kernel<D>), dim3(a.workers), dim3(T::NW * 64), 0, s, a);
+  if (hipError_t e = hipGetLastError()) return e;
+  return launch_join<D, T::TQ, 1>(a, p.tile_rows, s);
+}
+
+}  // namespace kv8
+
+hipError_t launch_kv8_tile(const Kv8Attn& a, const Kv4Plan& p, hipStream_t s) {
+  switch (a.c.d) {
+    case 64: return kv8::launch_tile_d<64>(a, p, s);
+    case 96: return kv8::launch_tile_d<96>(a, p, s);
+    case 128: return kv8::launch_tile_d<128>(a, p, s);
+    default: return kv8::launch_tile_d<256>(a, p, s);
+  }
+}
+
+}  // namespace gq
