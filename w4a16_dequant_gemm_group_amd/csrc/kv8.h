@@ -11,9 +11,9 @@
 //   keys (row = token, k = channel): steps s of 32 channels in pairs p = s / 2; lane l
 //     has 16 bytes at 1024 p + 16 l, channels 32 s + 8 kg .. of token m for both steps.
 //     A last step without a partner (96 channels): 8 bytes at 1024 p + 8 l.
-//   values (row = channel, k = token): tiles t of 16 channels; row m of tile 2 b + j is
-//     channel 32 b + 2 m + j.  Tiles in fours: lane l has 16 bytes at 1024 (t / 4) + 16 l,
-//     for each tile the tokens 4 kg .. 4 kg + 3 of its row.  Two tiles left (96 channels):
+//   values (row = channel, k = token): T = D / 16 tiles t of 16 channels; row m of tile t is
+//     channel T m + t.  Tiles in fours: lane l has 16 bytes at 1024 (t / 4) + 16 l, for
+//     each tile the tokens 4 kg .. 4 kg + 3 of its row.  Two tiles left (96 channels):
 //     8 bytes at 1024 + 8 l.
 #pragma once
 
@@ -50,7 +50,7 @@ struct Kv8Append {
   const int32_t* kv_lens;
   const int32_t* starts;            // or nullptr: one token per sequence
   uint16_t* bounds;                 // or nullptr
-  int32_t run;                      // tokens that a workgroup looks through
+  int32_t run, page_run;            // tokens that a workgroup looks through, for blocks and for bounds
 };
 
 hipError_t launch_kv8_append(const Kv8Append& a, gq_dtype dt, hipStream_t s);

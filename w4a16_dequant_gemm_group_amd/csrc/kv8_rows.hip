@@ -181,6 +181,80 @@ struct Rows8 : Rows<D, 1, NQ, true> {
     }
   }
 
+  // Joins the four waves' results and writes the rows, as Rows::finish does with the other
+  // order of channels: a lane's 2 D / 8 results of a row are consecutive ones.
+  __device__ __forceinline__ void finish(const Kv4Attn& a, const Seq& s, int h, int qt, float* part, float* smem, int wave,
+                                         int m, int kg) {
+    constexpr int T = 2 * NS, DH = Base::DH, kRow = Base::kSmemRow;
+    const int rows = s.n * a.r;
+    float* so = smem;
+    float* sm = smem + kWaves * 16 * kRow;
+    float* sl = sm + kWaves * 16;
+    if (rest) {
+#pragma unroll
+      for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[0][i][e] += __shfl_xor(o[0][i][e], 8);
+    }
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq) {
+      float lt = l[nq];
+      lt += __shfl_xor(lt, 16);
+      lt += __shfl_xor(lt, 32);
+      for (int half = 0; half < D / DH; ++half) {
+        __syncthreads();
+        if (kg == 0) {
+          sm[wave * 16 + m] = mref[nq];
+          sl[wave * 16 + m] = lt;
+        }
+        // channels 4 T kg .. : i T + t of them is element i of tile t
+        if (4 * T * kg / DH == half) {
+          float4* dst = (float4*)(so + (wave * 16 + m) * kRow + 4 * T * kg % DH);
+#pragma unroll
+          for (int c = 0; c < 4 * T; c += 4)
+            dst[c / 4] = make_float4(o[nq][c % T][c / T], o[nq][(c + 1) % T][(c + 1) / T], o[nq][(c + 2) % T][(c + 2) / T],
+                                     o[nq][(c + 3) % T][(c + 3) / T]);
+        }
+        __syncthreads();
+        constexpr int C = DH / 16;               // columns per thread
+        const int rr = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * C;
+        const int row = qt * TQ + nq * 16 + rr;
+        if (row < rows) {
+          float M = kNegInf;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) M = fmaxf(M, sm[w * 16 + rr]);
+          float L = 0.0f, acc[C];
+#pragma unroll
+          for (int i = 0; i < C; ++i) acc[i] = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) {
+            const float mw = sm[w * 16 + rr];
+            const float f = mw == kNegInf ? 0.0f : exp2_hw(mw - M);
+            L = __builtin_fmaf(f, sl[w * 16 + rr], L);
+#pragma unroll
+            for (int i = 0; i < C; ++i) acc[i] = __builtin_fmaf(f, so[(w * 16 + rr) * kRow + c0 + i], acc[i]);
+          }
+          if (part) {
+            float* po = part + (nq * 16 + rr) * D + half * DH + c0;
+#pragma unroll
+            for (int i = 0; i < C; ++i) po[i] = acc[i];
+            if ((threadIdx.x & 15) == 0 && half == 0) {
+              part[TQ * D + nq * 16 + rr] = M;
+              part[TQ * D + TQ + nq * 16 + rr] = L;
+            }
+          } else {
+            const int64_t orow = out_row(a, s, h, row);
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+            uint16_t* po = a.out + orow * D + half * DH + c0;
+#pragma unroll
+            for (int i = 0; i < C; i += 2) *(uint32_t*)(po + i) = Base::pack_out(a.bf16, acc[i] * inv, acc[i + 1] * inv);
+            if (a.lse && (threadIdx.x & 15) == 0 && half == 0) a.lse[orow] = Base::lse_of(M, L);
+          }
+        }
+      }
+    }
+  }
+
   // Key tiles j0 .. j1 - 1 of the span: as in the 4-bit kernel a wave's units of 32 keys
   // pass through LDS, two at a time, by loads that need no registers.
   __device__ __forceinline__ void keys(const Kv8Attn& a, const Seq& s, const Span& sp, int64_t b, int h, int qt, int j0,

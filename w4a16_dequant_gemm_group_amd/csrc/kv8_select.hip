@@ -28,10 +28,10 @@ struct Query {
 
 __device__ __forceinline__ Query find_query(const Kv8Select& a, int64_t t, int lane) {
   Query q{-1, 0, 0};
-  const RowSeq s = seq_of_row(a.q_starts, a.batch, a.q_tokens, t, lane);
+  const RowSeq s = seq_of_row(a.q_starts, a.kv_lens, a.batch, a.q_tokens, t, lane);
   if (s.b < 0) return q;
   const int64_t cap = a.most << a.page_shift;
-  int64_t kv = a.kv_lens[s.b];
+  int64_t kv = s.kv;
   kv = kv > cap ? cap : kv;
   const int64_t p = kv - s.n + (t - s.first);
   if (p < 0) return q;

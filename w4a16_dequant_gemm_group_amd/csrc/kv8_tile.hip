@@ -31,7 +31,7 @@ struct Tile8 : Tile<D, 1, true, false, false> {
   using Base::mref;
   using Base::o;
   using Base::q;
-  static constexpr int NS = D / 32, NW = Base::NW, TQ = Base::TQ, KP = Base::KP, VP = Base::VP;
+  static constexpr int NS = D / 32, NW = Base::NW, TQ = Base::TQ, KP = Base::KP, VP = kTK * 2;
   static constexpr int kV = kTK * KP;                 // the values, behind the keys
   static constexpr int kEx = kV + D * VP;             // floats {log2 S_V, 1 / S_V, S_K} of the four blocks
   static constexpr int kBuf = kEx + 48;
@@ -61,6 +61,11 @@ struct Tile8 : Tile<D, 1, true, false, false> {
     }
   };
 
+  // Where piece p (8 keys, 16 bytes) of a channel's 64 values lies in its row of 128 bytes:
+  // turned such that 16 rows next to each other, which are read together, and rows 2 NS
+  // apart, which are written together, spread over the banks.
+  static __device__ __forceinline__ int piece(int row, int p) { return ((p ^ (row >> 1) ^ (row >> 4)) & 7) * 16; }
+
   // Keys that no row sees are finite integers all the same, and masked later.
   static __device__ __forceinline__ void expand_k(const Codes& c, uint8_t* buf, int blk, int m, int kg) {
     if (m == 0 && kg == 0) ((float*)(buf + kEx))[8 + blk] = c.ok ? c.S : 1.0f;
@@ -77,10 +82,12 @@ struct Tile8 : Tile<D, 1, true, false, false> {
       ex[blk] = e;
       ex[4 + blk] = c.ok ? exp2_hw(-e) : 1.0f;
     }
-    uint8_t* vb = buf + kV + blk * 32 + (kg & 1) * 16 + (kg >> 1) * 8;
+    uint8_t* vb = buf + kV + (kg >> 1) * 8;
 #pragma unroll
-    for (int t = 0; t < 2 * NS; ++t)
-      *(uint2*)(vb + (32 * (t / 2) + 2 * m + t % 2) * VP) = make_uint2(bits(pair_lo(c.d[t])), bits(pair_hi(c.d[t])));
+    for (int t = 0; t < 2 * NS; ++t) {
+      const int row = 2 * NS * m + t;
+      *(uint2*)(vb + row * VP + piece(row, 2 * blk + (kg & 1))) = make_uint2(bits(pair_lo(c.d[t])), bits(pair_hi(c.d[t])));
+    }
   }
 
   // One tile of 64 keys from position u on, in the written order of kv4_tile.h: operands
@@ -108,7 +115,11 @@ struct Tile8 : Tile<D, 1, true, false, false> {
     }
     __builtin_amdgcn_s_setprio(0);
     const uint8_t* vb = buf + kV;
-    auto read_v = [&](int r) { return *(const f16x8*)(vb + (32 * (r % NS) + n) * VP + (r / NS) * 32 + hf * 16); };
+    // piece(32 d + n, 2 b + hf) by what d and b change of it: an even number
+    const uint8_t* vp[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) vp[i] = vb + n * VP + piece(n, 2 * i + hf);
+    auto read_v = [&](int r) { return *(const f16x8*)(vp[(r / NS ^ r % NS) & 3] + 32 * (r % NS) * VP); };
 #pragma unroll
     for (int r = 0; r < kAhead; ++r) ring[r] = read_v(r);
     const float4 ev = *(const float4*)(buf + kEx), ei = *(const float4*)(buf + kEx + 16), ek = *(const float4*)(buf + kEx + 32);
