@@ -13,7 +13,6 @@ namespace {
 
 constexpr int kThreads = 256, kGroupWaves = kThreads / 64;
 constexpr int kPasses = 4;      // pages that a lane has under way
-constexpr int kLdsKeys = 7168;  // pages whose scores are kept in LDS while they are sorted out
 
 template <bool BF16>
 __device__ __forceinline__ float wide(uint32_t h) {
@@ -41,41 +40,57 @@ __device__ __forceinline__ Query find_query(const Kv8Select& a, int64_t t, int l
   return q;
 }
 
-// Sum over the lanes of a page (D / 8, for 96 channels 16 of which 4 add zeros), in
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (uint32_t)b, CTRL, 0xF, 0xF, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (uint32_t)(b >> 32), CTRL, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Sum over the P lanes of a page (D / 8, for 96 channels 16 of which 4 add zeros), in
 // all of them.
 template <int P>
 __device__ __forceinline__ double page_sum(double v) {
-#pragma unroll
-  for (int d = 1; d < P; d <<= 1) v += __shfl_xor(v, d);
+  v += dpp_f64<0xB1>(v);      // quad_perm [1,0,3,2]
+  v += dpp_f64<0x4E>(v);      // quad_perm [2,3,0,1]
+  v += dpp_f64<0x141>(v);     // row_half_mirror: 8 lanes
+  if constexpr (P > 8) v += dpp_f64<0x140>(v);   // row_mirror: 16 lanes
+  if constexpr (P > 16) v += __shfl_xor(v, 16);
   return v;
 }
 
+// Eight channels of a query row, as they lie and widened.
+template <bool BF16>
+__device__ __forceinline__ void widen8(uint4 v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[2 * k] = wide<BF16>(w[k] & 0xFFFFu);
+    x[2 * k + 1] = wide<BF16>(w[k] >> 16);
+  }
+}
+
+// A wave scores kPasses x R pages: P lanes hold 8 channels each of a page's bounds and
+// of the query heads, which are taken one after another.
 template <int D, bool BF16>
 __global__ __launch_bounds__(kThreads) void kv8_score_kernel(Kv8Select a, int64_t lists, int chunks) {
   constexpr int P = D == 96 ? 16 : D / 8, R = 64 / P;        // lanes of a page, pages of a wave at once
   constexpr int kPages = kGroupWaves * R * kPasses;          // pages of a workgroup
-  extern __shared__ __attribute__((aligned(16))) float sq[];   // [r][D]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane % P, g = lane / P;
+  const bool live = c < D / 8;
   for (int64_t id = blockIdx.x; id < lists * chunks; id += gridDim.x) {
-    const int64_t list = id / chunks, t = list / a.hkv;
-    const int h = (int)(list - t * a.hkv), p0 = (int)(id - list * chunks) * kPages;
+    // the first pages of all lists, then the next ones: workgroups that find no pages (in
+    // lists shorter than the longest) come last, and those that do spread evenly
+    const int64_t chunk = id / lists, list = id - chunk * lists, t = list / a.hkv;
+    const int h = (int)(list - t * a.hkv), p0 = (int)chunk * kPages;
+    // the first head's channels are on their way while the sequence is looked up
+    const uint16_t* q = a.q + t * a.q_ts + (int64_t)h * a.r * a.q_hs + 8 * c;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (live) raw = *(const uint4*)q;
     const Query qu = find_query(a, t, lane);
     // all of few pages are taken, whatever their scores
-    if (qu.n <= a.keep || p0 >= qu.n) continue;
-    const uint16_t* q = a.q + t * a.q_ts + (int64_t)h * a.r * a.q_hs;
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.r * (D / 8); i += kThreads) {
-      const int head = i / (D / 8), at = i - head * (D / 8);
-      const uint4 v = *(const uint4*)(q + head * a.q_hs + 8 * at);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        sq[head * D + 8 * at + 2 * k] = wide<BF16>(w[k] & 0xFFFFu);
-        sq[head * D + 8 * at + 2 * k + 1] = wide<BF16>(w[k] >> 16);
-      }
-    }
-    __syncthreads();
+    if (qu.n <= a.keep || p0 + wave * R >= qu.n) continue;
     const int32_t* table = a.table + qu.b * a.table_pages;
     int at[kPasses];
     bool is[kPasses];
@@ -86,7 +101,7 @@ __global__ __launch_bounds__(kThreads) void kv8_score_kernel(Kv8Select a, int64_
       const int64_t page = at[i] < qu.n ? table[at[i]] : -1;
       is[i] = page >= 0 && page < a.n_pages;
       lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
-      if (is[i] && c < D / 8) {
+      if (is[i] && live) {
         const uint16_t* bd = a.bounds + (page * a.hkv + h) * (2 * D) + 8 * c;
         lo[i] = *(const uint4*)bd;
         hi[i] = *(const uint4*)(bd + D);
@@ -95,22 +110,28 @@ __global__ __launch_bounds__(kThreads) void kv8_score_kernel(Kv8Select a, int64_
     double best[kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) best[i] = -__builtin_inf();
-    for (int head = 0; head < a.r; ++head) {
+    for (int head = 0;;) {
       float x[8];
+      widen8<BF16>(raw, x);
+      // where a channel is negative, in pairs: there the smallest counts
+      typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+      uint32_t neg[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = c < D / 8 ? sq[head * D + 8 * c + k] : 0.0f;
+      for (int k = 0; k < 4; ++k) neg[k] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(i16x2, neg[k]) >> 15);
+      if (++head < a.r && live) raw = *(const uint4*)(q + head * a.q_hs);
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
         const uint32_t lw[4] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w}, hw[4] = {hi[i].x, hi[i].y, hi[i].z, hi[i].w};
         double s = 0.0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint32_t w = x[k] > 0.0f ? hw[k / 2] : lw[k / 2];
+          const uint32_t w = (lw[k / 2] & neg[k / 2]) | (hw[k / 2] & ~neg[k / 2]);
           s = __builtin_fma((double)x[k], (double)wide<BF16>(k & 1 ? w >> 16 : w & 0xFFFFu), s);
         }
         s = page_sum<P>(s);
-        best[i] = s > best[i] ? s : best[i];
+        best[i] = fmax(best[i], s);   // of a sum that is NaN the other
       }
+      if (head >= a.r) break;
     }
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
@@ -124,39 +145,51 @@ __device__ __forceinline__ uint64_t key_of(double s) {
   return b >> 63 ? ~b : b | 1ull << 63;
 }
 
-// Exclusive sum over the workgroup; total: of all.
-__device__ __forceinline__ uint64_t group_scan(uint64_t v, uint64_t* smem, uint64_t& total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint64_t s = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t u = __shfl_up(s, d);
-    if (lane >= d) s += u;
-  }
-  __syncthreads();
-  if (lane == 63) smem[wave] = s;
-  __syncthreads();
-  uint64_t before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kGroupWaves; ++w) {
-    if (w < wave) before += smem[w];
-    total += smem[w];
-  }
-  return before + s - v;
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ uint32_t dpp_or_0(uint32_t v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
 }
+// Sums over the lanes up to this one.
+__device__ __forceinline__ uint32_t wave_sums(uint32_t v) {
+  v += dpp_or_0<0x111>(v);        // row_shr 1, 2, 4, 8
+  v += dpp_or_0<0x112>(v);
+  v += dpp_or_0<0x114>(v);
+  v += dpp_or_0<0x118>(v);
+  v += dpp_or_0<0x142, 0xA>(v);   // row_bcast 15, 31
+  return v + dpp_or_0<0x143, 0xC>(v);
+}
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (uint32_t)v, CTRL, 0xF, 0xF, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (uint32_t)(v >> 32), CTRL, 0xF, 0xF, true);
+  return (uint64_t)hi << 32 | lo;
+}
+__device__ __forceinline__ uint64_t smaller(uint64_t a, uint64_t b) { return a < b ? a : b; }
+// Smallest over the wave, in every lane.
+__device__ __forceinline__ uint64_t wave_min(uint64_t v) {
+  v = smaller(v, dpp_u64<0xB1>(v));
+  v = smaller(v, dpp_u64<0x4E>(v));
+  v = smaller(v, dpp_u64<0x141>(v));
+  v = smaller(v, dpp_u64<0x140>(v));
+  v = smaller(v, __shfl_xor(v, 16));
+  return smaller(v, __shfl_xor(v, 32));
+}
+
+constexpr int kSort = 1024, kSortWaves = kSort / 64;   // threads of a workgroup that chooses
+constexpr int kHeld = 8;                               // scores that a thread keeps in registers
 
 // One workgroup per (query, head).  The score that the last page taken has is found
 // digit by digit, from the range of the scores down: a histogram of 256 steps, then of
 // the step that it falls into, until that step holds as many pages as are still needed,
-// or one score alone, of whose pages the earliest are taken.
-__global__ __launch_bounds__(kThreads) void kv8_choose_kernel(Kv8Select a, int64_t lists) {
-  extern __shared__ __attribute__((aligned(16))) uint64_t keys[];
-  __shared__ uint64_t sums[kGroupWaves];
-  __shared__ uint32_t bins[256];
-  __shared__ uint64_t edge[2];      // smallest and largest key
-  __shared__ uint32_t found[3];     // step, pages above it, pages in it
-  const int tid = threadIdx.x, lane = tid & 63;
+// or one score alone, of whose pages the earliest are taken.  A thread has a run of
+// pages; HELD: their scores stay in registers, else they are read again each time.
+template <bool HELD>
+__global__ __launch_bounds__(kSort) void kv8_choose_kernel(Kv8Select a, int64_t lists) {
+  __shared__ __attribute__((aligned(16))) uint32_t bins[2][256];
+  __shared__ uint64_t edge[2][kSortWaves];          // smallest key, and complement of the largest
+  __shared__ uint32_t sums[2][kSortWaves];
+  __shared__ uint32_t found[3];                     // step, pages above it, pages in it
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int64_t list = blockIdx.x; list < lists; list += gridDim.x) {
     const int64_t t = list / a.hkv;
     const int h = (int)(list - t * a.hkv);
@@ -165,96 +198,112 @@ __global__ __launch_bounds__(kThreads) void kv8_choose_kernel(Kv8Select a, int64
     const int32_t* table = a.table + (qu.b < 0 ? 0 : qu.b) * a.table_pages;
     const int taken = qu.n < a.keep ? qu.n : a.keep;
     if (tid == 0 && h == 0) a.lens[t] = taken > 0 ? ((taken - 1) << a.page_shift) + qu.in : 0;
-    for (int i = taken + tid; i < a.keep; i += kThreads) out[i] = -1;
+    for (int i = taken + tid; i < a.keep; i += kSort) out[i] = -1;
     if (qu.n <= a.keep) {
-      for (int i = tid; i < taken; i += kThreads) out[i] = table[i];
+      for (int i = tid; i < taken; i += kSort) out[i] = table[i];
       continue;
     }
+    for (int i = tid; i < a.first; i += kSort) out[i] = table[i];
+    for (int i = tid; i < a.last; i += kSort) out[a.keep - a.last + i] = table[qu.n - a.last + i];
     const int n = qu.n - a.first - a.last;       // candidates, from page `first` on
     uint32_t need = (uint32_t)(a.keep - a.first - a.last);
+    if (need == 0) continue;
     const double* score = a.scores + list * a.most + a.first;
-    const bool lds = n <= kLdsKeys;
-    auto key = [&](int i) { return lds ? keys[i] : key_of(score[i]); };
-    __syncthreads();
-    if (tid == 0) {
-      edge[0] = ~0ull;
-      edge[1] = 0;
-    }
-    uint64_t least = ~0ull, most = 0;
-    for (int i = tid; i < n; i += kThreads) {
-      const uint64_t k = key_of(score[i]);
-      if (lds) keys[i] = k;
-      least = k < least ? k : least;
-      most = k > most ? k : most;
-    }
+    const int run = (n + kSort - 1) / kSort, i0 = tid * run;
+    const int mine = i0 >= n ? 0 : (i0 + run < n ? run : n - i0);
+    uint64_t held[kHeld];
+    if constexpr (HELD) {
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const uint64_t u = __shfl_xor(least, d), w = __shfl_xor(most, d);
-      least = u < least ? u : least;
-      most = w > most ? w : most;
+      for (int j = 0; j < kHeld; ++j) held[j] = j < mine ? key_of(score[i0 + j]) : 0;
     }
-    __syncthreads();
+    auto each = [&](auto&& f) {
+      if constexpr (HELD) {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+          if (j < mine) f(j, held[j]);
+      } else {
+        for (int j = 0; j < mine; ++j) f(j, key_of(score[i0 + j]));
+      }
+    };
+    uint64_t least = ~0ull, most = ~0ull;        // of the complements
+    each([&](int, uint64_t k) {
+      least = smaller(least, k);
+      most = smaller(most, ~k);
+    });
+    least = wave_min(least);
+    most = wave_min(most);
+    __syncthreads();                             // the list before is done with what is shared
     if (lane == 0) {
-      atomicMin((unsigned long long*)&edge[0], (unsigned long long)least);
-      atomicMax((unsigned long long*)&edge[1], (unsigned long long)most);
+      edge[0][wave] = least;
+      edge[1][wave] = most;
     }
+    if (tid < 256) bins[0][tid] = 0;
     __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      least = smaller(least, edge[0][w]);
+      most = smaller(most, edge[1][w]);
+    }
     // pages with lo <= key <= hi: `need` of them are taken, with more than hi: all
-    uint64_t lo = edge[0], hi = edge[1];
+    uint64_t lo = least, hi = ~most;
     int shift = 64 - __builtin_clzll((hi - lo) | 1) - 8;
     shift = shift < 0 ? 0 : shift;
-    bool all = need == 0;           // none at all: the step is empty
-    if (all) { lo = ~0ull; hi = ~0ull; }
-    while (!all) {
-      bins[tid] = 0;
+    for (int b = 0;; b ^= 1) {
+      each([&](int, uint64_t k) {
+        if (k >= lo && k <= hi) atomicAdd(&bins[b][(uint32_t)((k - lo) >> shift)], 1u);
+      });
       __syncthreads();
-      for (int i = tid; i < n; i += kThreads) {
-        const uint64_t k = key(i);
-        if (k >= lo && k <= hi) atomicAdd(&bins[(uint32_t)((k - lo) >> shift)], 1u);
-      }
-      __syncthreads();
-      const uint32_t mine = bins[255 - tid];
-      uint64_t total;
-      const uint32_t above = (uint32_t)group_scan(mine, sums, total);
-      if (above < need && above + mine >= need) {
-        found[0] = 255 - tid;
-        found[1] = above;
-        found[2] = mine;
+      if (wave == 0) {
+        // lane l: steps 255 - 4 l down to 252 - 4 l
+        const uint4 v = *(const uint4*)&bins[b][252 - 4 * lane];
+        const uint32_t c[4] = {v.w, v.z, v.y, v.x};
+        const uint32_t own = v.x + v.y + v.z + v.w;
+        uint32_t above = wave_sums(own) - own;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (above < need && above + c[i] >= need) {
+            found[0] = 255 - 4 * lane - i;
+            found[1] = above;
+            found[2] = c[i];
+          }
+          above += c[i];
+        }
+      } else if (tid < 320) {
+        bins[b ^ 1][tid - 64] = 0;
       }
       __syncthreads();
       need -= found[1];
       lo += (uint64_t)found[0] << shift;
-      const uint64_t top = lo + (((uint64_t)1 << shift) - 1);
-      hi = top < hi ? top : hi;
-      all = found[2] == need;
-      if (shift == 0) break;
+      hi = smaller(hi, lo + (((uint64_t)1 << shift) - 1));
+      if (found[2] == need || shift == 0) break;
       shift = shift < 8 ? 0 : shift - 8;
     }
-    // a run of candidates per thread: how many above, how many in the step
-    const int run = (n + kThreads - 1) / kThreads, i0 = tid * run, i1 = i0 + run < n ? i0 + run : n;
-    uint64_t mine = 0;
-    const bool none = a.keep == a.first + a.last;
-    if (!none) {
-      for (int i = i0; i < i1; ++i) {
-        const uint64_t k = key(i);
-        mine += (uint64_t)(k > hi) + ((uint64_t)(k >= lo && k <= hi) << 32);
-      }
+    // how many of the thread's pages lie above, how many in the step
+    uint32_t above = 0, step = 0;
+    each([&](int, uint64_t k) {
+      above += k > hi;
+      step += (k >= lo) & (k <= hi);
+    });
+    uint32_t u = wave_sums(above), v = wave_sums(step);
+    if (lane == 63) {
+      sums[0][wave] = u;
+      sums[1][wave] = v;
     }
-    uint64_t total;
-    const uint64_t before = group_scan(mine, sums, total);
-    uint32_t in_step = (uint32_t)(before >> 32);
-    uint32_t at = (uint32_t)before + (in_step < need ? in_step : need);
-    if (!none) {
-      for (int i = i0; i < i1; ++i) {
-        const uint64_t k = key(i);
-        bool take = k > hi;
-        if (k >= lo && k <= hi) take = in_step++ < need;
-        if (take) out[a.first + at++] = table[a.first + i];
-      }
-    }
-    for (int i = tid; i < a.first; i += kThreads) out[i] = table[i];
-    for (int i = tid; i < a.last; i += kThreads) out[a.keep - a.last + i] = table[qu.n - a.last + i];
     __syncthreads();
+    u -= above;
+    v -= step;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w)
+      if (w < wave) {
+        u += sums[0][w];
+        v += sums[1][w];
+      }
+    uint32_t at = a.first + u + (v < need ? v : need);
+    each([&](int j, uint64_t k) {
+      bool take = k > hi;
+      if ((k >= lo) & (k <= hi)) take = v++ < need;
+      if (take) out[at++] = table[a.first + i0 + j];
+    });
   }
 }
 
@@ -265,11 +314,10 @@ hipError_t score_d(const Kv8Select& a, gq_dtype dt, hipStream_t s) {
   const int chunks = (int)((a.most + kPages - 1) / kPages);
   const int64_t n = lists * chunks;
   const dim3 grid((unsigned)(n < (1 << 22) ? n : 1 << 22));
-  const unsigned lds = (unsigned)(a.r * D * sizeof(float));
   if (dt == GQ_BF16)
-    hipLaunchKernelGGL((kv8_score_kernel<D, true>), grid, dim3(kThreads), lds, s, a, lists, chunks);
+    hipLaunchKernelGGL((kv8_score_kernel<D, true>), grid, dim3(kThreads), 0, s, a, lists, chunks);
   else
-    hipLaunchKernelGGL((kv8_score_kernel<D, false>), grid, dim3(kThreads), lds, s, a, lists, chunks);
+    hipLaunchKernelGGL((kv8_score_kernel<D, false>), grid, dim3(kThreads), 0, s, a, lists, chunks);
   return hipGetLastError();
 }
 
@@ -287,8 +335,11 @@ hipError_t launch_kv8_select(const Kv8Select& a, gq_dtype dt, hipStream_t s) {
     if (e) return e;
   }
   const int64_t lists = a.q_tokens * a.hkv;
-  const unsigned lds = a.most > a.keep ? (unsigned)((a.most < kLdsKeys ? a.most : kLdsKeys) * sizeof(uint64_t)) : 0;
-  hipLaunchKernelGGL(kv8_choose_kernel, dim3((unsigned)(lists < (1 << 22) ? lists : 1 << 22)), dim3(kThreads), lds, s, a, lists);
+  const dim3 grid((unsigned)(lists < (1 << 22) ? lists : 1 << 22));
+  if (a.most <= kSort * kHeld)
+    hipLaunchKernelGGL(kv8_choose_kernel<true>, grid, dim3(kSort), 0, s, a, lists);
+  else
+    hipLaunchKernelGGL(kv8_choose_kernel<false>, grid, dim3(kSort), 0, s, a, lists);
   return hipGetLastError();
 }
 
