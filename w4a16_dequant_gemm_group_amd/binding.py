@@ -824,27 +824,51 @@ def gq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
 # Rotary positions (include/gq_rope.h) and the 8-bit key/value cache (gq_kv8.h)
 # ---------------------------------------------------------------------------
 
-# Calls whose tensors lie on another device than the current one run there; a stream
-# has to be one of that device.
+# Small calls cost the host more than the GPU: the checks below look at every attribute
+# once and leave it to _need and _on_device to say what is wrong.  (A rotation of one
+# token 9.2 us with _need throughout, 3.4 of them the launch.)
 
-def _enter(dev, stream):
-    """The device to switch to for a call on `dev`, or None where it is the current one."""
-    sdev = getattr(stream, "device_index", None)
-    if sdev is not None and sdev != dev.index:
-        raise ValueError(f"the stream is on cuda:{sdev}, the tensors on {dev}")
-    return None if dev.index == torch.cuda.current_device() else dev
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _on_stream(stream, dev, make):
-    """Memory made by `make` for work on `stream` (default: dev's current one)."""
+def _is(t, name: str, dtype, shape) -> None:
+    """_need for one dtype and a whole shape."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _need(t, name, (dtype,), shape)
+
+
+def _place(dev: int, stream, names, *tensors):
+    """Check that all tensors (names: theirs, in one string) lie on the GPU `dev` and that
+    the stream is one of its own.  Returns the stream's handle, or None where the call has
+    to be made with `dev` as the current device."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            dev = -1
+    if dev < 0:
+        named = dict(zip(names.split(), tensors))
+        first = next(iter(named))
+        _on_device(None, **{first: named[first]})
+        _on_device(named[first].device, **named)
+    if stream is None:
+        if dev == _current_device():
+            return _raw_stream(dev) if _raw_stream is not None else _stream(None)
+        return None
+    if getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
+    return _stream(stream) if dev == _current_device() else None
+
+
+def _new(like, shape, dtype, stream):
+    """Uninitialised memory on like's device, allocated for work on `stream` (default: the
+    current one)."""
     if stream is None or not hasattr(stream, "cuda_stream"):
-        return make()
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return make()
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _scratch(need: int, workspace, dev, stream):
-    """The caller's workspace, or one allocated on the call's stream."""
+def _scratch(need: int, workspace, like, stream):
+    """The caller's workspace, or one allocated on the call's stream; its pointer and bytes."""
     if workspace is not None:
         if workspace.numel() < need:
             raise ValueError(f"workspace has {workspace.numel()} bytes, the call needs {need}")
@@ -854,7 +878,7 @@ def _scratch(need: int, workspace, dev, stream):
     if stream is not None and not hasattr(stream, "cuda_stream"):
         raise ValueError("with a raw stream handle the caller passes the workspace "
                          f"({need} bytes) that the call needs")
-    return _on_stream(stream, dev, lambda: torch.empty(need, dtype=torch.uint8, device=dev))
+    return _new(like, (need,), torch.uint8, stream)
 
 
 _ROPE_KINDS = {"none": 0, "linear": 1, "wavelength": 2, "yarn": 3}
@@ -880,14 +904,14 @@ def _heads3(t, name: str, dtypes, shape=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
+    strides = t.stride()
+    if len(strides) != 3 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
                          f"{'(tokens, heads, head_dim)' if shape is None else tuple(shape)}")
-    ts, hs, ds = t.stride()
-    if t.shape[2] > 1 and ds != 1:
-        raise ValueError(f"{name}: strides {t.stride()}; the last must be 1")
-    return (ts if t.shape[0] > 1 else 0), (hs if t.shape[1] > 1 else 0)
+    if strides[2] != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: strides {strides}; the last must be 1")
+    return strides[0], strides[1]
 
 
 def gq_rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, interleaved: bool = False,
@@ -896,31 +920,28 @@ def gq_rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, inter
     as it is) turned by its positions (int64 [tokens]) with freqs (float64 [rot_dim / 2]): pairs
     (i, i + rot_dim / 2), interleaved (2 i, 2 i + 1).  inverse: by the negative angles, which
     makes the gradient of x from that of the result.  out may be x."""
-    xts, xhs = _heads3(x, "x", tuple(_DT))
-    T, H, D = x.shape
-    _need(positions, "positions", (torch.int64,), (T,))
-    _need(freqs, "freqs", (torch.float64,))
-    if freqs.dim() != 1:
-        raise ValueError(f"freqs must be [rot_dim / 2], got {tuple(freqs.shape)}")
-    rot = 2 * freqs.shape[0]
+    xts, xhs = _heads3(x, "x", _DT)
+    T, H, D = shape = x.shape
+    _is(positions, "positions", torch.int64, (T,))
+    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+        raise ValueError("freqs must be a [rot_dim / 2] tensor")
+    rot = freqs.shape[0]
+    _is(freqs, "freqs", torch.float64, (rot,))
+    rot *= 2
     if rot < 2 or rot > D or D % 2 or D > 1024:
         raise ValueError(f"rot_dim {rot} must be in 2..head_dim={D}, and head_dim even and at most 1024")
     if out is not None:
-        ots, ohs = _heads3(out, "out", (x.dtype,), x.shape)
-    _on_device(None, x=x)
-    dev = x.device
-    _on_device(dev, positions=positions, freqs=freqs, out=out)
-    away = _enter(dev, stream)
-    if away is not None:
-        with torch.cuda.device(away):
+        ots, ohs = _heads3(out, "out", (x.dtype,), shape)
+    handle = _place(x.get_device(), stream, "x positions freqs out", x, positions, freqs, out)
+    if handle is None:
+        with torch.cuda.device(x.device):
             return gq_rope(x, positions, freqs, interleaved, amplitude, inverse, out, stream)
     if out is None:
-        out = _on_stream(stream, dev, lambda: x.new_empty((T, H, D)))
+        out = _new(x, shape, x.dtype, stream)
         ots, ohs = H * D, D
     a = GqRopeArgs(x.data_ptr(), xts, xhs, out.data_ptr(), ots, ohs, _DT[x.dtype], T, H, D, rot,
-                   positions.data_ptr(), freqs.data_ptr(), float(amplitude), int(bool(interleaved)),
-                   int(bool(inverse)))
-    _ok(lib().gq_rope(ctypes.byref(a), _stream(stream)), "gq_rope")
+                   positions.data_ptr(), freqs.data_ptr(), amplitude, bool(interleaved), bool(inverse))
+    _ok(lib().gq_rope(ctypes.byref(a), handle), "gq_rope")
     return out
 
 
@@ -960,7 +981,8 @@ _kv8_layouts = {}
 
 def _kv8_cache(cache, head_dim: int) -> GqKv8Layout:
     """Check a cache against head_dim; its layout."""
-    _need(cache, "cache", (torch.uint8,))
+    if not isinstance(cache, torch.Tensor) or cache.dtype is not torch.uint8 or not cache.is_contiguous():
+        _need(cache, "cache", (torch.uint8,))
     key = (cache.shape, head_dim)
     lay = _kv8_layouts.get(key)
     if lay is None:
@@ -972,23 +994,16 @@ def _kv8_cache(cache, head_dim: int) -> GqKv8Layout:
     return lay
 
 
-def _kv8_bounds(bounds, dtype, n_pages=None, heads=None, dim=None) -> None:
-    _need(bounds, "bounds", (dtype,))
-    want = (n_pages, heads, 2, dim)
-    if bounds.dim() != 4 or any(w is not None and w != g for w, g in zip(want, bounds.shape)):
-        raise ValueError(f"bounds has shape {tuple(bounds.shape)}, expected {want}")
-
-
 def _lengths(page_table, kv_lens, starts, name: str, dims):
     """Check a page table, lengths and row starts; the batch."""
-    _need(page_table, "page_table", (torch.int32,))
-    if page_table.dim() not in dims:
-        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [batch, pages]"
-                         + (" or [batch, kv_heads, pages]" if 3 in dims else ""))
-    nb = page_table.shape[0]
-    _need(kv_lens, "kv_lens", (torch.int32,), (nb,))
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() not in dims:
+        raise ValueError("page_table must be a tensor [batch, pages]" + (" or [batch, kv_heads, pages]" if 3 in dims else ""))
+    shape = page_table.shape
+    _is(page_table, "page_table", torch.int32, shape)
+    nb = shape[0]
+    _is(kv_lens, "kv_lens", torch.int32, (nb,))
     if starts is not None:
-        _need(starts, name, (torch.int32,), (nb + 1,))
+        _is(starts, name, torch.int32, (nb + 1,))
     return nb
 
 
@@ -1011,19 +1026,18 @@ def gq_kv8_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_ta
     nb = _lengths(page_table, kv_lens, starts, "starts", (2,))
     if starts is None and T != nb:
         raise ValueError(f"k has {T} tokens for {nb} sequences; other than one each needs starts")
+    n_pages = cache.shape[0]
     if bounds is not None:
-        _kv8_bounds(bounds, k.dtype, cache.shape[0], H, D)
-    _on_device(None, k=k)
-    dev = k.device
-    _on_device(dev, v=v, cache=cache, page_table=page_table, kv_lens=kv_lens, starts=starts, bounds=bounds)
-    away = _enter(dev, stream)
-    if away is not None:
-        with torch.cuda.device(away):
+        _is(bounds, "bounds", k.dtype, (n_pages, H, 2, D))
+    handle = _place(k.get_device(), stream, "k v cache page_table kv_lens starts bounds", k, v, cache, page_table,
+                    kv_lens, starts, bounds)
+    if handle is None:
+        with torch.cuda.device(k.device):
             return gq_kv8_append(k, v, cache, page_table, kv_lens, starts, bounds, stream)
     a = GqKv8AppendArgs(k.data_ptr(), kts, khs, v.data_ptr(), vts, vhs, _DT[k.dtype], T, cache.data_ptr(),
-                        cache.shape[0], lay, page_table.data_ptr(), nb, page_table.shape[1], kv_lens.data_ptr(),
+                        n_pages, lay, page_table.data_ptr(), nb, page_table.shape[1], kv_lens.data_ptr(),
                         _ptr(starts), _ptr(bounds))
-    _ok(lib().gq_kv8_append(ctypes.byref(a), _stream(stream)), "gq_kv8_append")
+    _ok(lib().gq_kv8_append(ctypes.byref(a), handle), "gq_kv8_append")
 
 
 def gq_kv8_read(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, out_dtype=torch.bfloat16, k=None, v=None,
@@ -1033,25 +1047,25 @@ def gq_kv8_read(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, out_dty
     lay = _kv8_cache(cache, head_dim)
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a 1-D tensor")
-    _slots(slots, slots.shape[0])
-    shape = (slots.shape[0], lay.kv_heads, head_dim)
+    n = slots.shape[0]
+    _is(slots, "slots", torch.int64, (n,))
+    shape = (n, lay.kv_heads, head_dim)
     if out_dtype not in _DT:
         raise TypeError(f"out_dtype {out_dtype} not in {tuple(_DT)}")
-    for name, t in (("k", k), ("v", v)):
-        if t is not None:
-            _need(t, name, (out_dtype,), shape)
-    _on_device(None, cache=cache)
-    dev = cache.device
-    _on_device(dev, slots=slots, k=k, v=v)
-    away = _enter(dev, stream)
-    if away is not None:
-        with torch.cuda.device(away):
+    if k is not None:
+        _is(k, "k", out_dtype, shape)
+    if v is not None:
+        _is(v, "v", out_dtype, shape)
+    handle = _place(cache.get_device(), stream, "cache slots k v", cache, slots, k, v)
+    if handle is None:
+        with torch.cuda.device(cache.device):
             return gq_kv8_read(cache, slots, head_dim, out_dtype, k, v, stream)
-    make = lambda: torch.empty(shape, dtype=out_dtype, device=dev)
-    k = _on_stream(stream, dev, make) if k is None else k
-    v = _on_stream(stream, dev, make) if v is None else v
-    _ok(lib().gq_kv8_read(cache.data_ptr(), cache.shape[0], lay, slots.data_ptr(), slots.shape[0], k.data_ptr(),
-                          v.data_ptr(), _DT[out_dtype], _stream(stream)), "gq_kv8_read")
+    if k is None:
+        k = _new(cache, shape, out_dtype, stream)
+    if v is None:
+        v = _new(cache, shape, out_dtype, stream)
+    _ok(lib().gq_kv8_read(cache.data_ptr(), cache.shape[0], lay, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
+                          _DT[out_dtype], handle), "gq_kv8_read")
     return k, v
 
 
@@ -1075,10 +1089,11 @@ def gq_kv8_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
         raise ValueError(f"page_table has {page_table.shape[1]} heads, the cache {lay.kv_heads}")
     if q_starts is None and T != nb:
         raise ValueError(f"q has {T} tokens for {nb} sequences; more than one each needs q_starts")
+    shape = (T, HQ, D)
     if out is not None:
-        _need(out, "out", (q.dtype,), (T, HQ, D))
+        _is(out, "out", q.dtype, shape)
     if lse is not None:
-        _need(lse, "lse", (torch.float32,), (T, HQ))
+        _is(lse, "lse", torch.float32, (T, HQ))
     if workspace is not None:
         _need(workspace, "workspace", (torch.uint8,))
     table_pages = page_table.shape[-1]
@@ -1086,28 +1101,24 @@ def gq_kv8_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
         max_q_len = 1 if q_starts is None else T
     if max_kv_len is None:
         max_kv_len = table_pages * lay.page_size
-    _on_device(None, q=q)
-    dev = q.device
-    _on_device(dev, cache=cache, page_table=page_table, kv_lens=kv_lens, q_starts=q_starts, out=out, lse=lse,
-               workspace=workspace)
-    away = _enter(dev, stream)
-    if away is not None:
-        with torch.cuda.device(away):
+    handle = _place(q.get_device(), stream, "q cache page_table kv_lens q_starts out lse workspace", q, cache, page_table,
+                    kv_lens, q_starts, out, lse, workspace)
+    if handle is None:
+        with torch.cuda.device(q.device):
             return gq_kv8_attention(q, cache, page_table, kv_lens, q_starts, max_q_len, max_kv_len, causal, window,
                                     scale, return_lse, out, lse, stream, workspace)
     if out is None:
-        out = _on_stream(stream, dev, lambda: q.new_empty((T, HQ, D)))
+        out = _new(q, shape, q.dtype, stream)
     if lse is None and return_lse:
-        lse = _on_stream(stream, dev, lambda: torch.empty((T, HQ), dtype=torch.float32, device=dev))
+        lse = _new(q, (T, HQ), torch.float32, stream)
     a = GqKv8AttentionArgs(
         q.data_ptr(), qts, qhs, T, HQ, _DT[q.dtype], cache.data_ptr(), cache.shape[0], lay,
-        page_table.data_ptr(), nb, table_pages, int(heads), kv_lens.data_ptr(), _ptr(q_starts), int(max_q_len),
-        int(max_kv_len), int(bool(causal)), int(window), D ** -0.5 if scale is None else float(scale),
-        out.data_ptr(), _ptr(lse))
+        page_table.data_ptr(), nb, table_pages, heads, kv_lens.data_ptr(), _ptr(q_starts), max_q_len,
+        max_kv_len, bool(causal), window, D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse))
     ref, size, L = ctypes.byref(a), ctypes.c_size_t(), lib()
     _ok(L.gq_kv8_attention_workspace_size(ref, ctypes.byref(size)), "gq_kv8_attention_workspace_size")
-    ws = _scratch(size.value, workspace, dev, stream)
-    _ok(L.gq_kv8_attention(ref, _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)), "gq_kv8_attention")
+    ws = _scratch(size.value, workspace, q, stream)
+    _ok(L.gq_kv8_attention(ref, _ptr(ws), 0 if ws is None else ws.numel(), handle), "gq_kv8_attention")
     return (out, lse) if return_lse else out
 
 
@@ -1121,9 +1132,11 @@ def gq_kv8_select(q: torch.Tensor, bounds: torch.Tensor, page_table: torch.Tenso
     int32 [tokens]): the page_table and kv_lens of a gq_kv8_attention call without q_starts."""
     qts, qhs = _rows16(q, "q", (torch.bfloat16, torch.float16))
     T, HQ, D = q.shape
-    _kv8_bounds(bounds, q.dtype, dim=D)
+    if not isinstance(bounds, torch.Tensor) or bounds.dim() != 4:
+        raise ValueError("bounds must be a tensor [n_pages, kv_heads, 2, head_dim]")
+    n_pages, H = bounds.shape[:2]
+    _is(bounds, "bounds", q.dtype, (n_pages, H, 2, D))
     _kv8_check(D, page_size)
-    H = bounds.shape[1]
     if H < 1 or HQ % H:
         raise ValueError(f"{HQ} query heads are not a multiple of {H} key/value heads")
     nb = _lengths(page_table, kv_lens, q_starts, "q_starts", (2,))
@@ -1132,32 +1145,29 @@ def gq_kv8_select(q: torch.Tensor, bounds: torch.Tensor, page_table: torch.Tenso
     if first < 0 or last < 1 or first + last > keep:
         raise ValueError(f"keep {keep} must be at least first {first} + last {last}, and last at least 1")
     if pages is not None:
-        _need(pages, "pages", (torch.int32,), (T, H, keep))
+        _is(pages, "pages", torch.int32, (T, H, keep))
     if lens is not None:
-        _need(lens, "lens", (torch.int32,), (T,))
+        _is(lens, "lens", torch.int32, (T,))
     if workspace is not None:
         _need(workspace, "workspace", (torch.uint8,))
+    table_pages = page_table.shape[1]
     if max_kv_len is None:
-        max_kv_len = page_table.shape[1] * page_size
-    _on_device(None, q=q)
-    dev = q.device
-    _on_device(dev, bounds=bounds, page_table=page_table, kv_lens=kv_lens, q_starts=q_starts, pages=pages, lens=lens,
-               workspace=workspace)
-    away = _enter(dev, stream)
-    if away is not None:
-        with torch.cuda.device(away):
+        max_kv_len = table_pages * page_size
+    handle = _place(q.get_device(), stream, "q bounds page_table kv_lens q_starts pages lens workspace", q, bounds,
+                    page_table, kv_lens, q_starts, pages, lens, workspace)
+    if handle is None:
+        with torch.cuda.device(q.device):
             return gq_kv8_select(q, bounds, page_table, kv_lens, keep, page_size, q_starts, max_kv_len, first, last,
                                  pages, lens, stream, workspace)
     if pages is None:
-        pages = _on_stream(stream, dev, lambda: torch.empty((T, H, keep), dtype=torch.int32, device=dev))
+        pages = _new(q, (T, H, keep), torch.int32, stream)
     if lens is None:
-        lens = _on_stream(stream, dev, lambda: torch.empty((T,), dtype=torch.int32, device=dev))
-    a = GqKv8SelectArgs(q.data_ptr(), qts, qhs, T, HQ, _DT[q.dtype], bounds.data_ptr(), bounds.shape[0],
-                        GqKv8Layout(H, D, page_size), page_table.data_ptr(), nb, page_table.shape[1],
-                        kv_lens.data_ptr(), _ptr(q_starts), int(max_kv_len), int(keep), int(first), int(last),
-                        pages.data_ptr(), lens.data_ptr())
+        lens = _new(q, (T,), torch.int32, stream)
+    a = GqKv8SelectArgs(q.data_ptr(), qts, qhs, T, HQ, _DT[q.dtype], bounds.data_ptr(), n_pages,
+                        GqKv8Layout(H, D, page_size), page_table.data_ptr(), nb, table_pages, kv_lens.data_ptr(),
+                        _ptr(q_starts), max_kv_len, keep, first, last, pages.data_ptr(), lens.data_ptr())
     ref, size, L = ctypes.byref(a), ctypes.c_size_t(), lib()
     _ok(L.gq_kv8_select_workspace_size(ref, ctypes.byref(size)), "gq_kv8_select_workspace_size")
-    ws = _scratch(size.value, workspace, dev, stream)
-    _ok(L.gq_kv8_select(ref, _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)), "gq_kv8_select")
+    ws = _scratch(size.value, workspace, q, stream)
+    _ok(L.gq_kv8_select(ref, _ptr(ws), 0 if ws is None else ws.numel(), handle), "gq_kv8_select")
     return pages, lens
