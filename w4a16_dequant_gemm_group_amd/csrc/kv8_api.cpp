@@ -127,7 +127,15 @@ Kv4Plan kv8_plan(const gq_kv8_attention_args& a) {
   constexpr int64_t kMany = (int64_t)1 << 24;
   const int64_t segs = std::min(kMany, std::min(kMany, a.batch * a.layout.kv_heads) * p.grid_q);
   const int64_t tiles = segs * (kOverhead + ((a.max_kv_len + (1 << p.grain) - 1) >> p.grain));
-  p.split = p.tile || a.max_kv_len > std::min<int64_t>(1024, 512 + 8 * segs) || segs >= kMany;
+  // One workgroup per row tile, without the second kernel, as long as that is faster than
+  // the split, which spreads few row tiles over the card.  Equal lengths, one against split, us:
+  //   8 row tiles of 128 channels, 512 / 768 keys 9.8 : 10.7 / 11.2 : 10.7; 160, 2048 keys 22.5 : 25.7
+  //   4 of 64, 768 / 2048 keys 9.0 : 10.0 / 14.8 : 10.4; 80, 2048 keys 15.2 : 16.3
+  //   8 of 256, 256 / 512 keys 11.9 : 13.9 / 16.1 : 14.2; 128, 1024 / 2048 keys 26.9 : 27.5 / 42 : 37
+  // Of more row tiles it would be faster for longer (512 of 128 channels: 4096 keys), but one
+  // long sequence among short ones runs alone then.
+  const int64_t alone = d == 64 ? 960 + 14 * segs : d == 256 ? 360 + 7 * segs : 600 + 8 * segs;
+  p.split = p.tile || a.max_kv_len > std::min<int64_t>(2048, alone) || segs >= kMany;
   if (p.split) {
     // as many workgroups (a wave on each SIMD) as run at once
     const int64_t want = (int64_t)num_cus() * (p.tile ? 1 : kv8_rows_waves(d, p.nq));

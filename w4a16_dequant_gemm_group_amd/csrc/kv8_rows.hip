@@ -33,7 +33,8 @@ __device__ __forceinline__ void dma4(const void* p, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(p) : "memory", "m0");
 }
 
-template <int D, int NQ>
+// NW waves a workgroup: kWaves, or twice that where a compute unit has one alone.
+template <int D, int NQ, int NW>
 struct Rows8 : Rows<D, 1, NQ, true> {
   using Base = Rows<D, 1, NQ, true>;
   using Base::A;
@@ -46,8 +47,9 @@ struct Rows8 : Rows<D, 1, NQ, true> {
   static constexpr int kSub = 32 * D;                 // bytes of a block's codes
   static constexpr int kUnitLds = 2 * kSub + 64;      // two blocks and their scales, padded
   static constexpr int kLoads = 2 * (kSub / 1024) + 1;   // wave-wide loads of a unit
-  static constexpr int kFloats = 4 * Base::kSmemFloats;
-  static constexpr int kSmem = kWaves * 2 * kUnitLds > kFloats ? kWaves * 2 * kUnitLds : kFloats;
+  static constexpr int kStep = NW * kUnit;            // keys that a workgroup takes at once
+  static constexpr int kFloats = 4 * NW * (16 * Base::kSmemRow + 2 * 16);
+  static constexpr int kSmem = NW * 2 * kUnitLds > kFloats ? NW * 2 * kUnitLds : kFloats;
 
   // x = codes . q of 32 keys, without the row's factor A and the block's scale.
   __device__ __forceinline__ void scores(const uint8_t* blk, uint32_t lane, float (&x)[NQ][2][4]) const {
@@ -181,15 +183,15 @@ struct Rows8 : Rows<D, 1, NQ, true> {
     }
   }
 
-  // Joins the four waves' results and writes the rows, as Rows::finish does with the other
+  // Joins the waves' results and writes the rows, as Rows::finish does with the other
   // order of channels: a lane's 2 D / 8 results of a row are consecutive ones.
   __device__ __forceinline__ void finish(const Kv4Attn& a, const Seq& s, int h, int qt, float* part, float* smem, int wave,
                                          int m, int kg) {
     constexpr int T = 2 * NS, DH = Base::DH, kRow = Base::kSmemRow;
     const int rows = s.n * a.r;
     float* so = smem;
-    float* sm = smem + kWaves * 16 * kRow;
-    float* sl = sm + kWaves * 16;
+    float* sm = smem + NW * 16 * kRow;
+    float* sl = sm + NW * 16;
     if (rest) {
 #pragma unroll
       for (int i = 0; i < T; ++i)
@@ -219,15 +221,15 @@ struct Rows8 : Rows<D, 1, NQ, true> {
         constexpr int C = DH / 16;               // columns per thread
         const int rr = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * C;
         const int row = qt * TQ + nq * 16 + rr;
-        if (row < rows) {
+        if (rr < 16 && row < rows) {
           float M = kNegInf;
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) M = fmaxf(M, sm[w * 16 + rr]);
+          for (int w = 0; w < NW; ++w) M = fmaxf(M, sm[w * 16 + rr]);
           float L = 0.0f, acc[C];
 #pragma unroll
           for (int i = 0; i < C; ++i) acc[i] = 0.0f;
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) {
+          for (int w = 0; w < NW; ++w) {
             const float mw = sm[w * 16 + rr];
             const float f = mw == kNegInf ? 0.0f : exp2_hw(mw - M);
             L = __builtin_fmaf(f, sl[w * 16 + rr], L);
@@ -265,9 +267,9 @@ struct Rows8 : Rows<D, 1, NQ, true> {
     int u = (int)tile_start(a, sp, j0);
     const int64_t cut = tile_start(a, sp, j1);
     const int end = cut < sp.hi ? (int)cut : sp.hi;
-    if (u < sp.lo) u = sp.lo & ~(kTile - 1);
+    if (u < sp.lo) u = sp.lo & ~(kTile - 1);   // only the first tile can hold keys before the span
     u += wave * kUnit;
-    if (u + kUnit <= sp.lo) u += kTile;
+    if (u + kUnit <= sp.lo) u += kStep;
     rest = NQ == 1 && !a.bf16 && s.n * a.r <= 8;
     this->reset();
     if (u >= end) return;
@@ -304,13 +306,13 @@ struct Rows8 : Rows<D, 1, NQ, true> {
       return ok;
     };
     const Pages first = pages(u);
-    Pages next = pages(u + kTile);
+    Pages next = pages(u + kStep);
     int ok = fetch(first, u, 0), oknext = 0;
-    if (u + kTile < end) oknext = fetch(next, u + kTile, 1);
+    if (u + kStep < end) oknext = fetch(next, u + kStep, 1);
     this->load_q(a, s, h, qt, m, kg);
     for (int buf = 0;; buf ^= 1) {
-      const int un = u + kTile;
-      next = pages(un + kTile);
+      const int un = u + kStep;
+      next = pages(un + kStep);
       if (un < end)
         wait_dma<kLoads>();
       else
@@ -332,17 +334,17 @@ struct Rows8 : Rows<D, 1, NQ, true> {
       if (un >= end) break;
       u = un;
       ok = oknext;
-      if (un + kTile < end) {
+      if (un + kStep < end) {
         wait_lds();
-        oknext = fetch(next, un + kTile, buf);
+        oknext = fetch(next, un + kStep, buf);
       }
     }
   }
 };
 
-template <int D, int NQ>
-__global__ __launch_bounds__(kWaves * 64, kv8_rows_waves(D, NQ)) void kv8_rows_kernel(Kv8Attn a) {
-  using R = Rows8<D, NQ>;
+template <int D, int NQ, int NW>
+__global__ __launch_bounds__(NW * 64, NW > kWaves ? 2 : kv8_rows_waves(D, NQ)) void kv8_rows_kernel(Kv8Attn a) {
+  using R = Rows8<D, NQ, NW>;
   __shared__ __attribute__((aligned(16))) uint8_t smem[R::kSmem];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -400,10 +402,23 @@ __global__ __launch_bounds__(kWaves * 64, kv8_rows_waves(D, NQ)) void kv8_rows_k
   if (split && threadIdx.x == 0) leave_meta(a, sh, last, cur, s);
 }
 
+// Eight waves where all workgroups run at once with them and their units fit in LDS: of 8
+// sequences' heads 1024 keys 12.7 us, so 14.2, 2048 keys 18.8 : 22.9 (vector instructions of one
+// compute unit); 128 keys 7.2 : 6.7.
+constexpr int64_t kLds = 160 * 1024;
+template <int D, int NQ>
+constexpr bool kWide = Rows8<D, NQ, 2 * kWaves>::kSmem <= kLds && D * NQ <= 128;
+
 template <int D, int NQ>
 hipError_t launch_rows(const Kv8Attn& a, const Kv4Plan& p, hipStream_t s) {
   const int64_t n = p.split ? a.workers : (int64_t)p.grid_q * a.c.hkv * a.batch;
-  hipLaunchKernelGGL((kv8_rows_kernel<D, NQ>), dim3((unsigned)n), dim3(kWaves * 64), 0, s, a);
+  if constexpr (kWide<D, NQ>) {
+    if (!p.split && n * Rows8<D, NQ, 2 * kWaves>::kSmem <= (int64_t)num_cus() * kLds) {
+      hipLaunchKernelGGL((kv8_rows_kernel<D, NQ, 2 * kWaves>), dim3((unsigned)n), dim3(2 * kWaves * 64), 0, s, a);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((kv8_rows_kernel<D, NQ, kWaves>), dim3((unsigned)n), dim3(kWaves * 64), 0, s, a);
   if (hipError_t e = hipGetLastError()) return e;
   return p.split ? launch_join<D, 16 * NQ, 256 / (D / 4)>(a, p.tile_rows, s) : hipSuccess;
 }
