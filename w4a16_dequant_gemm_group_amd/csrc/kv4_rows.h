@@ -110,6 +110,16 @@ __device__ __forceinline__ int64_t tile_start(const Kv4Attn& a, const Span& sp, 
   return (int64_t)(sp.t0 + (j > a.over ? j - a.over : 0)) << a.grain;
 }
 
+// The i-th row tile of n in the order that the split goes through them: as they are,
+// or (TURN) the last, the first, the last but one, ... so that under a causal mask any
+// two next to each other hold about the same number of keys, and runs of equal work end
+// at their borders.
+template <bool TURN>
+__device__ __forceinline__ int tile_at(int i, int n) {
+  if constexpr (!TURN) return i;
+  return i & 1 ? i >> 1 : n - 1 - (i >> 1);
+}
+
 // Where the split stands: sequence, head, row tile, and the key tiles of the
 // row tile that lie before.
 struct Cursor {
@@ -128,13 +138,13 @@ __device__ __forceinline__ uint32_t lane_of(uint32_t v, int lane) { return __bui
 
 // Key tiles of one head over all row tiles of a sequence; lanes share the row
 // tiles.  With `find`: the row tile that holds tile number i.
-template <int TQ>
+template <int TQ, bool TURN>
 __device__ __forceinline__ uint32_t seq_tiles(const Kv4Attn& a, const Seq& s, int lane, bool find, uint32_t i,
                                               Cursor* cur) {
   const int nqt = row_tiles(a, s, TQ);
   uint32_t base = 0;
   for (int q = 0; q < nqt; q += 64) {
-    const uint32_t v = q + lane < nqt ? get_span<TQ>(a, s, q + lane).cnt : 0;
+    const uint32_t v = q + lane < nqt ? get_span<TQ>(a, s, tile_at<TURN>(q + lane, nqt)).cnt : 0;
     const uint32_t sc = wave_scan(v, lane);
     if (find) {
       const uint64_t hit = __ballot(base + sc > i);
@@ -178,7 +188,7 @@ struct Share {
   }
 };
 
-template <int TQ>
+template <int TQ, bool TURN = false>
 __device__ __forceinline__ Share find_share(const Kv4Attn& a, int lane) {
   Share sh{};
   sh.cur = Cursor{0, 0, 0, 0};
@@ -212,7 +222,7 @@ __device__ __forceinline__ Share find_share(const Kv4Attn& a, int lane) {
         const uint32_t i = sh.at - (base + lane_of(sc - v, l)) * heads;
         sh.cur.b = b0 + l;
         sh.cur.h = (int)(i / per);
-        seq_tiles<TQ>(a, wave_seq(a, sh.cur.b), lane, true, i % per, &sh.cur);
+        seq_tiles<TQ, TURN>(a, wave_seq(a, sh.cur.b), lane, true, i % per, &sh.cur);
         return sh;
       }
       base += lane_of(sc, 63);
@@ -222,8 +232,8 @@ __device__ __forceinline__ Share find_share(const Kv4Attn& a, int lane) {
     // one sequence: its lengths are loaded once, and up to 64 row tiles scanned once
     const Seq s = wave_seq(a, 0);
     const int nqt = row_tiles(a, s, TQ);
-    const uint32_t v = lane < nqt ? get_span<TQ>(a, s, lane).cnt : 0, sc = wave_scan(v, lane);
-    const uint32_t per = nqt <= 64 ? lane_of(sc, 63) : seq_tiles<TQ>(a, s, lane, false, 0, nullptr);
+    const uint32_t v = lane < nqt ? get_span<TQ>(a, s, tile_at<TURN>(lane, nqt)).cnt : 0, sc = wave_scan(v, lane);
+    const uint32_t per = nqt <= 64 ? lane_of(sc, 63) : seq_tiles<TQ, TURN>(a, s, lane, false, 0, nullptr);
     sh.total = per * heads;
     sh.cut(a);
     if (sh.at == sh.end) return sh;
@@ -234,22 +244,22 @@ __device__ __forceinline__ Share find_share(const Kv4Attn& a, int lane) {
       sh.cur.qt = l;
       sh.cur.off = (int)(i - lane_of(sc - v, l));
     } else {
-      seq_tiles<TQ>(a, s, lane, true, i, &sh.cur);
+      seq_tiles<TQ, TURN>(a, s, lane, true, i, &sh.cur);
     }
     return sh;
   }
-  for (int b = 0; b < batch; ++b) base += seq_tiles<TQ>(a, wave_seq(a, b), lane, false, 0, nullptr);
+  for (int b = 0; b < batch; ++b) base += seq_tiles<TQ, TURN>(a, wave_seq(a, b), lane, false, 0, nullptr);
   sh.total = base * heads;
   sh.cut(a);
   if (sh.at == sh.end) return sh;
   base = 0;
   for (int b = 0;; ++b) {
     const Seq s = wave_seq(a, b);
-    const uint32_t per = seq_tiles<TQ>(a, s, lane, false, 0, nullptr), i = sh.at - base * heads;
+    const uint32_t per = seq_tiles<TQ, TURN>(a, s, lane, false, 0, nullptr), i = sh.at - base * heads;
     if (i < per * heads) {
       sh.cur.b = b;
       sh.cur.h = (int)(i / per);
-      seq_tiles<TQ>(a, s, lane, true, i % per, &sh.cur);
+      seq_tiles<TQ, TURN>(a, s, lane, true, i % per, &sh.cur);
       return sh;
     }
     base += per;

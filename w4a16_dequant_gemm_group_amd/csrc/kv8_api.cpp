@@ -12,7 +12,10 @@ namespace {
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
-constexpr int kOverhead = 2;   // what a row tile costs besides its keys, in tiles of keys (kv4_api.cpp)
+// What a row tile costs besides its keys, in tiles of keys: a prompt of 4096 at 128 channels
+// with 2 / 3 / 4 / 5 / 6 / 8 213 / 205 / 196 / 191 / 192 / 194 us, at 256 151 / 137 / 137 / 136 / 139 / 142,
+// chunks of 1010 tokens there 57 / 55 / 55 / 59 / 58 / 58.
+constexpr int overhead(int d, bool tile) { return !tile ? 2 : d > 128 ? 3 : 5; }
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 constexpr int64_t kMaxBatch = 1 << 24;
 
@@ -122,11 +125,12 @@ Kv4Plan kv8_plan(const gq_kv8_attention_args& a) {
   const int64_t cap = a.table_pages * a.layout.page_size;
   const int64_t row_tiles = (a.q_tokens * r / tq + std::min(a.batch, a.q_tokens)) * a.layout.kv_heads;
   p.grain = p.tile ? 6 : 7;
-  while (p.grain < 30 && row_tiles * ((cap >> p.grain) + 1 + kOverhead) >= INT32_MAX) ++p.grain;
+  const int over = overhead(d, p.tile);
+  while (p.grain < 30 && row_tiles * ((cap >> p.grain) + 1 + over) >= INT32_MAX) ++p.grain;
   // counted up to 2^24: so many row tiles are split and take all workgroups in any case
   constexpr int64_t kMany = (int64_t)1 << 24;
   const int64_t segs = std::min(kMany, std::min(kMany, a.batch * a.layout.kv_heads) * p.grid_q);
-  const int64_t tiles = segs * (kOverhead + ((a.max_kv_len + (1 << p.grain) - 1) >> p.grain));
+  const int64_t tiles = segs * (over + ((a.max_kv_len + (1 << p.grain) - 1) >> p.grain));
   // One workgroup per row tile, without the second kernel, as long as that is faster than
   // the split, which spreads few row tiles over the card.  Equal lengths, one against split, us:
   //   8 row tiles of 128 channels, 512 / 768 keys 9.8 : 10.7 / 11.2 : 10.7; 160, 2048 keys 22.5 : 25.7
@@ -275,7 +279,7 @@ gq_status gq_kv8_attention(const gq_kv8_attention_args* args, void* workspace,
   k.r_mul = (uint32_t)((((uint64_t)1 << (31 + k.r_shift)) + k.r - 1) / k.r);
   k.workers = p.workers;
   k.grain = p.grain;
-  k.over = kOverhead;
+  k.over = overhead(c.d, p.tile);
   k.few = p.few;
   k.grid_q = p.grid_q;
   k.meta = (int32_t*)workspace;

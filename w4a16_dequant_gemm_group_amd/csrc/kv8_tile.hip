@@ -211,7 +211,7 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv8_til
   const bool is_k = wave < 4;
   const int ps = a.c.page_shift;
   T st;
-  const Share sh = find_share<T::TQ>(a, lane);
+  const Share sh = find_share<T::TQ, true>(a, lane);
   uint32_t at = sh.at;
   int last = -1;
   Cursor cur = sh.cur;
@@ -219,11 +219,12 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv8_til
   if (at < sh.end) {
     s = wave_seq(a, cur.b);
     for (;;) {
-      const Span sp = get_span<T::TQ>(a, s, cur.qt);
+      const int nqt = row_tiles(a, s, T::TQ), qt = tile_at<true>(cur.qt, nqt);   // cur.qt counts in the turned order
+      const Span sp = get_span<T::TQ>(a, s, qt);
       const int j0 = cur.off, left = (int)(sh.end - at);
       const int j1 = sp.cnt - j0 < left ? sp.cnt : j0 + left;
       const bool starts = j0 == 0, ends = j1 == sp.cnt;
-      const int row0 = cur.qt * T::TQ + wave * 32;
+      const int row0 = qt * T::TQ + wave * 32;
       // the run's keys, 64 at a time
       const int64_t cut = tile_start(a, sp, j1);
       const int stop = cut < sp.hi ? (int)cut : sp.hi;
@@ -279,11 +280,13 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv8_til
         part = a.part + ((int64_t)2 * sh.w + (starts ? 1 : 0)) * (T::TQ * (D + 2));
         if (starts) last = sh.worker_with(at + sp.cnt - 1);
       }
-      st.finish(a, s, cur.h, cur.qt, wave * 32 + n, part, hf);
+      st.finish(a, s, cur.h, qt, wave * 32 + n, part, hf);
       at += j1 - j0;
-      if (at >= sh.end) break;
+      if (at >= sh.end) {
+        cur.qt = qt;
+        break;
+      }
       cur.off = 0;
-      const int nqt = row_tiles(a, s, T::TQ);
       if (++cur.qt == nqt) {
         cur.qt = 0;
         if (++cur.h == a.c.hkv) {
