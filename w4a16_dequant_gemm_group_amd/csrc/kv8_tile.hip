@@ -90,6 +90,50 @@ struct Tile8 : Tile<D, 1, true, false, false> {
     }
   }
 
+  // The queries as they lie, and then as fp16 times a power of two per row (as Base::load_q
+  // does in one go): the first codes come in between.
+  __device__ __forceinline__ void fetch_q(const Kv4Attn& a, const Seq& s, int h, int row, int hf) {
+    const bool ok = row < s.n * a.r;
+    const uint16_t* p = a.q;
+    const int tok = div_r(a, row);
+    if (ok) p += (int64_t)(s.q0 + tok) * a.q_ts + (int64_t)(h * a.r + row - tok * a.r) * a.q_hs;
+#pragma unroll
+    for (int st = 0; st < D / 16; ++st) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (ok) v = *(const uint4*)(p + 16 * st + 8 * hf);
+      q[st] = __builtin_bit_cast(f16x8, u32x4{v.x, v.y, v.z, v.w});
+    }
+  }
+  __device__ __forceinline__ void take_q(const Kv4Attn& a) {
+    float mx = 0.0f;
+#pragma unroll
+    for (int st = 0; st < D / 16; ++st) {
+      float x[8];
+      Base::widen(a.bf16, q[st], x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(x[i]));
+    }
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    int e = (int)(__float_as_uint(mx) >> 23) - 127;
+    e = e < -112 ? -112 : (e > 127 ? 127 : e);   // 128: infinite or NaN
+    const float f = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+    A = a.scale_log2 * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+    A = fmaxf(A, 0x1p-100f);   // see Base::load_q
+#pragma unroll
+    for (int st = 0; st < D / 16; ++st) {
+      float x[8];
+      Base::widen(a.bf16, q[st], x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[st][i] = (_Float16)(x[i] * f);
+    }
+    mref = kNegInf;
+    l = 0.0f;
+#pragma unroll
+    for (int d = 0; d < NS; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+  }
+
   // One tile of 64 keys from position u on, in the written order of kv4_tile.h: operands
   // are read kAhead products before their use, the exponentials of 16 keys stand beside the
   // products of the 16 before.
@@ -252,8 +296,10 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv8_til
           T::expand_v(ck, buf, blk, m, kg);
         }
       };
-      fetch(page_of(u0), u0);
-      st.load_q(a, s, cur.h, row0 + n, hf);   // beside the codes
+      const int64_t page = page_of(u0);
+      st.fetch_q(a, s, cur.h, row0 + n, hf);
+      fetch(page, u0);
+      st.take_q(a);
       expand(smem);
       fetch(page_of(u0 + kTK), u0 + kTK);
       int64_t next = page_of(u0 + 2 * kTK);
