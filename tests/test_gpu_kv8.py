@@ -166,6 +166,81 @@ def test_light_weights_beside_a_heavy_one(q_len):
         Case(2, 1, d, 16, dtype, [q_len], [kv], k=k, v=v, q=q).check(causal=False)
 
 
+@pytest.mark.parametrize("q_len", [1, 20])
+@pytest.mark.parametrize("at", [2.0 ** -30, 2.0 ** 100, 2.0 ** 120])
+def test_light_weights_of_large_and_small_values(q_len, at):
+    """Sums of weights far apart stay right where the values' scale is at an end of its range:
+    64 keys 13 nats behind the first, which lies in a block of zeros and weighs nothing else."""
+    kv, d = 1040, 64
+    k = torch.zeros(kv, 1, d)
+    k[:, 0, 0] = -6.5
+    k[0, 0, 0] = 6.5
+    v = torch.full((kv, 1, d), at)
+    v[:16] = 0
+    q = torch.zeros(q_len, 2, d)
+    q[..., 0] = 8.0
+    Case(2, 1, d, 16, "bf16", [q_len], [kv], k=k, v=v, q=q).check(causal=False)
+    v[:16] = at * 2
+    Case(2, 1, d, 16, "bf16", [q_len], [kv], k=k, v=v, q=q).check(causal=False)
+
+
+@pytest.mark.parametrize("q_len", [1, 20])
+def test_keys_of_the_largest_scale_beside_zeros(q_len):
+    """A block whose scale times the query's is beyond fp32 beside keys of zeros: scores 0."""
+    kv, d = 64, 64
+    k = torch.zeros(kv, 1, d)
+    k[16, 0, 1] = 2.0 ** 126                     # a channel in which the queries are 0
+    v = torch.randn(kv, 1, d, generator=torch.Generator().manual_seed(0))
+    q = torch.zeros(q_len, 2, d)
+    q[..., 0] = 2.0 ** 100
+    c = Case(2, 1, d, 16, "bf16", [q_len], [kv], k=k, v=v, q=q)
+    out, lse = c.run(causal=False)
+    mean = U.cached(c.v)[0].mean(0)
+    assert bool(((out.cpu().double() - mean).abs() <= 2.0 ** -8 * mean.abs() + 2.0 ** -10).all())
+    assert bool(((lse.cpu().double() - math.log(kv)).abs() <= 2.0 ** -18).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_many_sequences(dtype):
+    """More sequences than lanes, empty ones among them; with and without the split, single
+    tokens and prompts."""
+    kv = [(i * 37) % 90 for i in range(130)] + [400]
+    Case(4, 2, 64, 16, dtype, [1] * 131, kv, seed=11).check()
+    c = Case(4, 2, 64, 16, dtype, [1] * 131, kv, seed=12)
+    c.check(max_kv_len=1 << 20)
+    q = [min(n, (i * 5) % 23) for i, n in enumerate(kv)]
+    Case(4, 2, 64, 16, dtype, q, kv, seed=13).check()
+    Case(6, 2, 128, 32, dtype, q, kv, seed=14).check(window=30)
+
+
+def test_cache_of_more_than_4_gib():
+    """Pages beyond 2^32 bytes: appended, read back and attended to."""
+    d, page, n_pages = 256, 1024, 8300
+    cache = B.gq_kv8_empty(n_pages, 1, d, page, device=device())
+    assert cache.numel() > 1 << 32
+    table = torch.tensor([[8299, 5], [8200, 8298]], dtype=torch.int32)
+    k, v = draw(1100 + 1500, 1, d, "bf16", 1), draw(2600, 1, d, "bf16", 2)
+    lens = [1100, 1500]
+    dt = table.to(device())
+    B.gq_kv8_append(k.to(device()), v.to(device()), cache, dt, I32(lens), starts_of(lens))
+    slot = torch.tensor([8299 * 1024 + 7, 8298 * 1024 + 475], device=device())
+    got = B.gq_kv8_read(cache, slot, d, torch.float32)[1].cpu()
+    want = [U.cached(v[:1100])[0], U.cached(v[1100:])[0]]
+    assert torch.equal(got, torch.stack((want[0][7], want[1][1499])).float())
+    q = torch.randn(2 + 40, 4, d, generator=torch.Generator().manual_seed(3)).bfloat16()
+    for n in (1, 20):
+        out = B.gq_kv8_attention(q[:2 * n].to(device()), cache, dt, I32(lens), I32([0, n, 2 * n]), n, 1500).cpu().double()
+        at = 0
+        for b, m in enumerate(lens):
+            kk, sk = U.cached(k[at:at + m])
+            vv, sv = U.cached(v[at:at + m])
+            qq = q[b * n:b * n + n].double()
+            o, l, p = attention64(qq, kk, vv, n, m, True, 0, d ** -0.5)
+            tol, _ = U.attention_bounds(qq, kk, vv, sk, sv, o, l, p, d ** -0.5, torch.bfloat16, False)
+            assert bool(((out[b * n:b * n + n] - o).abs() <= tol).all())
+            at += m
+
+
 def test_views_rows_left_alone_and_scale():
     c = Case(8, 2, 128, 16, "bf16", [3, 2], [50, 20], seed=3)
     want, wl = c.run()

@@ -106,6 +106,10 @@ def test_queries_without_pages_and_lengths_out_of_range():
     assert bool((pages[[0, 1, 6, 7]] == -1).all()) and pages[2, 0].tolist() == [int(table[0, 0]), -1, -1]
     pages, lens = B.gq_kv8_select(q[:2].to(device()), bounds, table.to(device()), I32([-3, 10000]), 3, page)
     assert lens.tolist() == [0, 48] and bool((pages[0] == -1).all())      # the table holds 7 pages: 112 of 10000
+    # a bound that is too small: lengths count as that many, rounded up to whole pages
+    pages, lens = B.gq_kv8_select(q[:2].to(device()), bounds, table.to(device()), I32([100, 40]), 3, page, max_kv_len=33)
+    want, seen = B.gq_kv8_select(q[:2].to(device()), bounds, table.to(device()), I32([48, 40]), 3, page)
+    assert torch.equal(lens, seen) and torch.equal(pages, want) and lens.tolist() == [48, 40]
     pages, lens = B.gq_kv8_select(q[:2].to(device()), bounds, table[:, :0].contiguous().to(device()), I32([5, 5]), 3, page)
     assert lens.tolist() == [0, 0] and bool((pages == -1).all())
     pages, lens = B.gq_kv8_select(q[:0].to(device()), bounds, table[:0].to(device()), I32([]), 3, page)

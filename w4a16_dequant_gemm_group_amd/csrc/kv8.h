@@ -64,6 +64,18 @@ struct Kv8Attn : Kv4Attn {
   int64_t table_b, table_h;         // page_table entries from a sequence, and a head, to the next
 };
 
+// A weight p without its value scale S_V of 2^-40 .. 2^121 spans more than fp32 does where
+// p S_V has to be near 2^11.  So the sums hold p 2^40: at most 2^95, at least 2^-70 for the
+// heaviest key, with room for those far lighter; the results, which hold p S_V, get the
+// factor when they are done, and the reference of both is 40 less.
+constexpr float kKv8Shift = 40.0f, kKv8Up = 0x1p40f, kKv8Down = 0x1p-40f;
+
+// Factor of the scores of a block: what a row's queries and the block's keys were divided
+// by.  Never 0, which would make NaN of a hidden key's -inf, nor infinite, of a score of 0.
+__device__ __forceinline__ float kv8_factor(float A, float sk) {
+  return __builtin_amdgcn_fmed3f(A * sk, 0x1p-120f, 0x1.fffffep127f);
+}
+
 // Waves per SIMD of the rows kernel: as many workgroups as fit the LDS of a compute unit.
 constexpr int kv8_rows_waves(int d, int nq) {
   if (d == 64) return nq > 1 ? 3 : 4;   // four with two row tiles spill

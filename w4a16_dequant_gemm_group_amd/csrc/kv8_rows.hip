@@ -83,10 +83,10 @@ struct Rows8 : Rows<D, 1, NQ, true> {
     }
   }
 
-  // Scores to weights p = 2^(x A S_K - mref); `masked` where some row does not see
+  // Scores to weights p = 2^(x A S_K - mref + 40); `masked` where some row does not see
   // all 32 keys from position u on.  ok: bit t, block t exists.  The reference is the
-  // running maximum of score + log2 S_V less the room, so that P' = p S_V is what lies in
-  // fp16's range.  With S_V of 2^-40 .. 2^121 p stays in fp32's.
+  // running maximum of score + log2 S_V less the room, so that P' = p S_V 2^-40 is what lies in
+  // fp16's range (kKv8Shift).
   __device__ __forceinline__ void weights(const Kv4Attn& a, const Seq& s, int qt, int u, bool masked, int ok,
                                           const float (&sk)[2], const float (&sv)[2], float (&x)[NQ][2][4], int kg) {
     float lv[2];
@@ -94,7 +94,7 @@ struct Rows8 : Rows<D, 1, NQ, true> {
     for (int t = 0; t < 2; ++t) lv[t] = __log2f(sv[t]) - kRoom;
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) {
-      const float f[2] = {A[nq] * sk[0], A[nq] * sk[1]};
+      const float f[2] = {kv8_factor(A[nq], sk[0]), kv8_factor(A[nq], sk[1])};
       uint32_t hide = 0;
       float top = kNegInf;
       if (masked) {
@@ -127,10 +127,11 @@ struct Rows8 : Rows<D, 1, NQ, true> {
 #pragma unroll
         for (int i = 0; i < 2 * NS; ++i) o[nq][i] *= c;
       }
+      const float base = kKv8Shift - mref[nq];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[nq][t][i] = exp2_hw(__builtin_fmaf(x[nq][t][i], f[t], -mref[nq]));
+        for (int i = 0; i < 4; ++i) x[nq][t][i] = exp2_hw(__builtin_fmaf(x[nq][t][i], f[t], base));
       if (masked) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -154,7 +155,7 @@ struct Rows8 : Rows<D, 1, NQ, true> {
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float e = p[nq][t][i] * sv[t];
+          const float e = p[nq][t][i] * (sv[t] * kKv8Down);
           _Float16 h = (_Float16)e;
           if (rest) {
             const _Float16 d = (_Float16)(e - (float)h);
@@ -200,6 +201,9 @@ struct Rows8 : Rows<D, 1, NQ, true> {
     }
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq) {
+#pragma unroll
+      for (int i = 0; i < T; ++i) o[nq][i] *= kKv8Up;
+      mref[nq] -= kKv8Shift;
       float lt = l[nq];
       lt += __shfl_xor(lt, 16);
       lt += __shfl_xor(lt, 32);

@@ -335,7 +335,7 @@ hipError_t launch_kv8_select(const Kv8Select& a, gq_dtype dt, hipStream_t s) {
     if (e) return e;
   }
   const int64_t lists = a.q_tokens * a.hkv;
-  const dim3 grid((unsigned)(lists < (1 << 22) ? lists : 1 << 22));
+  const dim3 grid((unsigned)(lists < (1 << 21) ? lists : 1 << 21));   // fewer than 2^32 threads
   if (a.most <= kSort * kHeld)
     hipLaunchKernelGGL(kv8_choose_kernel<true>, grid, dim3(kSort), 0, s, a, lists);
   else

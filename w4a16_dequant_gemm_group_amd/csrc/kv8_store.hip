@@ -407,14 +407,14 @@ __device__ __forceinline__ void write_heads(const Kv8Append& a, const Part& p, i
   }
 }
 
-// grid.y: heads (or as many of them as run at once); grid.z: blocks (a wave for keys, a
-// wave for values), bounds.
+// grid.y: heads (or as many of them as run at once); grid.z: bounds, blocks (a wave for keys, a
+// wave for values).
 template <int D, bool BF16>
 __global__ __launch_bounds__(128) void kv8_append_kernel(Kv8Append a) {
   __shared__ uint4 smem[16 * kTurnPitch<D> > 4096 ? 16 * kTurnPitch<D> / 32 : 128][2];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const bool pages = blockIdx.z == 1;
+  const bool pages = blockIdx.z + 1 < gridDim.z;   // first, as theirs is the longest chain of loads
   const int ps = a.c.page_shift, unit = pages ? ps : 4, run = pages ? a.page_run : a.run;
   const int64_t cap = a.table_pages << ps;
   for (int64_t r0 = (int64_t)blockIdx.x * run; r0 < a.tokens; r0 += (int64_t)gridDim.x * run) {

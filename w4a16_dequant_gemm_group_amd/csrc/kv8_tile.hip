@@ -31,9 +31,10 @@ struct Tile8 : Tile<D, 1, true, false, false> {
   using Base::mref;
   using Base::o;
   using Base::q;
+  float ltop;      // log2 of the largest value scale so far
   static constexpr int NS = D / 32, NW = Base::NW, TQ = Base::TQ, KP = Base::KP, VP = kTK * 2;
   static constexpr int kV = kTK * KP;                 // the values, behind the keys
-  static constexpr int kEx = kV + D * VP;             // floats {log2 S_V, 1 / S_V, S_K} of the four blocks
+  static constexpr int kEx = kV + D * VP;             // floats {log2 S_V, 2^40 / S_V, S_K} of the four blocks
   static constexpr int kBuf = kEx + 48;
   static constexpr int kBufs = 2 * kBuf <= 160 * 1024 ? 2 : 1;
 
@@ -80,7 +81,7 @@ struct Tile8 : Tile<D, 1, true, false, false> {
       // -inf takes keys that do not exist out of the softmax
       const float e = c.ok ? __log2f(c.S) : kNegInf;
       ex[blk] = e;
-      ex[4 + blk] = c.ok ? exp2_hw(-e) : 1.0f;
+      ex[4 + blk] = c.ok ? exp2_hw(kKv8Shift - e) : 1.0f;
     }
     uint8_t* vb = buf + kV + (kg >> 1) * 8;
 #pragma unroll
@@ -126,12 +127,22 @@ struct Tile8 : Tile<D, 1, true, false, false> {
 #pragma unroll
       for (int i = 0; i < 8; ++i) q[st][i] = (_Float16)(x[i] * f);
     }
-    mref = kNegInf;
+    mref = ltop = kNegInf;
     l = 0.0f;
 #pragma unroll
     for (int d = 0; d < NS; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+  }
+
+  // Base::finish with the reference of kKv8Shift.
+  __device__ __forceinline__ void finish(const Kv4Attn& a, const Seq& s, int h, int qt, int ri, float* part, int hf) {
+#pragma unroll
+    for (int d = 0; d < NS; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] *= kKv8Up;
+    mref -= kKv8Shift;
+    Base::finish(a, s, h, qt, ri, part, hf);
   }
 
   // One tile of 64 keys from position u on, in the written order of kv4_tile.h: operands
@@ -167,7 +178,8 @@ struct Tile8 : Tile<D, 1, true, false, false> {
 #pragma unroll
     for (int r = 0; r < kAhead; ++r) ring[r] = read_v(r);
     const float4 ev = *(const float4*)(buf + kEx), ei = *(const float4*)(buf + kEx + 16), ek = *(const float4*)(buf + kEx + 32);
-    const float evv[4] = {ev.x, ev.y, ev.z, ev.w}, eiv[4] = {ei.x, ei.y, ei.z, ei.w}, ekv[4] = {ek.x, ek.y, ek.z, ek.w};
+    const float evv[4] = {ev.x, ev.y, ev.z, ev.w}, ekv[4] = {ek.x, ek.y, ek.z, ek.w};
+    float eiv[4] = {ei.x, ei.y, ei.z, ei.w};
     const float least = fminf(fminf(ev.x, ev.y), fminf(ev.z, ev.w));
     // whether every row of the wave sees all 64 keys
     const int rows = s.n * a.r;
@@ -189,10 +201,9 @@ struct Tile8 : Tile<D, 1, true, false, false> {
           x[tt][i] = j <= last && j >= first && evv[2 * tt + i / 8] != kNegInf ? x[tt][i] : kNegInf;
         }
     }
-    // never 0, which would make NaN of a hidden key's -inf
     float Ab[4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) Ab[b] = fmaxf(A * ekv[b], 0x1p-120f);
+    for (int b = 0; b < 4; ++b) Ab[b] = kv8_factor(A, ekv[b]);
     float top = kNegInf;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -214,6 +225,18 @@ struct Tile8 : Tile<D, 1, true, false, false> {
         for (int i = 0; i < 16; ++i) o[d][i] *= f;
     }
     const float base = mref == kNegInf ? 0.0f : mref;
+    // A block whose values are 2^80 and more smaller than others: its weights times its scale
+    // are nothing to the results, but may be most of the sum, and too small for fp32.
+    ltop = fmaxf(fmaxf(fmaxf(ev.x, ev.y), fmaxf(ev.z, ev.w)), ltop);
+    if (__builtin_expect(__builtin_amdgcn_readfirstlane(least < ltop - 80.0f), 0)) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (evv[b] < ltop - 80.0f) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) l += exp2_hw(__builtin_fmaf(x[b >> 1][8 * (b & 1) + i], Ab[b], kKv8Shift - base));
+          eiv[b] = 0.0f;
+        }
+    }
     f16x8 pw[2];
     float sum[2];
     auto weigh = [&](int b, int from, int to) {
