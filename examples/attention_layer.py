@@ -32,8 +32,7 @@ class AttentionLayer:
         self.o = self._weight(hidden, q_heads * head_dim, gen)
         self.cache = B.gq_kv4_empty(n_pages, kv_heads, head_dim, page, group)
         self.free = list(range(n_pages))
-        half = head_dim // 2
-        self.freq = 10000.0 ** (-torch.arange(half, device="cuda", dtype=torch.float64) / half)
+        self.freq, _ = B.gq_rope_frequencies(head_dim, 10000.0)
 
     def _weight(self, n, k, gen):
         w = (torch.randn(n, k, generator=gen, device="cuda") / math.sqrt(k)).to(self.dtype)
@@ -44,12 +43,6 @@ class AttentionLayer:
         f16 = "_f16" if self.dtype == torch.float16 else ""
         kind = "gemv" if x.shape[0] <= 16 else "gemm"
         return getattr(B, f"gq_w4a16_{kind}{f16}")(x, *w, group_size=self.g)
-
-    def _rotate(self, x, pos):
-        a = pos.double()[:, None, None] * self.freq
-        c, s = a.cos().float(), a.sin().float()
-        lo, hi = x.float().chunk(2, -1)
-        return torch.cat((lo * c - hi * s, hi * c + lo * s), -1).to(x.dtype)
 
     def pages_for(self, lengths, room):
         """A page table for sequences that may grow to lengths + room tokens."""
@@ -68,8 +61,8 @@ class AttentionLayer:
         the cache at `slots` and every token attends to its sequence so far."""
         t = x.shape[0]
         qkv = self._matmul(x, self.qkv).view(t, self.hq + 2 * self.hkv, self.d)
-        q = self._rotate(qkv[:, :self.hq], pos)
-        k = self._rotate(qkv[:, self.hq:self.hq + self.hkv], pos)
+        turned = B.gq_rope(qkv[:, :self.hq + self.hkv], pos, self.freq)
+        q, k = turned[:, :self.hq], turned[:, self.hq:]
         v = qkv[:, self.hq + self.hkv:]                       # a strided slice, taken as it is
         B.gq_kv4_write(k, v, self.cache, slots, self.g)
         out = B.gq_kv4_attention(q, self.cache, table, kv_lens, self.g, q_starts=q_starts, max_q_len=max_q_len,
