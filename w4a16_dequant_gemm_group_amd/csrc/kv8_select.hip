@@ -165,14 +165,24 @@ __device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
   return (uint64_t)hi << 32 | lo;
 }
 __device__ __forceinline__ uint64_t smaller(uint64_t a, uint64_t b) { return a < b ? a : b; }
-// Smallest over the wave, in every lane.
-__device__ __forceinline__ uint64_t wave_min(uint64_t v) {
+// Smallest over a row of 16 lanes, and over the wave, in every lane.
+__device__ __forceinline__ uint64_t row_min(uint64_t v) {
   v = smaller(v, dpp_u64<0xB1>(v));
   v = smaller(v, dpp_u64<0x4E>(v));
   v = smaller(v, dpp_u64<0x141>(v));
-  v = smaller(v, dpp_u64<0x140>(v));
+  return smaller(v, dpp_u64<0x140>(v));
+}
+__device__ __forceinline__ uint64_t wave_min(uint64_t v) {
+  v = row_min(v);
   v = smaller(v, __shfl_xor(v, 16));
   return smaller(v, __shfl_xor(v, 32));
+}
+// Sum over a row of 16 lanes, in every lane.
+__device__ __forceinline__ uint32_t row_sum(uint32_t v) {
+  v += dpp_or_0<0xB1>(v);
+  v += dpp_or_0<0x4E>(v);
+  v += dpp_or_0<0x141>(v);
+  return v + dpp_or_0<0x140>(v);
 }
 
 constexpr int kSort = 1024, kSortWaves = kSort / 64;   // threads of a workgroup that chooses
@@ -239,11 +249,9 @@ __global__ __launch_bounds__(kSort) void kv8_choose_kernel(Kv8Select a, int64_t 
     }
     if (tid < 256) bins[0][tid] = 0;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) {
-      least = smaller(least, edge[0][w]);
-      most = smaller(most, edge[1][w]);
-    }
+    static_assert(kSortWaves == 16, "a lane of a row per wave");
+    least = row_min(edge[0][lane & 15]);
+    most = row_min(edge[1][lane & 15]);
     // pages with lo <= key <= hi: `need` of them are taken, with more than hi: all
     uint64_t lo = least, hi = ~most;
     int shift = 64 - __builtin_clzll((hi - lo) | 1) - 8;
@@ -290,14 +298,9 @@ __global__ __launch_bounds__(kSort) void kv8_choose_kernel(Kv8Select a, int64_t 
       sums[1][wave] = v;
     }
     __syncthreads();
-    u -= above;
-    v -= step;
-#pragma unroll
-    for (int w = 0; w < kSortWaves; ++w)
-      if (w < wave) {
-        u += sums[0][w];
-        v += sums[1][w];
-      }
+    const bool before = (lane & 15) < wave;
+    u += row_sum(before ? sums[0][lane & 15] : 0u) - above;
+    v += row_sum(before ? sums[1][lane & 15] : 0u) - step;
     uint32_t at = a.first + u + (v < need ? v : need);
     each([&](int j, uint64_t k) {
       bool take = k > hi;
