@@ -96,6 +96,28 @@ def test_pages_that_do_not_exist_and_values_that_are_not_finite():
     assert pages[0, 0].tolist() == table[0, [0, 1, 2, 3, 4, 39]].tolist()
 
 
+def test_scores_that_are_infinite():
+    """Scores of both infinities and between them, pages that do not exist among them: the
+    whole range of the scores' integers."""
+    h, d, page, n = 1, 64, 16, 300
+    table, n_pages = tables([n * page], page)
+    bounds = B.gq_kv8_bounds_empty(n_pages, h, d, torch.bfloat16, device=device())
+    q = torch.zeros(1, 2, d).bfloat16()
+    q[0, 0, 0], q[0, 0, 1], q[0, 1, 1] = float("inf"), 1.0, 2.0 ** 100
+    g = torch.Generator().manual_seed(6)
+    for every in (2, 7, 150):
+        lo = torch.randn(n_pages, h, 2, d, generator=g).sort(2).values      # smallest, largest
+        up = torch.arange(n) % every == 1
+        lo[table[0].long(), 0, :, 0] = torch.where(up, 1.0, -1.0)[:, None]
+        bounds.copy_(lo)
+        for keep in (2, 3, 17, 100, 299):
+            check(q[:, :1], bounds, table, [1], [n * page], page, keep, 1, 1, h)      # +inf and -inf alone
+            check(q, bounds, table, [1], [n * page], page, keep, 1, 1, h)             # and finite ones
+            gone = table.clone()
+            gone[0, 3::5] = -1
+            check(q, bounds, gone, [1], [n * page], page, keep, 1, 1, h)
+
+
 def test_queries_without_pages_and_lengths_out_of_range():
     h, d, page = 2, 64, 16
     table, n_pages, k, cache, bounds = setup(h, d, page, "bf16", [100, 40], seed=4)

@@ -282,7 +282,8 @@ __global__ __launch_bounds__(kSort) void kv8_choose_kernel(Kv8Select a, int64_t 
       __syncthreads();
       need -= found[1];
       lo += (uint64_t)found[0] << shift;
-      hi = smaller(hi, lo + (((uint64_t)1 << shift) - 1));
+      const uint64_t rest = ((uint64_t)1 << shift) - 1;
+      hi = hi - lo < rest ? hi : lo + rest;      // lo + rest may be beyond 64 bits: +infinity lies near their end
       if (found[2] == need || shift == 0) break;
       shift = shift < 8 ? 0 : shift - 8;
     }
