@@ -62,14 +62,14 @@ gq_status gq_rope_frequencies(int64_t rot_dim, double base, gq_rope_scaling scal
  *              are the elements from one token, and from one head, to the next,
  *              head_dim contiguous: slices of a fused projection's output are taken as
  *              they are.  out may be x itself, with the same strides; other overlaps
- *              are not allowed
+ *              are not allowed, nor are rows of out that overlap
  *   positions  [tokens] int64, of any sign
  *   freqs      [rot_dim / 2] double
  * Angles are products in binary64, reduced to a turn there (off by 2^-52 of the
  * angle); sines, products and sums are fp32, rounded once to dtype (nearest-even).
  * Errors: INVALID_ARG (tokens < 0 or > 2^30, heads < 0 or > 65536, head_dim odd or
  * outside 2 .. 1024, rot_dim odd or outside 2 .. head_dim, strides beyond 2^40,
- * amplitude not finite, x == out with other strides, NULL), MISALIGNED (x, out to their
+ * amplitude not finite, x == out with other strides, out's strides below head_dim, NULL), MISALIGNED (x, out to their
  * elements, positions and freqs to 8 bytes), UNSUPPORTED (device). */
 typedef struct {
   const void* x;

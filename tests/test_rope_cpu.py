@@ -103,7 +103,10 @@ def test_refusals():
                dict(head_dim=1026), dict(rot_dim=0), dict(rot_dim=130), dict(rot_dim=63),
                dict(x_token_stride=(1 << 40) + 1), dict(out_head_stride=-(1 << 40) - 1),
                dict(amplitude=float("nan")), dict(amplitude=float("inf")), dict(interleaved=2), dict(inverse=-1),
-               dict(out=FAKE, out_token_stride=2048), dict(out=FAKE, out_head_stride=256)):
+               dict(out=FAKE, out_token_stride=2048), dict(out=FAKE, out_head_stride=256),
+               # rows that overlap
+               dict(out_token_stride=0), dict(out_head_stride=0), dict(out_head_stride=-127),
+               dict(out=FAKE, x_token_stride=0, out_token_stride=0)):
         assert L.gq_rope(args(**kw), None) == B.GQ_ERR_INVALID_ARG, kw
     for kw in (dict(x=FAKE + 1), dict(out=FAKE + 1), dict(positions=FAKE + 4), dict(freqs=FAKE + 4),
                dict(dtype=B.GQ_F32, x=FAKE + 2)):

@@ -5,9 +5,9 @@
 // the same for all of its heads, so a workgroup first makes the table of cosines
 // and sines of a few tokens in LDS and then turns all their heads with it: 64
 // sines and cosines per token against 40 x 8 pieces of 40 heads of 128.
-// An angle is p f in binary64, reduced to a turn there; what fp32 cannot hold of the
-// turn is put back as a small rotation, so that cosine and sine are good to about an
-// ulp of 1 at any position.
+// An angle is p f in binary64, reduced to a turn there (off by 2^-52 of the angle: 2^-22 at
+// a position of 2^30); what fp32 cannot hold of the turn is put back as a small rotation, so
+// that cosine and sine are good to about an ulp of 1 besides.
 #include "rope.h"
 #include "stream_util.h"
 

@@ -2,6 +2,7 @@
 // host before any HIP call, and the frequencies.
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 
 #include "rope.h"
 
@@ -71,7 +72,10 @@ gq_status gq_rope(const gq_rope_args* args, void* stream) {
     return GQ_ERR_INVALID_ARG;
   if (a.tokens == 0 || a.heads == 0) return GQ_OK;
   if (!a.x || !a.out || !a.positions || !a.freqs) return GQ_ERR_INVALID_ARG;
-  // the stride of a dimension of one element is never walked
+  // Rows of out apart from each other.  The stride of a dimension of one element is never walked.
+  if ((a.tokens > 1 && std::llabs(a.out_token_stride) < a.head_dim) ||
+      (a.heads > 1 && std::llabs(a.out_head_stride) < a.head_dim))
+    return GQ_ERR_INVALID_ARG;
   if (a.x == a.out && ((a.tokens > 1 && a.x_token_stride != a.out_token_stride) ||
                        (a.heads > 1 && a.x_head_stride != a.out_head_stride)))
     return GQ_ERR_INVALID_ARG;
