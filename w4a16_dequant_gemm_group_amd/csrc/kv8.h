@@ -76,6 +76,19 @@ __device__ __forceinline__ float kv8_factor(float A, float sk) {
   return __builtin_amdgcn_fmed3f(A * sk, 0x1p-120f, 0x1.fffffep127f);
 }
 
+// Two results as 16 bits, nearest-even.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_result(float a, float b) {
+  if constexpr (BF16) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+  } else {
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+  }
+}
+
 // Waves per SIMD of the rows kernel: as many workgroups as fit the LDS of a compute unit.
 constexpr int kv8_rows_waves(int d, int nq) {
   if (d == 64) return nq > 1 ? 3 : 4;   // four with two row tiles spill

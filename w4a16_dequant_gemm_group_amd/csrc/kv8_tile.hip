@@ -10,6 +10,7 @@
 // 2.1 / 2.35 us at 64 / 96 / 128 channels, a row tile taken up about five of them.
 #include "kv8.h"
 #include "kv4_tile.h"
+#include <type_traits>
 
 namespace gq {
 namespace kv8 {
@@ -138,14 +139,47 @@ struct Tile8 : Tile<D, 1, true, false, false> {
       for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
   }
 
-  // Base::finish with the reference of kKv8Shift.
+  // Writes the rows: to `part`, or as results (of lanes n and n + 32 each gets 8 channels of
+  // two pieces, so that stores are 16 bytes).
   __device__ __forceinline__ void finish(const Kv4Attn& a, const Seq& s, int h, int qt, int ri, float* part, int hf) {
-#pragma unroll
-    for (int d = 0; d < NS; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[d][i] *= kKv8Up;
+    const int row = qt * TQ + ri;
+    const float L = l + __shfl_xor(l, 32);
+    if (row >= s.n * a.r) return;
     mref -= kKv8Shift;
-    Base::finish(a, s, h, qt, ri, part, hf);
+    if (part) {
+#pragma unroll
+      for (int d = 0; d < NS; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *(float4*)(part + ri * D + 32 * d + 8 * i + 4 * hf) =
+              make_float4(o[d][4 * i] * kKv8Up, o[d][4 * i + 1] * kKv8Up, o[d][4 * i + 2] * kKv8Up, o[d][4 * i + 3] * kKv8Up);
+      if (hf == 0) {
+        part[TQ * D + ri] = mref;
+        part[TQ * D + TQ + ri] = L;
+      }
+      return;
+    }
+    const int64_t orow = out_row(a, s, h, row);
+    const float inv = L == 0.0f ? 0.0f : kKv8Up / L;
+    uint16_t* const out = a.out + orow * D + 8 * hf;
+    auto write = [&](auto bf16) {
+#pragma unroll
+      for (int d = 0; d < NS; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = pack_result<decltype(bf16)::value>(o[d][i + 2 * j] * inv, o[d][i + 2 * j + 1] * inv);
+          const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+          const auto y = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+          *(uint4*)(out + 32 * d + 2 * i) = make_uint4(x[0], y[0], x[1], y[1]);
+        }
+    };
+    if (a.bf16)
+      write(std::true_type{});
+    else
+      write(std::false_type{});
+    if (a.lse && hf == 0) a.lse[orow] = Rows<D, 1, 1, true>::lse_of(mref, L);
   }
 
   // One tile of 64 keys from position u on, in the written order of kv4_tile.h: operands
