@@ -36,6 +36,15 @@ struct Tile8 : Tile<D, 1, true, false, false> {
   using Base::o;
   using Base::q;
   float ltop;      // log2 of the largest value scale so far
+  bool steep;
+  int full0, full1;   // tiles from positions in between on: every row of the wave sees all 64 keys
+
+  __device__ __forceinline__ void set_full(const Kv4Attn& a, const Seq& s, int row0) {
+    const int rows = s.n * a.r, last = row0 + 32 < rows ? row0 + 31 : rows - 1, p = s.kv - s.n;
+    full1 = s.kv - kTK;
+    if (a.causal) full1 = min(full1, p + div_r(a, row0) - (kTK - 1));
+    full0 = a.window > 0 ? p + div_r(a, last) - a.window + 1 : 0;
+  }
   static constexpr int NS = D / 32, NW = Base::NW, TQ = Base::TQ, KP = Base::KP, VP = kTK * 2;
   static constexpr int kV = kTK * KP;                 // the values, behind the keys
   static constexpr int kEx = kV + D * VP;             // floats {log2 S_V, 2^40 / S_V, S_K} of the four blocks
@@ -131,7 +140,10 @@ struct Tile8 : Tile<D, 1, true, false, false> {
 #pragma unroll
       for (int i = 0; i < 8; ++i) q[st][i] = (_Float16)(x[i] * f);
     }
-    mref = ltop = kNegInf;
+    // A finite reference below all scores and a scale below all: nothing has to be told apart.
+    mref = -0x1.fffffep127f;
+    ltop = -100.0f;
+    steep = __any(!(A < 0x1p6f));   // times a scale of 2^121 beyond fp32
     l = 0.0f;
 #pragma unroll
     for (int d = 0; d < NS; ++d)
@@ -217,16 +229,14 @@ struct Tile8 : Tile<D, 1, true, false, false> {
     const float4 ev = *(const float4*)(buf + kEx), ei = *(const float4*)(buf + kEx + 16), ek = *(const float4*)(buf + kEx + 32);
     const float evv[4] = {ev.x, ev.y, ev.z, ev.w}, ekv[4] = {ek.x, ek.y, ek.z, ek.w};
     float eiv[4] = {ei.x, ei.y, ei.z, ei.w};
-    const float least = fminf(fminf(ev.x, ev.y), fminf(ev.z, ev.w));
-    // whether every row of the wave sees all 64 keys
-    const int rows = s.n * a.r;
-    const int lastrow = row0 + 32 < rows ? row0 + 31 : rows - 1;
-    bool full = u + kTK <= s.kv;
-    if (a.causal) full = full && u + kTK - 1 <= s.kv - s.n + div_r(a, row0);
-    if (a.window > 0) full = full && u > s.kv - s.n + div_r(a, lastrow) - a.window;
-    // and all of them exist: a query that is not finite makes NaN of what stands there
-    full = full && __builtin_amdgcn_readfirstlane(__float_as_uint(least)) != __float_as_uint(kNegInf);
-    if (!full) {
+    // (Minima and maxima start with a number: two operands that might be signalling NaN cost an
+    // instruction more each.)
+    const float least = fminf(fminf(fminf(fminf(-kNegInf, ev.x), ev.y), ev.z), ev.w);
+    ltop = fmaxf(fmaxf(fmaxf(fmaxf(ltop, ev.x), ev.y), ev.z), ev.w);
+    // A block that does not exist, or whose values are 2^80 and more smaller than others.
+    const bool odd = __builtin_amdgcn_readfirstlane(least < ltop - 80.0f);
+    // A query that is not finite makes NaN of what stands where no block is.
+    if (u < full0 || u > full1 || odd) {
       const int pos = s.kv - s.n + div_r(a, row0 + n);
       const int last = a.causal && pos < s.kv - 1 ? pos : s.kv - 1;
       const int first = a.window > 0 ? pos - a.window + 1 : 0;
@@ -240,18 +250,21 @@ struct Tile8 : Tile<D, 1, true, false, false> {
     }
     float Ab[4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) Ab[b] = kv8_factor(A, ekv[b]);
+    for (int b = 0; b < 4; ++b) Ab[b] = A * ekv[b];
+    if (__builtin_expect(steep, 0)) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) Ab[b] = kv8_factor(A, ekv[b]);
+    }
     float top = kNegInf;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      float t = x[b >> 1][8 * (b & 1)];
+      float t = kNegInf;   // first: a maximum of two products of the matrix cores costs two more instructions
 #pragma unroll
-      for (int i = 1; i < 8; ++i) t = fmaxf(t, x[b >> 1][8 * (b & 1) + i]);
+      for (int i = 0; i < 8; ++i) t = fmaxf(t, x[b >> 1][8 * (b & 1) + i]);
       top = fmaxf(top, __builtin_fmaf(t, Ab[b], evv[b]));
     }
-    top -= kTileRoom;
-    if (__any(top > mref + kTileSlack)) {
-      top = fmaxf(top, __shfl_xor(top, 32));
+    if (__any(top > mref + (kTileRoom + kTileSlack))) {
+      top = fmaxf(top, __shfl_xor(top, 32)) - kTileRoom;
       const float mn = fmaxf(top, mref);
       const float f = mn == mref ? 1.0f : exp2_hw(mref - mn);
       mref = mn;
@@ -261,16 +274,14 @@ struct Tile8 : Tile<D, 1, true, false, false> {
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] *= f;
     }
-    const float base = mref == kNegInf ? 0.0f : mref;
-    // A block whose values are 2^80 and more smaller than others: its weights times its scale
-    // are nothing to the results, but may be most of the sum, and too small for fp32.
-    ltop = fmaxf(fmaxf(fmaxf(ev.x, ev.y), fmaxf(ev.z, ev.w)), ltop);
-    if (__builtin_expect(__builtin_amdgcn_readfirstlane(least < ltop - 80.0f), 0)) {
+    // Small values' weights times their scale are nothing to the results, but may be most of
+    // the sum, and too small for fp32.
+    if (__builtin_expect(odd, 0)) {
 #pragma unroll
       for (int b = 0; b < 4; ++b)
         if (evv[b] < ltop - 80.0f) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) l += exp2_hw(__builtin_fmaf(x[b >> 1][8 * (b & 1) + i], Ab[b], kKv8Shift - base));
+          for (int i = 0; i < 8; ++i) l += exp2_hw(__builtin_fmaf(x[b >> 1][8 * (b & 1) + i], Ab[b], kKv8Shift - mref));
           eiv[b] = 0.0f;
         }
     }
@@ -280,7 +291,7 @@ struct Tile8 : Tile<D, 1, true, false, false> {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i >= from && i < to) {
-          const float e = exp2_hw(__builtin_fmaf(x[b >> 1][8 * (b & 1) + i], Ab[b], evv[b] - base));
+          const float e = exp2_hw(__builtin_fmaf(x[b >> 1][8 * (b & 1) + i], Ab[b], evv[b] - mref));
           sum[b & 1] = i == 0 ? e : sum[b & 1] + e;
           pw[b & 1][i] = (_Float16)e;
           if (i == 7) l = __builtin_fmaf(sum[b & 1], eiv[b], l);
@@ -360,6 +371,7 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv8_til
       st.fetch_q(a, s, cur.h, row0 + n, hf);
       fetch(page, u0);
       st.take_q(a);
+      st.set_full(a, s, row0);
       expand(smem);
       fetch(page_of(u0 + kTK), u0 + kTK);
       int64_t next = page_of(u0 + 2 * kTK);
@@ -367,7 +379,8 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv8_til
       // Codes are fetched a tile before they are expanded.  The waves of keys
       // expand before their products and those of values after: of the two
       // waves of a SIMD one has vector work while the other multiplies.
-      for (int u = u0, b = 0; u < stop; u += kTK, b ^= T::kBufs - 1) {
+      auto step = [&](int u, auto which) {
+        constexpr int b = decltype(which)::value;
         const bool more = u + kTK < stop;
         auto refill = [&] {
           if (!more) return;
@@ -380,6 +393,10 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv8_til
         if (T::kBufs == 1) __syncthreads();
         if (kBoth || !is_k) refill();
         __syncthreads();
+      };
+      for (int u = u0; u < stop; u += 2 * kTK) {
+        step(u, std::integral_constant<int, 0>{});
+        if (u + kTK < stop) step(u + kTK, std::integral_constant<int, T::kBufs - 1>{});
       }
       float* part = nullptr;
       if (!(starts && ends)) {
