@@ -57,10 +57,12 @@ struct Tile8 : Tile<D, 1, true, false, false> {
     float S;
     bool ok;
 
-    __device__ __forceinline__ void load(const Kv8Attn& a, int64_t page, int h, int u, bool values, uint32_t lane) {
-      ok = page >= 0 && page < a.c.n_pages;
-      const int64_t blk = kv8_block(ok ? page : 0, a.c.hkv, h, a.c.page_shift, ok ? u & ((1 << a.c.page_shift) - 1) : 0);
-      const uint8_t* p = a.c.cache + blk * (32 * D) + (values ? 16 * D : 0);
+    // p0, s0: codes and scale of the head's first block of page 0; per: blocks of a page.
+    __device__ __forceinline__ void load(const uint8_t* p0, const float* s0, uint32_t per, uint32_t n_pages, int page, int in,
+                                         uint32_t lane) {
+      ok = (uint32_t)page < n_pages;
+      const uint64_t blk = ok ? (uint64_t)(uint32_t)page * per + (uint32_t)in : 0;
+      const uint8_t* p = p0 + blk * (32 * D);
 #pragma unroll
       for (int s = 0; s + 1 < NS; s += 2) {
         const u32x4 w = *(const u32x4*)(p + 512 * s + 16 * lane);
@@ -70,8 +72,7 @@ struct Tile8 : Tile<D, 1, true, false, false> {
         const uint2 w = *(const uint2*)(p + 512 * (NS - 1) + 8 * lane);
         d[2 * NS - 2] = w.x; d[2 * NS - 1] = w.y;
       }
-      const float2 sc = a.scales[blk];
-      S = values ? sc.y : sc.x;
+      S = s0[2 * blk];
     }
   };
 
@@ -347,15 +348,20 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv8_til
       if (u0 < sp.lo) u0 = sp.lo & ~(kTK - 1);
       const PageRow table = (PageRow)(a.table + cur.b * a.table_b + cur.h * a.table_h);
       // page of this wave's 16 of the 64 keys from u on, -1 where no row sees them
-      auto page_of = [&](int u) -> int64_t {
+      auto page_of = [&](int u) -> int {
         const int pos = u + blk * 16;
         return pos < stop && pos + 16 > sp.lo ? table[pos >> ps] : -1;
       };
       typename T::Codes ck, cv;   // a wave that expands one of them uses ck for it
-      auto fetch = [&](int64_t page, int u) {
-        u += blk * 16;
-        ck.load(a, page, cur.h, u, !kBoth && !is_k, lane);
-        if constexpr (kBoth) cv.load(a, page, cur.h, u, true, lane);
+      const int64_t head = (int64_t)cur.h << (ps - 4);
+      const bool ckv = !kBoth && !is_k;
+      const uint8_t* const codes0 = a.c.cache + head * (32 * D) + (ckv ? 16 * D : 0);
+      const float* const scales0 = (const float*)(a.scales + head) + (ckv ? 1 : 0);
+      const uint32_t per = (uint32_t)a.c.hkv << (ps - 4), n_pages = (uint32_t)a.c.n_pages;
+      auto fetch = [&](int page, int u) {
+        const int in = ((u + blk * 16) & ((1 << ps) - 1)) >> 4;
+        ck.load(codes0, scales0, per, n_pages, page, in, lane);
+        if constexpr (kBoth) cv.load(codes0 + 16 * D, scales0 + 1, per, n_pages, page, in, lane);
       };
       auto expand = [&](uint8_t* buf) {
         if constexpr (kBoth) {
@@ -367,14 +373,14 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv8_til
           T::expand_v(ck, buf, blk, m, kg);
         }
       };
-      const int64_t page = page_of(u0);
+      const int page = page_of(u0);
       st.fetch_q(a, s, cur.h, row0 + n, hf);
       fetch(page, u0);
       st.take_q(a);
       st.set_full(a, s, row0);
       expand(smem);
       fetch(page_of(u0 + kTK), u0 + kTK);
-      int64_t next = page_of(u0 + 2 * kTK);
+      int next = page_of(u0 + 2 * kTK);
       __syncthreads();
       // Codes are fetched a tile before they are expanded.  The waves of keys
       // expand before their products and those of values after: of the two
@@ -384,9 +390,10 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv8_til
         const bool more = u + kTK < stop;
         auto refill = [&] {
           if (!more) return;
+          const int after = page_of(u + 3 * kTK);   // on its way while the codes are expanded
           expand(smem + (b ^ (T::kBufs - 1)) * T::kBuf);
           fetch(next, u + 2 * kTK);
-          next = page_of(u + 3 * kTK);
+          next = after;
         };
         if (!kBoth && is_k) refill();
         if (row0 < s.n * a.r) st.attend(a, s, row0, u, smem + b * T::kBuf, n, hf);
