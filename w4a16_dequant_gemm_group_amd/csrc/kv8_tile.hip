@@ -434,7 +434,9 @@ hipError_t launch_tile_d(const Kv8Attn& a, const Kv4Plan& p, hipStream_t s) {
   using T = Tile8<D>;
   hipLaunchKernelGGL((kv8_tile_kernel<D>), dim3(a.workers), dim3(T::NW * 64), 0, s, a);
   if (hipError_t e = hipGetLastError()) return e;
-  return launch_join<D, T::TQ, 1>(a, p.tile_rows, s);
+  // Workgroups for 64 rows of a row tile go over all of them: where nothing was split, which a
+  // causal prompt's order often brings about, four times as many took 1 us more to start and end.
+  return launch_join<D, T::TQ, 1>(a, p.tile_rows < 64 ? p.tile_rows : 64, s);
 }
 
 }  // namespace kv8
