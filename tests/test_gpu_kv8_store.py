@@ -258,6 +258,28 @@ def test_many_sequences_and_long_prompts():
         assert torch.equal(bounds[long[j]].cpu()[:, 0], part.amin(0))
 
 
+@pytest.mark.parametrize("page,lens", [(32, [1111, 40, 1700]), (64, [2053, 700, 31]), (128, [1025, 2000]), (256, [4097])])
+def test_long_prompts_in_pages_of_several_blocks(page, lens):
+    """Every block and every bound of prompts that fill the dies several times over."""
+    d, h = 64, 2
+    table, n_pages = tables(lens, page, seed=page)
+    k = draw(sum(lens), h, d, "bf16", 9)
+    cache = B.gq_kv8_empty(n_pages, h, d, page, device=device()).fill_(0xFF)
+    bounds = B.gq_kv8_bounds_empty(n_pages, h, d, device=device()).fill_(float("nan"))
+    x = k.to(device())
+    B.gq_kv8_append(x, -x, cache, table.to(device()), I32(lens), starts_of(lens), bounds)
+    gk, gv = read_all(cache, table, lens, page, d, torch.float32)
+    bounds, at = bounds.cpu(), 0
+    for b, n in enumerate(lens):
+        want = expect(k[at:at + n], [], "bf16")[0]
+        assert torch.equal(gk[at:at + n].cpu(), want) and torch.equal(gv[at:at + n].cpu(), -want)
+        for j in range(-(-n // page)):
+            part = k[at + page * j:at + min(n, page * j + page)]
+            got = bounds[table[b, j].long()]
+            assert torch.equal(got[:, 0], part.amin(0)) and torch.equal(got[:, 1], part.amax(0))
+        at += n
+
+
 def test_graph_and_stream():
     d, h, page = 128, 2, 16
     table, n_pages = tables([64], page)
