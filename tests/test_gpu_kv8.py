@@ -213,6 +213,15 @@ def test_many_sequences(dtype):
     Case(6, 2, 128, 32, dtype, q, kv, seed=14).check(window=30)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("hq,h,d,q_len,batch,bound", [
+    (8, 4, 64, 1, 150, 2048), (8, 4, 64, 9, 150, 2048), (8, 2, 128, 1, 3, 1 << 20), (4, 1, 96, 5, 3, 1 << 20), (4, 1, 256, 5, 3, 1 << 20)])
+def test_bounds_that_promise_much(dtype, hq, h, d, q_len, batch, bound):
+    """Where the bounds say that more is read than the caches hold, codes pass them by."""
+    kv = [q_len + (i * 29) % 130 for i in range(batch)]
+    Case(hq, h, d, 16, dtype, [q_len] * batch, kv, seed=15).check(max_kv_len=bound)
+
+
 def test_cache_of_more_than_4_gib():
     """Pages beyond 2^32 bytes: appended, read back and attended to."""
     d, page, n_pages = 256, 1024, 8300

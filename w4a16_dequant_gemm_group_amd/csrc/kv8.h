@@ -95,8 +95,11 @@ constexpr int kv8_rows_waves(int d, int nq) {
   return d == 96 ? 3 : d == 128 ? 2 : 1;
 }
 
-Kv4Plan kv8_plan(const gq_kv8_attention_args& a);
-hipError_t launch_kv8_rows(const Kv8Attn& a, const Kv4Plan& p, hipStream_t s);
+struct Kv8Plan : Kv4Plan {
+  bool once;   // rows kernel: codes pass the caches by
+};
+Kv8Plan kv8_plan(const gq_kv8_attention_args& a);
+hipError_t launch_kv8_rows(const Kv8Attn& a, const Kv8Plan& p, hipStream_t s);
 hipError_t launch_kv8_tile(const Kv8Attn& a, const Kv4Plan& p, hipStream_t s);
 
 // Choice of pages: what the kernels get.

@@ -106,10 +106,10 @@ size_t select_bytes(const gq_kv8_select_args& a) {
 
 }  // namespace
 
-Kv4Plan kv8_plan(const gq_kv8_attention_args& a) {
+Kv8Plan kv8_plan(const gq_kv8_attention_args& a) {
   const int d = a.layout.head_dim, r = a.q_heads / a.layout.kv_heads;
   const int64_t rows = std::max<int64_t>(1, a.max_q_len) * r;
-  Kv4Plan p;
+  Kv8Plan p;
   p.workers = 0;
   p.ws_bytes = 0;
   p.nq = rows <= 16 ? 1 : 2;
@@ -139,6 +139,13 @@ Kv4Plan kv8_plan(const gq_kv8_attention_args& a) {
   // Of more row tiles it would be faster for longer (512 of 128 channels: 4096 keys), but one
   // long sequence among short ones runs alone then.
   const int64_t alone = d == 64 ? 960 + 14 * segs : d == 256 ? 360 + 7 * segs : 600 + 8 * segs;
+  // Codes that are read once, and are more than stays in the caches beside all else until they
+  // are read again, pass them by.  Without / with, us: 64 sequences of up to 8191 keys of 8 heads
+  // of 128 120.5 / 109.7, 131071 keys of one 65.0 / 58.7, 16 of 8000 75.1 / 68.6 (262 MB); but
+  // 32 of 8000 with one head (65 MB) 31.8 / 34.2, 4 of 500 14.7 / 15.3.  Chosen pages are often
+  // those of the queries beside (head_tables: 40 queries of 16 sequences 28.5 / 29.2).
+  const int64_t seen = a.window > 0 ? std::min<int64_t>(a.max_kv_len, (int64_t)a.window + a.max_q_len) : a.max_kv_len;
+  p.once = !a.head_tables && (double)a.batch * (double)seen * a.layout.kv_heads * 2.0 * d > (double)(1 << 27);
   p.split = p.tile || a.max_kv_len > std::min<int64_t>(2048, alone) || segs >= kMany;
   if (p.split) {
     // as many workgroups (a wave on each SIMD) as run at once
@@ -236,7 +243,7 @@ gq_status gq_kv8_attention(const gq_kv8_attention_args* args, void* workspace,
   if (!aligned16(a.q) || !aligned16(a.cache) || !aligned16(a.out)) return GQ_ERR_MISALIGNED;
   if (!aligned4(a.page_table) || !aligned4(a.kv_lens) || !aligned4(a.q_starts) || !aligned4(a.lse)) return GQ_ERR_MISALIGNED;
   probe_device();   // the split depends on the device's compute-unit count
-  const Kv4Plan p = kv8_plan(a);
+  const Kv8Plan p = kv8_plan(a);
   if (p.ws_bytes > 0 && (!workspace || workspace_bytes < p.ws_bytes)) return GQ_ERR_INVALID_ARG;
   if (p.ws_bytes > 0 && !aligned16(workspace)) return GQ_ERR_MISALIGNED;
   hipStream_t s = (hipStream_t)stream;

@@ -36,8 +36,14 @@ __device__ __forceinline__ void dma4(const void* p, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(p) : "memory", "m0");
 }
 
-// NW waves a workgroup: kWaves, or twice that where a compute unit has one alone.
-template <int D, int NQ, int NW>
+// dma16 of bytes that are not read again soon.
+__device__ __forceinline__ void dma16_once(const uint8_t* p, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" : : "s"(lds), "v"(voff), "s"(p) : "memory", "m0");
+}
+
+// NW waves a workgroup: kWaves, or twice that where a compute unit has one alone.  ONCE: codes
+// pass the caches by.
+template <int D, int NQ, int NW, bool ONCE>
 struct Rows8 : Rows<D, 1, NQ, true> {
   using Base = Rows<D, 1, NQ, true>;
   using Base::A;
@@ -307,7 +313,7 @@ struct Rows8 : Rows<D, 1, NQ, true> {
         const uint8_t* p = a.c.cache + blk[t] * kSub;
         const uint32_t dst = lds + buf * kUnitLds + t * kSub;
 #pragma unroll
-        for (int i = 0; i < kSub; i += 1024) dma16(p + i, lane * 16u, dst + i);
+        for (int i = 0; i < kSub; i += 1024) ONCE ? dma16_once(p + i, lane * 16u, dst + i) : dma16(p + i, lane * 16u, dst + i);
       }
       if (lane < 4) dma4((const float*)(a.scales + (lane & 2 ? blk[1] : blk[0])) + (lane & 1), lds + buf * kUnitLds + 2 * kSub);
       return ok;
@@ -349,9 +355,9 @@ struct Rows8 : Rows<D, 1, NQ, true> {
   }
 };
 
-template <int D, int NQ, int NW>
+template <int D, int NQ, int NW, bool ONCE>
 __global__ __launch_bounds__(NW * 64, NW > kWaves ? 2 : kv8_rows_waves(D, NQ)) void kv8_rows_kernel(Kv8Attn a) {
-  using R = Rows8<D, NQ, NW>;
+  using R = Rows8<D, NQ, NW, ONCE>;
   __shared__ __attribute__((aligned(16))) uint8_t smem[R::kSmem];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -414,30 +420,31 @@ __global__ __launch_bounds__(NW * 64, NW > kWaves ? 2 : kv8_rows_waves(D, NQ)) v
 // compute unit); 128 keys 7.2 : 6.7.
 constexpr int64_t kLds = 160 * 1024;
 template <int D, int NQ>
-constexpr bool kWide = Rows8<D, NQ, 2 * kWaves>::kSmem <= kLds && D * NQ <= 128;
+constexpr bool kWide = Rows8<D, NQ, 2 * kWaves, true>::kSmem <= kLds && D * NQ <= 128;
 
-template <int D, int NQ>
-hipError_t launch_rows(const Kv8Attn& a, const Kv4Plan& p, hipStream_t s) {
+template <int D, int NQ, bool ONCE>
+hipError_t launch_rows(const Kv8Attn& a, const Kv8Plan& p, hipStream_t s) {
   const int64_t n = p.split ? a.workers : (int64_t)p.grid_q * a.c.hkv * a.batch;
   if constexpr (kWide<D, NQ>) {
-    if (!p.split && n * Rows8<D, NQ, 2 * kWaves>::kSmem <= (int64_t)num_cus() * kLds) {
-      hipLaunchKernelGGL((kv8_rows_kernel<D, NQ, 2 * kWaves>), dim3((unsigned)n), dim3(2 * kWaves * 64), 0, s, a);
+    if (!p.split && n * Rows8<D, NQ, 2 * kWaves, ONCE>::kSmem <= (int64_t)num_cus() * kLds) {
+      hipLaunchKernelGGL((kv8_rows_kernel<D, NQ, 2 * kWaves, ONCE>), dim3((unsigned)n), dim3(2 * kWaves * 64), 0, s, a);
       return hipGetLastError();
     }
   }
-  hipLaunchKernelGGL((kv8_rows_kernel<D, NQ, kWaves>), dim3((unsigned)n), dim3(kWaves * 64), 0, s, a);
+  hipLaunchKernelGGL((kv8_rows_kernel<D, NQ, kWaves, ONCE>), dim3((unsigned)n), dim3(kWaves * 64), 0, s, a);
   if (hipError_t e = hipGetLastError()) return e;
   return p.split ? launch_join<D, 16 * NQ, 256 / (D / 4)>(a, p.tile_rows, s) : hipSuccess;
 }
 
 template <int D>
-hipError_t launch_rows_d(const Kv8Attn& a, const Kv4Plan& p, hipStream_t s) {
-  return p.nq == 1 ? launch_rows<D, 1>(a, p, s) : launch_rows<D, 2>(a, p, s);
+hipError_t launch_rows_d(const Kv8Attn& a, const Kv8Plan& p, hipStream_t s) {
+  if (p.once) return p.nq == 1 ? launch_rows<D, 1, true>(a, p, s) : launch_rows<D, 2, true>(a, p, s);
+  return p.nq == 1 ? launch_rows<D, 1, false>(a, p, s) : launch_rows<D, 2, false>(a, p, s);
 }
 
 }  // namespace kv8
 
-hipError_t launch_kv8_rows(const Kv8Attn& a, const Kv4Plan& p, hipStream_t s) {
+hipError_t launch_kv8_rows(const Kv8Attn& a, const Kv8Plan& p, hipStream_t s) {
   switch (a.c.d) {
     case 64: return kv8::launch_rows_d<64>(a, p, s);
     case 96: return kv8::launch_rows_d<96>(a, p, s);
