@@ -18,6 +18,7 @@ namespace {
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
@@ -219,7 +220,8 @@ __device__ __forceinline__ void write_keys(const Kv8Append& a, const Part& p, in
 
 // Values are loaded as they lie, 8 channels of a token per lane (loads of 4 bytes in the
 // order of the codes took 7 us more for 16 K tokens): D / 8 lanes hold a token, 96 channels
-// 12 of 16.  Register j of a lane holds the j-th of its tokens.
+// 12 of 16.  Register j of a lane holds the j-th of its tokens.  They pass the caches by, which
+// leaves room for the keys, that bounds are made of too (16 K tokens 34 us, so 32).
 template <int D>
 struct Load {
   static constexpr int P = D == 96 ? 16 : D / 8;   // lanes of a token
@@ -234,7 +236,8 @@ __device__ __forceinline__ void load_values(const Kv8Append& a, const Part& p, i
   for (int j = 0; j < L::N; ++j) {
     const int tok = L::R * j + lane / L::P;
     const bool fresh = tok >= p.a && tok < p.e && c < D / 8;
-    const uint4 v = fresh ? *(const uint4*)(row + (p.t + (tok - p.a)) * a.v_ts) : make_uint4(0, 0, 0, 0);
+    u32x4 v = {0, 0, 0, 0};
+    if (fresh) v = __builtin_nontemporal_load((const u32x4*)(row + (p.t + (tok - p.a)) * a.v_ts));
     raw[4 * j] = v.x; raw[4 * j + 1] = v.y; raw[4 * j + 2] = v.z; raw[4 * j + 3] = v.w;
   }
 }
