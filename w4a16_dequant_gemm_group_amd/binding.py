@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -118,6 +119,30 @@ class GqKv8SelectArgs(ctypes.Structure):
                 ("lens", ctypes.c_void_p)]
 
 
+def _packer(args):
+    """A function that packs the fields of an argument structure, nested ones in place, as the C
+    ABI lays them out: the bytes are made in 0.4 us, the structure in 1.7."""
+    codes = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f"}
+
+    def fields(s):
+        return "".join(codes[t] if t in codes else fields(t) for _, t in s._fields_)
+
+    layout = struct.Struct("@" + fields(args) + "0q")
+    assert layout.size == ctypes.sizeof(args), args.__name__
+    pack = layout.pack
+
+    def packed(*values):
+        try:
+            return pack(*values)
+        except (struct.error, OverflowError, TypeError) as e:
+            raise ValueError(f"an argument of the call does not fit its type: {e}") from None
+    return packed
+
+
+_rope_args, _kv8_append_args = _packer(GqRopeArgs), _packer(GqKv8AppendArgs)
+_kv8_attention_args, _kv8_select_args = _packer(GqKv8AttentionArgs), _packer(GqKv8SelectArgs)
+
+
 class GqError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -171,14 +196,14 @@ def lib() -> ctypes.CDLL:
         "gq_kv4_attention": [ctypes.POINTER(GqKv4AttentionArgs), p, sz, p],
         "gq_rope_frequencies": [i64, ctypes.c_double, GqRopeScaling, ctypes.POINTER(ctypes.c_double),
                                 ctypes.POINTER(ctypes.c_double)],
-        "gq_rope": [ctypes.POINTER(GqRopeArgs), p],
+        "gq_rope": [p, p],     # here and below: a structure by reference, or its bytes
         "gq_kv8_cache_bytes": [i64, GqKv8Layout, ctypes.POINTER(sz)],
-        "gq_kv8_append": [ctypes.POINTER(GqKv8AppendArgs), p],
+        "gq_kv8_append": [p, p],
         "gq_kv8_read": [p, i64, GqKv8Layout, p, i64, p, p, c, p],
-        "gq_kv8_attention_workspace_size": [ctypes.POINTER(GqKv8AttentionArgs), ctypes.POINTER(sz)],
-        "gq_kv8_attention": [ctypes.POINTER(GqKv8AttentionArgs), p, sz, p],
-        "gq_kv8_select_workspace_size": [ctypes.POINTER(GqKv8SelectArgs), ctypes.POINTER(sz)],
-        "gq_kv8_select": [ctypes.POINTER(GqKv8SelectArgs), p, sz, p],
+        "gq_kv8_attention_workspace_size": [p, ctypes.POINTER(sz)],
+        "gq_kv8_attention": [p, p, sz, p],
+        "gq_kv8_select_workspace_size": [p, ctypes.POINTER(sz)],
+        "gq_kv8_select": [p, p, sz, p],
         "gq_stream_read": [p, i64, p, p],
         "gq_probe_mfma_valu": [i32, i32, i32, p, p, p],
         "gq_probe_lds_read": [i32, i32, i32, p, p, p],
@@ -939,9 +964,9 @@ def gq_rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, inter
     if out is None:
         out = _new(x, shape, x.dtype, stream)
         ots, ohs = H * D, D
-    a = GqRopeArgs(x.data_ptr(), xts, xhs, out.data_ptr(), ots, ohs, _DT[x.dtype], T, H, D, rot,
+    a = _rope_args(x.data_ptr(), xts, xhs, out.data_ptr(), ots, ohs, _DT[x.dtype], T, H, D, rot,
                    positions.data_ptr(), freqs.data_ptr(), amplitude, bool(interleaved), bool(inverse))
-    _ok(lib().gq_rope(ctypes.byref(a), handle), "gq_rope")
+    _ok(lib().gq_rope(a, handle), "gq_rope")
     return out
 
 
@@ -1034,10 +1059,10 @@ def gq_kv8_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_ta
     if handle is None:
         with torch.cuda.device(k.device):
             return gq_kv8_append(k, v, cache, page_table, kv_lens, starts, bounds, stream)
-    a = GqKv8AppendArgs(k.data_ptr(), kts, khs, v.data_ptr(), vts, vhs, _DT[k.dtype], T, cache.data_ptr(),
-                        n_pages, lay, page_table.data_ptr(), nb, page_table.shape[1], kv_lens.data_ptr(),
-                        _ptr(starts), _ptr(bounds))
-    _ok(lib().gq_kv8_append(ctypes.byref(a), handle), "gq_kv8_append")
+    a = _kv8_append_args(k.data_ptr(), kts, khs, v.data_ptr(), vts, vhs, _DT[k.dtype], T, cache.data_ptr(), n_pages,
+                         H, D, lay.page_size, page_table.data_ptr(), nb, page_table.shape[1], kv_lens.data_ptr(),
+                         _ptr(starts) or 0, _ptr(bounds) or 0)
+    _ok(lib().gq_kv8_append(a, handle), "gq_kv8_append")
 
 
 def gq_kv8_read(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, out_dtype=torch.bfloat16, k=None, v=None,
@@ -1111,14 +1136,14 @@ def gq_kv8_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
         out = _new(q, shape, q.dtype, stream)
     if lse is None and return_lse:
         lse = _new(q, (T, HQ), torch.float32, stream)
-    a = GqKv8AttentionArgs(
-        q.data_ptr(), qts, qhs, T, HQ, _DT[q.dtype], cache.data_ptr(), cache.shape[0], lay,
-        page_table.data_ptr(), nb, table_pages, heads, kv_lens.data_ptr(), _ptr(q_starts), max_q_len,
-        max_kv_len, bool(causal), window, D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse))
-    ref, size, L = ctypes.byref(a), ctypes.c_size_t(), lib()
-    _ok(L.gq_kv8_attention_workspace_size(ref, ctypes.byref(size)), "gq_kv8_attention_workspace_size")
+    a = _kv8_attention_args(
+        q.data_ptr(), qts, qhs, T, HQ, _DT[q.dtype], cache.data_ptr(), cache.shape[0], lay.kv_heads, D, lay.page_size,
+        page_table.data_ptr(), nb, table_pages, heads, kv_lens.data_ptr(), _ptr(q_starts) or 0, max_q_len,
+        max_kv_len, bool(causal), window, D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse) or 0)
+    size, L = ctypes.c_size_t(), lib()
+    _ok(L.gq_kv8_attention_workspace_size(a, ctypes.byref(size)), "gq_kv8_attention_workspace_size")
     ws = _scratch(size.value, workspace, q, stream)
-    _ok(L.gq_kv8_attention(ref, _ptr(ws), 0 if ws is None else ws.numel(), handle), "gq_kv8_attention")
+    _ok(L.gq_kv8_attention(a, _ptr(ws), 0 if ws is None else ws.numel(), handle), "gq_kv8_attention")
     return (out, lse) if return_lse else out
 
 
@@ -1163,11 +1188,11 @@ def gq_kv8_select(q: torch.Tensor, bounds: torch.Tensor, page_table: torch.Tenso
         pages = _new(q, (T, H, keep), torch.int32, stream)
     if lens is None:
         lens = _new(q, (T,), torch.int32, stream)
-    a = GqKv8SelectArgs(q.data_ptr(), qts, qhs, T, HQ, _DT[q.dtype], bounds.data_ptr(), n_pages,
-                        GqKv8Layout(H, D, page_size), page_table.data_ptr(), nb, table_pages, kv_lens.data_ptr(),
-                        _ptr(q_starts), max_kv_len, keep, first, last, pages.data_ptr(), lens.data_ptr())
-    ref, size, L = ctypes.byref(a), ctypes.c_size_t(), lib()
-    _ok(L.gq_kv8_select_workspace_size(ref, ctypes.byref(size)), "gq_kv8_select_workspace_size")
+    a = _kv8_select_args(q.data_ptr(), qts, qhs, T, HQ, _DT[q.dtype], bounds.data_ptr(), n_pages, H, D, page_size,
+                         page_table.data_ptr(), nb, table_pages, kv_lens.data_ptr(), _ptr(q_starts) or 0, max_kv_len,
+                         keep, first, last, pages.data_ptr(), lens.data_ptr())
+    size, L = ctypes.c_size_t(), lib()
+    _ok(L.gq_kv8_select_workspace_size(a, ctypes.byref(size)), "gq_kv8_select_workspace_size")
     ws = _scratch(size.value, workspace, q, stream)
-    _ok(L.gq_kv8_select(ref, _ptr(ws), 0 if ws is None else ws.numel(), handle), "gq_kv8_select")
+    _ok(L.gq_kv8_select(a, _ptr(ws), 0 if ws is None else ws.numel(), handle), "gq_kv8_select")
     return pages, lens
