@@ -850,8 +850,8 @@ def gq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
 # ---------------------------------------------------------------------------
 
 # Small calls cost the host more than the GPU: the checks below look at every attribute
-# once and leave it to _need and _on_device to say what is wrong.  (A rotation of one
-# token 9.2 us with _need throughout, 3.4 of them the launch.)
+# once and leave it to _need and _on_device to say what is wrong.  (Of the 9 us of a rotation of
+# one token 3.4 are the launch.)
 
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 

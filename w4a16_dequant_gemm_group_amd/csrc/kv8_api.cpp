@@ -14,7 +14,8 @@ bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 // What a row tile costs besides its keys, in tiles of keys: a prompt of 4096 at 128 channels
 // with 2 / 3 / 4 / 5 / 6 / 8 213 / 205 / 196 / 191 / 192 / 194 us, at 256 151 / 137 / 137 / 136 / 139 / 142,
-// chunks of 1010 tokens there 57 / 55 / 55 / 59 / 58 / 58.
+// chunks of 1010 tokens there 57 / 55 / 55 / 59 / 58 / 58, before row tiles were dealt in turn and
+// their ends became cheaper; 3 to 6 are within 2 % of each other since.
 constexpr int overhead(int d, bool tile) { return !tile ? 2 : d > 128 ? 3 : 5; }
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 constexpr int64_t kMaxBatch = 1 << 24;
@@ -133,9 +134,9 @@ Kv8Plan kv8_plan(const gq_kv8_attention_args& a) {
   const int64_t tiles = segs * (over + ((a.max_kv_len + (1 << p.grain) - 1) >> p.grain));
   // One workgroup per row tile, without the second kernel, as long as that is faster than
   // the split, which spreads few row tiles over the card.  Equal lengths, one against split, us:
-  //   8 row tiles of 128 channels, 512 / 768 keys 9.8 : 10.7 / 11.2 : 10.7; 160, 2048 keys 22.5 : 25.7
-  //   4 of 64, 768 / 2048 keys 9.0 : 10.0 / 14.8 : 10.4; 80, 2048 keys 15.2 : 16.3
-  //   8 of 256, 256 / 512 keys 11.9 : 13.9 / 16.1 : 14.2; 128, 1024 / 2048 keys 26.9 : 27.5 / 42 : 37
+  //   8 row tiles of 128 channels, 512 / 768 keys 9.4 : 11.2 / 10.9 : 11.1; 160, 2048 keys 22.0 : 25.7
+  //   4 of 64, 768 / 2048 keys 8.9 : 11.1 / 14.6 : 11.7; 80, 2048 keys 15.3 : 16.6
+  //   2 of 256, 256 / 512 keys 11.1 : 13.5 / 15.3 : 13.8; 128, 1024 / 2048 keys 26.2 : 27.3 / 41 : 36
   // Of more row tiles it would be faster for longer (512 of 128 channels: 4096 keys), but one
   // long sequence among short ones runs alone then.
   const int64_t alone = d == 64 ? 960 + 14 * segs : d == 256 ? 360 + 7 * segs : 600 + 8 * segs;

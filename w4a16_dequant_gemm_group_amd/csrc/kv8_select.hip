@@ -5,9 +5,9 @@
 // factors) in binary64: whatever the order of its terms, it is off by 2^-52 or so, and the
 // choice is the one that the formula makes.
 // sum_d max(q_d min_d, q_d max_d) = sum_d q_d (q_d > 0 ? max_d : min_d).
-// Bound by latency: 2048 pages of 8 heads of 128 are scored in 6.6 us (8.4 MB) and chosen in 7;
-// 40 queries over 16 sequences of up to 1000 pages, 4 heads of 64, in 12.6 (vector work, 60 %
-// busy) and 6.8.
+// Bound by latency: 2048 pages of 8 heads of 128 are scored in 6.6 us (8.4 MB) and chosen in 5.9;
+// 40 queries over 16 sequences of up to 1000 pages, 4 heads of 64, in 12.7 (vector work, 60 %
+// busy) and 5.8.
 #include "kv8.h"
 #include "kv8_seq.h"
 

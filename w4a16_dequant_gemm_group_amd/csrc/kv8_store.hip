@@ -6,9 +6,9 @@
 // block among them (the first of its sequence, or one at a multiple of 16).  Lanes hold
 // the channels in the order of the codes (kv8.h): loads of 16 bytes, those of values change
 // places in LDS, codes leave in pieces of 16 bytes that make one run.
-// 16 K tokens of 8 heads of 128: 34 us (98 MB read, the keys once more for their bounds, and
-// 34 MB written: 3.9 TB/s; bound by loads in flight), without bounds 25; read back in 18.5
-// (101 MB).  One token 4.6.
+// 16 K tokens of 8 heads of 128: 32 us (98 MB read, the keys once more for their bounds, and
+// 34 MB written: 4.1 TB/s; bound by loads in flight), without bounds and with the inputs in
+// cache 23.5; read back in 18.4 (101 MB).  One token 4.6.
 #include "kv8.h"
 #include "kv8_seq.h"
 #include "stream_util.h"

@@ -6,8 +6,8 @@
 // 16 keys, so both products take one part each: the keys' scale is a factor of 16 scores
 // at once, the values' goes into the exponent of the weights.
 // Bound by vector work beside the products (57 and 44 % busy): a prompt of 4096 with 32 heads of
-// 128 on 8 150 us (916 TFLOP/s), 512 queries behind 32 K keys 302 (904).  A key tile costs 1.8 /
-// 2.1 / 2.35 us at 64 / 96 / 128 channels, a row tile taken up about five of them.
+// 128 on 8 150 us (916 TFLOP/s), 512 queries behind 32 K keys 284 to 294 (960 to 926).  A key tile
+// costs 1.7 / 1.95 / 2.25 us at 64 / 96 / 128 channels, a row tile taken up about five of them.
 #include "kv8.h"
 #include "kv4_tile.h"
 #include <type_traits>
