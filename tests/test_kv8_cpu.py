@@ -213,3 +213,26 @@ def test_definition_of_blocks():
     # blocks begin at multiples of 16, and zeros have the least scale
     z = U.Blocks(1).append(torch.zeros(17, 1))
     assert z.scales == [U.LEAST, U.LEAST] and z.codes.shape == (17, 1)
+
+
+@pytest.mark.parametrize("args,pack", [
+    (B.GqRopeArgs, B._rope_args), (B.GqKv8AppendArgs, B._kv8_append_args),
+    (B.GqKv8AttentionArgs, B._kv8_attention_args), (B.GqKv8SelectArgs, B._kv8_select_args)])
+def test_packed_arguments_are_the_structure(args, pack):
+    """Every field in its place, and a value that does not fit its field is refused, not cut."""
+    flat, whole, n = [], [], 0
+    for _, t in args._fields_:
+        if t is B.GqKv8Layout:
+            flat += [n + 1, n + 2, n + 3]
+            whole.append(B.GqKv8Layout(n + 1, n + 2, n + 3))
+            n += 3
+        else:
+            n += 1
+            v = n + 0.5 if t is ctypes.c_float else n
+            flat.append(v)
+            whole.append(v)
+    assert pack(*flat) == bytes(args(*whole))
+    for bad in (1 << 200, None, "x", -(1 << 200)):      # beyond fp32 too
+        for i in range(len(flat)):
+            with pytest.raises(ValueError):
+                pack(*flat[:i], bad, *flat[i + 1:])
