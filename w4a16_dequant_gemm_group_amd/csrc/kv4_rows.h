@@ -34,6 +34,30 @@ constexpr float kRoom = 11.0f, kSlack = 4.0f;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// A sum of weights l that follows its reference from `from` up to `to`, f = 2^(from - to): the
+// product of what this returns.  References that hold scales which lie up to 2^161 apart (the
+// 8-bit cache's) can move so far that f is below fp32, and l f still worth keeping.  Then whole
+// and broken powers of two are taken apart, which also keeps the bits that from - to would lose.
+struct Moved {
+  float l, f;
+};
+
+__device__ __forceinline__ bool moves_far(float from, float to) {
+  return from - to < -100.0f && from - to > -300.0f;   // beyond it nothing is left
+}
+
+__device__ __forceinline__ Moved move_sum(float l, float from, float to, float f) {
+  if (!moves_far(from, to)) return Moved{l, f};
+  const float u = __builtin_rintf(from), v = __builtin_rintf(to);
+  return Moved{__builtin_ldexpf(l * exp2_hw((from - u) - (to - v)), (int)(u - v)), 1.0f};
+}
+
+// The same, done.
+__device__ __forceinline__ float sum_at(float l, float from, float to) {
+  const Moved m = move_sum(l, from, to, exp2_hw(from - to));
+  return m.l * m.f;
+}
+
 struct Seq {
   int q0, n, kv;   // first query row of q, queries, keys
 };
@@ -995,13 +1019,14 @@ __global__ __launch_bounds__(kWaves * 64, kv4_rows_waves(D, NG, NQ)) void kv4_ro
 // its last row tile open: the workers after it, up to `last`, hold the rest.
 // One workgroup per worker and RW rows at a time: D / 4 threads hold a row, PG
 // such sets take every PG-th partial of it (many partials of few rows for
-// single tokens, few of many rows for prompts).
-template <int D, int TQ, int PG>
+// single tokens, few of many rows for prompts).  FAR: where references
+// lie far apart the sum of weights is made once more at the end, by move_sum.
+template <int D, int TQ, int PG, bool FAR>
 __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
   constexpr int QD = D / 4, RW = 256 / (QD * PG);
   constexpr int64_t kSlot = TQ * (D + 2);
   __shared__ float4 so[RW][PG][QD];
-  __shared__ float sm[RW][PG], sl[RW][PG];
+  __shared__ float sm[RW][PG], sl[RW][PG], sn[FAR ? RW : 1][PG];
   const int w = blockIdx.x;
   const int4* mt = (const int4*)(a.meta + (int64_t)w * kMetaInts);
   const int4 open = mt[0], seq = mt[1];
@@ -1014,7 +1039,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
   for (int r0 = blockIdx.y * RW; r0 < rows; r0 += gridDim.y * RW) {
     const int ri = r0 + rw;      // row within the tile
     const bool mine = rw < RW && ri < rows;
-    float M = kNegInf, L = 0.0f;
+    float M = kNegInf, L = 0.0f, low = -kNegInf;   // low: the lowest reference that has a sum
     float4 acc = make_float4(0, 0, 0, 0);
     if (mine) {
       auto add = [&](int c) {
@@ -1025,8 +1050,9 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
         const float f0 = M == kNegInf ? 0.0f : exp2_hw(M - mn);
         // NaN statistics (a non-finite query) come with reference -inf: kept
         const float f1 = mc == kNegInf ? 0.0f : exp2_hw(mc - mn);
+        if constexpr (FAR) low = lc == 0.0f ? low : fminf(low, mc);
         M = mn;
-        L = L * f0 + lc * f1;
+        L = __builtin_fmaf(L, f0, lc * f1);
         acc.x = acc.x * f0 + v.x * f1;
         acc.y = acc.y * f0 + v.y * f1;
         acc.z = acc.z * f0 + v.z * f1;
@@ -1038,7 +1064,11 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
     if constexpr (PG > 1) {
       if (mine) {
         so[rw][pg][qd] = acc;
-        if (qd == 0) { sm[rw][pg] = M; sl[rw][pg] = L; }
+        if (qd == 0) {
+          sm[rw][pg] = M;
+          sl[rw][pg] = L;
+          if constexpr (FAR) sn[rw][pg] = low;
+        }
       }
       __syncthreads();
       if (mine && pg == 0) {
@@ -1051,6 +1081,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
         for (int i = 0; i < PG; ++i) {
           const float f = sm[rw][i] == kNegInf ? 0.0f : exp2_hw(sm[rw][i] - M);
           const float4 v = so[rw][i][qd];
+          if constexpr (FAR) low = fminf(low, sn[rw][i]);
           L += f * sl[rw][i];
           acc.x += f * v.x;
           acc.y += f * v.y;
@@ -1061,6 +1092,16 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
       __syncthreads();
     }
     if (mine && pg == 0) {
+      if constexpr (FAR) {
+        if (low - M < -100.0f) {
+          L = 0.0f;
+#pragma unroll 1
+          for (int c = w; c <= last; ++c) {
+            const float* p = a.part + (2 * (int64_t)c + (c == w ? 1 : 0)) * kSlot + TQ * D + ri;
+            L += sum_at(p[TQ], p[0], M);
+          }
+        }
+      }
       using R = Rows<D, 1, 1, true>;
       const float inv = L == 0.0f ? 0.0f : 1.0f / L;
       const int row = qt * TQ + ri;
@@ -1072,10 +1113,10 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Attn a) {
   }
 }
 
-template <int D, int TQ, int PG>
+template <int D, int TQ, int PG, bool FAR = false>
 hipError_t launch_join(const Kv4Attn& a, int rows, hipStream_t s) {
   constexpr int RW = 256 / (D / 4 * PG);
-  hipLaunchKernelGGL((kv4_join_kernel<D, TQ, PG>), dim3(a.workers, (rows + RW - 1) / RW), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((kv4_join_kernel<D, TQ, PG, FAR>), dim3(a.workers, (rows + RW - 1) / RW), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -67,7 +67,8 @@ struct Kv8Attn : Kv4Attn {
 // A weight p without its value scale S_V of 2^-40 .. 2^121 spans more than fp32 does where
 // p S_V has to be near 2^11.  So the sums hold p 2^40: at most 2^95, at least 2^-70 for the
 // heaviest key, with room for those far lighter; the results, which hold p S_V, get the
-// factor when they are done, and the reference of both is 40 less.
+// factor when they are done, and the reference of both is 40 less.  A reference that rises from
+// the smallest scale to the largest moves by more than fp32 holds: the sums follow it by move_sum.
 constexpr float kKv8Shift = 40.0f, kKv8Up = 0x1p40f, kKv8Down = 0x1p-40f;
 
 // Factor of the scores of a block: what a row's queries and the block's keys were divided

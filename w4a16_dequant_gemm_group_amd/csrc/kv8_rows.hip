@@ -132,8 +132,9 @@ struct Rows8 : Rows<D, 1, NQ, true> {
         top = fmaxf(top, __shfl_xor(top, 32));
         const float mn = fmaxf(top, mref[nq]);
         const float c = mn == mref[nq] ? 1.0f : exp2_hw(mref[nq] - mn);
+        const Moved lm = move_sum(l[nq], mref[nq], mn, c);
         mref[nq] = mn;
-        l[nq] *= c;
+        l[nq] = lm.l * lm.f;
 #pragma unroll
         for (int i = 0; i < 2 * NS; ++i) o[nq][i] *= c;
       }
@@ -245,7 +246,8 @@ struct Rows8 : Rows<D, 1, NQ, true> {
         for (int w = 0; w < NW; ++w) {
           const float mw = sm[w * 16 + rr];
           const float f = mw == kNegInf ? 0.0f : exp2_hw(mw - M);
-          L = __builtin_fmaf(f, sl[w * 16 + rr], L);
+          const Moved lm = move_sum(sl[w * 16 + rr], mw, M, f);
+          L = __builtin_fmaf(lm.f, lm.l, L);
 #pragma unroll
           for (int i = 0; i < C; ++i) acc[i] = __builtin_fmaf(f, so[(w * 16 + rr) * kRow + c0 + i], acc[i]);
         }
@@ -433,7 +435,7 @@ hipError_t launch_rows(const Kv8Attn& a, const Kv8Plan& p, hipStream_t s) {
   }
   hipLaunchKernelGGL((kv8_rows_kernel<D, NQ, kWaves, ONCE>), dim3((unsigned)n), dim3(kWaves * 64), 0, s, a);
   if (hipError_t e = hipGetLastError()) return e;
-  return p.split ? launch_join<D, 16 * NQ, 256 / (D / 4)>(a, p.tile_rows, s) : hipSuccess;
+  return p.split ? launch_join<D, 16 * NQ, 256 / (D / 4), true>(a, p.tile_rows, s) : hipSuccess;
 }
 
 template <int D>

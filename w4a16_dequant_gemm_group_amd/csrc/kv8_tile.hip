@@ -268,8 +268,11 @@ struct Tile8 : Tile<D, 1, true, false, false> {
       top = fmaxf(top, __shfl_xor(top, 32)) - kTileRoom;
       const float mn = fmaxf(top, mref);
       const float f = mn == mref ? 1.0f : exp2_hw(mref - mn);
+      if (__builtin_expect(__any(moves_far(mref, mn)), 0))
+        l = sum_at(l, mref, mn);
+      else
+        l *= f;
       mref = mn;
-      l *= f;
 #pragma unroll
       for (int d = 0; d < NS; ++d)
 #pragma unroll
@@ -436,7 +439,7 @@ hipError_t launch_tile_d(const Kv8Attn& a, const Kv4Plan& p, hipStream_t s) {
   if (hipError_t e = hipGetLastError()) return e;
   // Workgroups for 64 rows of a row tile go over all of them: where nothing was split, which a
   // causal prompt's order often brings about, four times as many took 1 us more to start and end.
-  return launch_join<D, T::TQ, 1>(a, p.tile_rows < 64 ? p.tile_rows : 64, s);
+  return launch_join<D, T::TQ, 1, true>(a, p.tile_rows < 64 ? p.tile_rows : 64, s);
 }
 
 }  // namespace kv8
