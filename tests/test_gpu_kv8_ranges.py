@@ -55,3 +55,21 @@ def test_many_sequences_of_zeros_and_large_values():
         v[kv * i:kv * i + 32 * i] = 0
     q = torch.randn(20 * n, 2, d, generator=g)
     Case(2, 1, d, 16, "bf16", [20] * n, [kv] * n, k=torch.zeros(kv * n, 1, d), v=v, q=q).check()
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("q_len", [1, 10, 20])
+@pytest.mark.parametrize("low,high", [(-84, 84), (-90, 90), (-118, 116), (112, -30)])
+def test_small_queries_and_large_keys(low, high, q_len, d):
+    """Scores of ordinary size out of factors at the ends of the range, rows of zeros among them."""
+    kv = 200
+    g = torch.Generator().manual_seed(4)
+    k, v = torch.randn(kv, 1, d, generator=g) * 2.0 ** high, torch.randn(kv, 1, d, generator=g)
+    q = torch.randn(q_len, 4, d, generator=g) * 2.0 ** low
+    scale = d ** -0.5 * 2.0 ** -(low + high)
+    for zero in (False, True):
+        if zero:
+            q[:, 1] = 0
+        c = Case(4, 1, d, 16, "bf16", [q_len], [kv], k=k, v=v, q=q)
+        c.check(scale=scale)
+        c.check(scale=scale, window=20)

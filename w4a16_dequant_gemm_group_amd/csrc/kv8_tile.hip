@@ -133,7 +133,7 @@ struct Tile8 : Tile<D, 1, true, false, false> {
     e = e < -112 ? -112 : (e > 127 ? 127 : e);   // 128: infinite or NaN
     const float f = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
     A = a.scale_log2 * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
-    A = fmaxf(A, 0x1p-100f);   // see Base::load_q
+    if (mx == 0.0f) A = 1.0f;   // all scores are 0
 #pragma unroll
     for (int st = 0; st < D / 16; ++st) {
       float x[8];
@@ -144,7 +144,9 @@ struct Tile8 : Tile<D, 1, true, false, false> {
     // A finite reference below all scores and a scale below all: nothing has to be told apart.
     mref = -0x1.fffffep127f;
     ltop = -100.0f;
-    steep = __any(!(A < 0x1p6f));   // times a scale of 2^121 beyond fp32
+    // times a scale of 2^121 beyond fp32, or times one of 2^-40 near 0, which makes NaN of a
+    // hidden key's -inf
+    steep = __any(!(A >= 0x1p-80f && A < 0x1p6f));
     l = 0.0f;
 #pragma unroll
     for (int d = 0; d < NS; ++d)
