@@ -130,10 +130,12 @@ gq_status gq_kv8_read(const uint8_t* cache, int64_t n_pages, gq_kv8_layout layou
  * Scores, softmax statistics and outputs are kept in fp32.  The matrix cores take codes
  * exactly and queries as fp16 times a power of two per row (elements below 2^-29 of a
  * row's largest have fewer bits); weights times value scales are rounded to fp16 once
- * (2^-11; for fp16 results of at most 8 rows per key/value head not at all), those below
- * 2^-22 of a row's largest have fewer bits, below 2^-33 none.  scale times the largest |q|
- * of a row, and that times the largest |k| that it sees, have to lie in fp32's range (scores
- * of 0 are right beyond it too); the first has fewer bits below 2^-120. */
+ * (2^-11), those below 2^-22 of a row's largest have fewer bits, below 2^-33 none.  What that
+ * leaves is carried along (2^-22 remains) for fp16 results of a sequence of at most 8 rows
+ * (queries times query heads per key/value head) in a call whose max_q_len makes at most 16;
+ * with a larger max_q_len it is not.  scale times the largest |q| of a row, and that times the
+ * largest |k| that it sees, have to lie in fp32's range (scores of 0 are right beyond it
+ * too); the first has fewer bits below 2^-120. */
 typedef struct {
   const void* q;
   int64_t q_token_stride, q_head_stride;

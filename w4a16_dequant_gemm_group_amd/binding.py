@@ -1102,7 +1102,9 @@ def gq_kv8_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Ten
     """Attention of q [tokens, q_heads, head_dim] (bf16 or fp16) over the 8-bit cache, as
     gq_kv4_attention over the 4-bit one.  page_table [batch, pages], or [batch, kv_heads,
     pages] with pages of each key/value head's own: what gq_kv8_select returns, together
-    with its lengths, makes the attention over the pages it chose."""
+    with its lengths, makes the attention over the pages it chose.  With q_starts a tight
+    max_q_len (default: all tokens) chooses the kernel, and with it whether fp16 results of a
+    few rows keep all bits of the weights (see the header)."""
     qts, qhs = _rows16(q, "q", (torch.bfloat16, torch.float16))
     T, HQ, D = q.shape
     lay = _kv8_cache(cache, D)
