@@ -69,8 +69,9 @@ gq_status gq_rope_frequencies(int64_t rot_dim, double base, gq_rope_scaling scal
  * angle); sines, products and sums are fp32, rounded once to dtype (nearest-even).
  * Errors: INVALID_ARG (tokens < 0 or > 2^30, heads < 0 or > 65536, head_dim odd or
  * outside 2 .. 1024, rot_dim odd or outside 2 .. head_dim, strides beyond 2^40,
- * amplitude not finite, x == out with other strides, out's strides below head_dim, NULL), MISALIGNED (x, out to their
- * elements, positions and freqs to 8 bytes), UNSUPPORTED (device). */
+ * amplitude not finite, x == out with other strides, rows of out that overlap each
+ * other, NULL), MISALIGNED (x, out to their elements, positions and freqs to 8 bytes),
+ * UNSUPPORTED (device).  Other overlaps of x and out are the caller's to avoid. */
 typedef struct {
   const void* x;
   int64_t x_token_stride, x_head_stride;

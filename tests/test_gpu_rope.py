@@ -145,3 +145,20 @@ def test_special_values_empty_stream_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, B.gq_rope(x, pos, f))
+
+
+@pytest.mark.parametrize("tokens,heads,ts,hs", [(9, 5, 64, 9 * 64), (2, 3, 48 * 8, 32 * 8), (4, 4, 55 * 8, 22 * 8)])
+def test_layouts_of_out(tokens, heads, ts, hs):
+    """Rows of out apart from each other in orders other than tokens of heads."""
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(tokens, heads, 64, generator=g).bfloat16().to(device())
+    pos, f = torch.arange(tokens, device=device()), freqs(64)
+    size = (tokens - 1) * ts + (heads - 1) * hs + 64
+    memory = torch.full((size + 64,), 7.0, dtype=torch.bfloat16, device=device())
+    out = memory.as_strided((tokens, heads, 64), (ts, hs, 1))
+    B.gq_rope(x, pos, f, out=out)
+    assert torch.equal(out, B.gq_rope(x, pos, f))
+    assert int((memory == 7).sum()) >= memory.numel() - x.numel() and bool((memory[size:] == 7).all())
+    for strides in ((64, 64), (128, 64)):
+        with pytest.raises(B.GqError):
+            B.gq_rope(x, pos, f, out=memory.as_strided((tokens, heads, 64), strides + (1,)))

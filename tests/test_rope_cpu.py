@@ -116,6 +116,27 @@ def test_refusals():
     assert L.gq_rope(args(heads=0, x=None, out=None), None) == B.GQ_OK
 
 
+@pytest.mark.parametrize("tokens,heads,d,ts,hs", [
+    (2, 2, 128, 128, 128), (3, 8, 128, 128, 128), (3, 8, 128, 256, 128), (3, 8, 128, 1023, 128), (8, 3, 128, 128, 1023),
+    (3, 8, 128, 896, 128), (2, 9, 64, 512, 64), (2, 2, 128, 128, -128), (3, 8, 128, -1000, 128), (9, 3, 2, 2, 16),
+    (4, 4, 10, 35, 24), (1 << 30, 65536, 2, (1 << 17) - 1, 2), (1 << 30, 65536, 2, 1 << 40, (1 << 40) - 1),
+    (1 << 30, 65536, 2, 4, 65536 * 4 + 1)])
+def test_rows_of_out_that_overlap(tokens, heads, d, ts, hs):
+    a = dict(tokens=tokens, heads=heads, head_dim=d, rot_dim=d, out_token_stride=ts, out_head_stride=hs)
+    assert B.lib().gq_rope(args(**a, positions=FAKE + 4), None) == B.GQ_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("tokens,heads,d,ts,hs", [
+    (3, 8, 128, 1024, 128), (3, 8, 128, 128, 384), (3, 8, 128, -1024, -128), (1, 8, 128, 0, 128), (3, 1, 128, 128, 0),
+    (2, 2, 128, 384, 256), (2, 2, 128, 256, 384), (4, 4, 10, 55, 22), (2, 3, 10, 36, 24), (1 << 30, 65536, 2, 1 << 17, 2),
+    (1 << 30, 256, 2, 2, 1 << 31), (1 << 30, 65536, 2, 1 << 40, 2)])
+def test_rows_of_out_apart(tokens, heads, d, ts, hs):
+    """Rows that do not overlap, in whatever order they lie, pass the check: the call is refused
+    for what is checked behind it, before anything is launched."""
+    a = dict(tokens=tokens, heads=heads, head_dim=d, rot_dim=d, out_token_stride=ts, out_head_stride=hs)
+    assert B.lib().gq_rope(args(**a, positions=FAKE + 4), None) == B.GQ_ERR_MISALIGNED
+
+
 def test_binding_checks():
     x = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
     pos, f = torch.zeros(3, dtype=torch.int64), torch.zeros(32, dtype=torch.float64)

@@ -14,6 +14,23 @@ constexpr int64_t kMaxStride = (int64_t)1 << 40;
 
 bool bad_stride(int64_t s) { return s < -kMaxStride || s > kMaxStride; }
 
+// Whether rows of d elements, `tokens` x `heads` of them at these strides, overlap.  The stride of
+// a dimension of one element is never walked.
+bool rows_overlap(int64_t tokens, int64_t heads, int64_t token_stride, int64_t head_stride, int64_t d) {
+  const int64_t t = std::llabs(token_stride), h = std::llabs(head_stride);
+  if ((tokens > 1 && t < d) || (heads > 1 && h < d)) return true;
+  if (tokens < 2 || heads < 2) return false;
+  // one dimension inside a step of the other: nearly every layout
+  if ((heads - 1) * h + d <= t || (h - d) / t >= tokens - 1) return false;
+  // else rows i tokens and j heads apart (in either direction): for each j the nearest i
+  for (int64_t j = 1; j < heads; ++j) {
+    const int64_t x = j * h;
+    for (int64_t i = x / t; i <= x / t + 1; ++i)
+      if (i >= 1 && i < tokens && std::llabs(x - i * t) < d) return true;
+  }
+  return false;
+}
+
 gq_status check_scaling(const gq_rope_scaling& s) {
   if (s.kind < GQ_ROPE_NONE || s.kind > GQ_ROPE_YARN) return GQ_ERR_INVALID_ARG;
   if (s.kind == GQ_ROPE_NONE) return GQ_OK;
@@ -72,10 +89,7 @@ gq_status gq_rope(const gq_rope_args* args, void* stream) {
     return GQ_ERR_INVALID_ARG;
   if (a.tokens == 0 || a.heads == 0) return GQ_OK;
   if (!a.x || !a.out || !a.positions || !a.freqs) return GQ_ERR_INVALID_ARG;
-  // Rows of out apart from each other.  The stride of a dimension of one element is never walked.
-  if ((a.tokens > 1 && std::llabs(a.out_token_stride) < a.head_dim) ||
-      (a.heads > 1 && std::llabs(a.out_head_stride) < a.head_dim))
-    return GQ_ERR_INVALID_ARG;
+  if (rows_overlap(a.tokens, a.heads, a.out_token_stride, a.out_head_stride, a.head_dim)) return GQ_ERR_INVALID_ARG;
   if (a.x == a.out && ((a.tokens > 1 && a.x_token_stride != a.out_token_stride) ||
                        (a.heads > 1 && a.x_head_stride != a.out_head_stride)))
     return GQ_ERR_INVALID_ARG;
