@@ -109,7 +109,9 @@ gq_status gq_kv4_read(const uint8_t* cache, int64_t n_pages, gq_kv4_layout layou
  * the values not at all.  Weights below 2^-22 of a row's largest have fewer bits
  * (2^-25 for up to 32 rows, of weight times value scale), below 2^-33 (2^-36) none.
  * For more than 32 rows keys and values are also off by up to 2^-33 of the largest
- * element among the 16 tokens of a sub-block.  Scores have to lie in fp32's range. */
+ * element among the 16 tokens of a sub-block.  Scores have to lie within +-2^22: beyond,
+ * their own rounding moves weights by more than fp16 has room for, and results may be
+ * infinite or NaN. */
 typedef struct {
   const void* q;
   int64_t q_token_stride, q_head_stride;

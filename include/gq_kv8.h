@@ -133,9 +133,9 @@ gq_status gq_kv8_read(const uint8_t* cache, int64_t n_pages, gq_kv8_layout layou
  * (2^-11), those below 2^-22 of a row's largest have fewer bits, below 2^-33 none.  What that
  * leaves is carried along (2^-22 remains) for fp16 results of a sequence of at most 8 rows
  * (queries times query heads per key/value head) in a call whose max_q_len makes at most 16;
- * with a larger max_q_len it is not.  scale times the largest |q| of a row, and that times the
- * largest |k| that it sees, have to lie in fp32's range (scores of 0 are right beyond it
- * too); the first has fewer bits below 2^-120. */
+ * with a larger max_q_len it is not.  Scores have to lie within +-2^22: beyond, their own
+ * rounding moves weights by more than fp16 has room for, and results may be infinite or
+ * NaN.  scale times the largest |q| of a row has fewer bits below 2^-112. */
 typedef struct {
   const void* q;
   int64_t q_token_stride, q_head_stride;

@@ -73,3 +73,26 @@ def test_small_queries_and_large_keys(low, high, q_len, d):
         c = Case(4, 1, d, 16, "bf16", [q_len], [kv], k=k, v=v, q=q)
         c.check(scale=scale)
         c.check(scale=scale, window=20)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("q_len", [1, 10, 20])
+def test_scores_as_large_as_they_may_be(q_len, dtype):
+    """Scores up to 2^22, where their steps in fp32 are as large as 1/2: the heaviest key is found,
+    and what comes out is a mean of the values."""
+    kv, d = 700, 64
+    g = torch.Generator().manual_seed(5)
+    k, v = torch.randn(kv, 1, d, generator=g), torch.randn(kv, 1, d, generator=g)
+    q = torch.randn(q_len, 2, d, generator=g)
+    most = float((q[:, :, None] * k[None, :, 0][:, None]).sum(-1).abs().max())
+    for sign in (1, -1):
+        for drift in (0.0, 1.0):
+            # with drift: every key a little heavier than the one before
+            kk = k * (1 - drift) + drift * (1 + torch.arange(kv)[:, None, None] * 2.0 ** -9).expand(kv, 1, d) / 2.5
+            qq = q * (1 - drift) + drift
+            top = most if drift == 0 else float((qq[0, 0] * kk[:, 0]).sum(-1).abs().max())
+            scale = 0.98 * 2.0 ** 22 / top
+            c = Case(2, 1, d, 16, dtype, [q_len], [kv], k=kk, v=v, q=sign * qq)
+            for bound in BOUNDS:
+                out = c.check(scale=scale, **bound)
+                assert bool((out.abs() <= c.v.double().abs().max() * (1 + 2.0 ** -6)).all())
