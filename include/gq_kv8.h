@@ -180,8 +180,10 @@ gq_status gq_kv8_attention(const gq_kv8_attention_args* args, void* workspace,
  * 0 .. p / page_size of its row of page_table.  For query t and key/value head h the
  * score of a page is the largest, over the query heads of h, of
  *   sum_d max(q_d min_d, q_d max_d)
- * which no key of the page exceeds (as it was appended), summed in binary64; sums that
- * are NaN do not count.  Of n pages min(n, keep) are taken: the first `first` and the last
+ * which no key of the page exceeds (as it was appended), summed in binary64 and taken as
+ * q_d max_d where q_d is positive, q_d min_d where it is negative (which tells them apart
+ * for an infinite q_d beside a bound of 0: that product alone is NaN); sums that are NaN do not
+ * count.  Of n pages min(n, keep) are taken: the first `first` and the last
  * `last`, then those with the largest scores, of equal ones the earlier.  A page number
  * outside 0 .. n_pages - 1 has the lowest score, as has a page whose sums are all NaN.
  *   q       [q_tokens, q_heads, head_dim] of dtype, the bounds' own; strides as in

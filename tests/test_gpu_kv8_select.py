@@ -242,3 +242,26 @@ def compare(out, q, k, v, cuts, n, dt, sel=None, page=None):
         o, l, p = attention64(qh, a[0], a[1], n, keep.numel(), True, 0, d ** -0.5)
         tol, _ = U.attention_bounds(qh, *a, o, l, p, d ** -0.5, dt, False)
         assert bool(((out[:, h * r:(h + 1) * r].cpu().double() - o).abs() <= tol).all())
+
+
+def test_infinite_queries_beside_bounds_of_zero():
+    """The product with the bound that does not count is not formed: infinity times 0 makes NaN only
+    of pages where it does."""
+    h, d, page, n = 1, 64, 16, 60
+    table, n_pages = tables([n * page], page)
+    bounds = B.gq_kv8_bounds_empty(n_pages, h, d, torch.bfloat16, device=device())
+    lo = torch.zeros(n_pages, h, 2, d)
+    rows = table[0].long()
+    lo[rows[0::3], 0, 1] = 5.0                       # 0 .. 5
+    lo[rows[1::3], 0, 0] = -5.0                      # -5 .. 0
+    lo[rows[2::3], 0, 0], lo[rows[2::3], 0, 1] = -1.0, 2.0
+    bounds.copy_(lo)
+    first = lambda which, skip: [j for j in range(which, n, 3) if j not in skip]
+    for sign, best, nan in ((1.0, (0, 2), 1), (-1.0, (1, 2), 0)):
+        q = torch.zeros(1, 1, d).bfloat16()
+        q[0, 0, 7] = sign * float("inf")
+        for keep in (10, 45):
+            pages, lens = B.gq_kv8_select(q.to(device()), bounds, table.to(device()), I32([n * page]), keep, page)
+            order = sorted(first(best[0], (0, n - 1)) + first(best[1], (0, n - 1))) + first(nan, (0, n - 1))
+            want = sorted([0, n - 1] + order[:keep - 2])
+            assert pages[0, 0].tolist() == table[0, want].tolist() and int(lens[0]) == keep * page
