@@ -250,17 +250,12 @@ gq_status gq_kv8_attention(const gq_kv8_attention_args* args, void* workspace,
   hipStream_t s = (hipStream_t)stream;
   if (gq_status st = check_device(s)) return st;
   const Kv8Geo c = geometry(a.cache, a.n_pages, a.layout);
-  Kv8Attn k;
+  Kv8Attn k{};
   k.c.cache = c.cache;
   k.c.n_pages = c.n_pages;
   k.c.hkv = c.hkv;
   k.c.d = c.d;
-  k.c.g = c.d;
-  k.c.ng = 1;
-  k.c.sym = 1;
   k.c.page_shift = c.page_shift;
-  k.c.meta = 0;
-  k.c.sb = 32 * (uint32_t)c.d;
   k.scales = c.scales;
   k.q = (const uint16_t*)a.q;
   k.q_ts = a.q_token_stride;

@@ -49,7 +49,7 @@ struct Tile8 : Tile<D, 1, true, false, false> {
   static constexpr int kV = kTK * KP;                 // the values, behind the keys
   static constexpr int kEx = kV + D * VP;             // floats {log2 S_V, 2^40 / S_V, S_K} of the four blocks
   static constexpr int kBuf = kEx + 48;
-  static constexpr int kBufs = 2 * kBuf <= 160 * 1024 ? 2 : 1;
+  static_assert(2 * kBuf <= 160 * 1024, "two tiles in LDS");
 
   // What a wave holds of the next tile: the codes of 16 keys or 16 values.
   struct Codes {
@@ -324,7 +324,7 @@ template <int D>
 __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv8_tile_kernel(Kv8Attn a) {
   using T = Tile8<D>;
   constexpr bool kBoth = T::NW == 4;   // a wave expands keys and values of its block; else one of them
-  __shared__ __attribute__((aligned(16))) uint8_t smem[T::kBufs * T::kBuf];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * T::kBuf];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, kg = lane >> 4, n = lane & 31, hf = lane >> 5;
@@ -396,19 +396,18 @@ __global__ __launch_bounds__(tile_waves(D) * 64, tile_waves(D) / 4) void kv8_til
         auto refill = [&] {
           if (!more) return;
           const int after = page_of(u + 3 * kTK);   // on its way while the codes are expanded
-          expand(smem + (b ^ (T::kBufs - 1)) * T::kBuf);
+          expand(smem + (b ^ 1) * T::kBuf);
           fetch(next, u + 2 * kTK);
           next = after;
         };
         if (!kBoth && is_k) refill();
         if (row0 < s.n * a.r) st.attend(a, s, row0, u, smem + b * T::kBuf, n, hf);
-        if (T::kBufs == 1) __syncthreads();
         if (kBoth || !is_k) refill();
         __syncthreads();
       };
       for (int u = u0; u < stop; u += 2 * kTK) {
         step(u, std::integral_constant<int, 0>{});
-        if (u + kTK < stop) step(u + kTK, std::integral_constant<int, T::kBufs - 1>{});
+        if (u + kTK < stop) step(u + kTK, std::integral_constant<int, 1>{});
       }
       float* part = nullptr;
       if (!(starts && ends)) {
