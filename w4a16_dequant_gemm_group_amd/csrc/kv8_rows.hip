@@ -239,17 +239,23 @@ struct Rows8 : Rows<D, 1, NQ, true> {
         float M = kNegInf;
 #pragma unroll
         for (int w = 0; w < NW; ++w) M = fmaxf(M, sm[w * 16 + rr]);
-        float L = 0.0f, acc[C];
+        float L = 0.0f, low = -kNegInf, acc[C];   // low: the lowest reference that has a sum
 #pragma unroll
         for (int i = 0; i < C; ++i) acc[i] = 0.0f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-          const float mw = sm[w * 16 + rr];
+          const float mw = sm[w * 16 + rr], lw = sl[w * 16 + rr];
           const float f = mw == kNegInf ? 0.0f : exp2_hw(mw - M);
-          const Moved lm = move_sum(sl[w * 16 + rr], mw, M, f);
-          L = __builtin_fmaf(lm.f, lm.l, L);
+          low = lw == 0.0f ? low : fminf(low, mw);
+          L = __builtin_fmaf(f, lw, L);
 #pragma unroll
           for (int i = 0; i < C; ++i) acc[i] = __builtin_fmaf(f, so[(w * 16 + rr) * kRow + c0 + i], acc[i]);
+        }
+        if (low - M < -100.0f) {
+          // once more, apart: with move_sum in the loop above short contexts took 0.1 us more
+          L = 0.0f;
+#pragma unroll 1
+          for (int w = 0; w < NW; ++w) L += sum_at(sl[w * 16 + rr], sm[w * 16 + rr], M);
         }
         if (part) {
           float* po = part + (nq * 16 + rr) * D + c0;
