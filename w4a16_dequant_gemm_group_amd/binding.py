@@ -7,7 +7,8 @@ caller-supplied outputs alike, all before the first library call), allocate
 missing outputs and workspaces with torch (device memory plumbing), and pass
 raw pointers plus the current HIP stream to the library.  Every step of the
 computation runs in the library's kernels; there is no fallback path.  A
-missing ``libgq.so`` raises immediately.
+missing ``libgq.so`` raises immediately.  Autograd does not see these calls:
+what they return carries no graph, also where an input requires gradients.
 """
 from __future__ import annotations
 
@@ -944,7 +945,8 @@ def gq_rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, inter
     """x [tokens, heads, head_dim] (bf16, fp16 or fp32; a view with contiguous rows is taken
     as it is) turned by its positions (int64 [tokens]) with freqs (float64 [rot_dim / 2]): pairs
     (i, i + rot_dim / 2), interleaved (2 i, 2 i + 1).  inverse: by the negative angles, which
-    makes the gradient of x from that of the result.  out may be x."""
+    makes the gradient of x from that of the result (a call of the caller's own: autograd does
+    not make it).  out may be x; rows of out must not overlap."""
     xts, xhs = _heads3(x, "x", _DT)
     T, H, D = shape = x.shape
     _is(positions, "positions", torch.int64, (T,))

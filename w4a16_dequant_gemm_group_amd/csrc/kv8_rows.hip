@@ -8,7 +8,7 @@
 // lane, so keys cost one factor per block, and P' = p S_V, rounded to fp16 once, one
 // product per weight.
 // Bound by memory: 64 sequences of up to 8191 keys, 8 heads of 128 with 4 query heads each,
-// 88 us (531 MB at 6.0 TB/s); 131071 keys of one sequence 48 (5.6 TB/s); 201 keys 7.8, a chain
+// 88 us (531 MB at 6.0 TB/s); 131071 keys of one sequence 48 (5.6 TB/s); 201 keys 8.0, a chain
 // of loads.
 #include "kv8.h"
 #include "kv4_rows.h"

@@ -8,7 +8,7 @@
 // places in LDS, codes leave in pieces of 16 bytes that make one run.
 // 16 K tokens of 8 heads of 128: 32 us (98 MB read, the keys once more for their bounds, and
 // 34 MB written: 4.1 TB/s; bound by loads in flight), without bounds and with the inputs in
-// cache 23.5; read back in 18.4 (101 MB).  One token 4.6.
+// cache 24 to 25; read back in 18.4 (101 MB).  One token 4.6.
 #include "kv8.h"
 #include "kv8_seq.h"
 #include "stream_util.h"

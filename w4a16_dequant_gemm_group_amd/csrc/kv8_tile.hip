@@ -5,8 +5,9 @@
 // all 64 with its own rows.  Codes are exact as fp16 and a block's scales are the same for
 // 16 keys, so both products take one part each: the keys' scale is a factor of 16 scores
 // at once, the values' goes into the exponent of the weights.
-// Bound by vector work beside the products (57 and 44 % busy): a prompt of 4096 with 32 heads of
-// 128 on 8 150 us (916 TFLOP/s), 512 queries behind 32 K keys 284 to 294 (960 to 926).  A key tile
+// Bound by vector work beside the products (57 and 49 % busy): a prompt of 4096 with 32 heads of
+// 128 on 8 143 us among other calls (962 TFLOP/s) and 145 to 150 in bursts, 512 queries behind 32 K keys 284 to 295
+// (960 to 925).  A key tile
 // costs 1.7 / 1.95 / 2.25 us at 64 / 96 / 128 channels, a row tile taken up about five of them.
 #include "kv8.h"
 #include "kv4_tile.h"

@@ -8,8 +8,10 @@
 // An angle is p f in binary64, reduced to a turn there (off by 2^-52 of the angle: 2^-22 at
 // a position of 2^30); what fp32 cannot hold of the turn is put back as a small rotation, so
 // that cosine and sine are good to about an ulp of 1 besides.
-// Bound by memory: 8191 tokens of 40 heads of 128, 168 MB, in 29 us repeated and 33 among other
-// work (5.1 TB/s, a copy's rate); one token 2.6.
+// Bound by memory: 8191 tokens of 40 heads of 128, 168 MB, in 29 us where part of them is in the
+// caches and 33 over four inputs in turn (5.0 TB/s; a copy 5.1), 36 a call among other work; one token
+// 2.7.  Rows that are no whole pieces of 16 bytes go pair by pair: 40 heads of 80 (105 MB) of which 20 are
+// rotated 64 us, all 80 27.
 #include "rope.h"
 #include "stream_util.h"
 
