@@ -68,8 +68,11 @@ gq_status gq_kv8_cache_bytes(int64_t n_pages, gq_kv8_layout layout, size_t* byte
  *           0 .. tokens
  *   bounds  as above, 16-byte aligned, or NULL.  A page's bounds start over when its
  *           first position is written; else they are widened
- * Where a sequence is cut back and appended to again, the scale (and the bounds) of
- * the block (page) it is cut in stay as wide as they were.  Errors: INVALID_ARG
+ * Where a call begins inside a block, the tokens before it in the block are ones that were
+ * appended (their scale is read and kept at least, whatever the memory holds), and with
+ * bounds those of its page were, with bounds.  Where a sequence is cut back and appended to
+ * again, the scale (and the bounds) of the block (page) it is cut in stay as wide as they
+ * were.  Errors: INVALID_ARG
  * (layout, shapes, NULL), UNSUPPORTED (dtype, head_dim, device), MISALIGNED. */
 typedef struct {
   const void* k;
